@@ -20,7 +20,8 @@ import torch
 from . import _native
 from ._native import (LLAMA_BF16, LLAMA_F32, LLAMA_OK, LLAMA_ERR_INVALID_ARG, LLAMA_ERR_UNSUPPORTED_DIMS,
                       LLAMA_ERR_POS_RANGE, LLAMA_ERR_WORKSPACE, LLAMA_ERR_CUDA, LLAMA_ERR_DEVICE_TIMEOUT,
-                      llama_block_dims, llama_block_weights, llama_kv_cache, llama_rope_scaling)
+                      LLAMA_ERR_NO_PAGES, llama_block_dims, llama_block_weights, llama_kv_cache, llama_paged_cache,
+                      llama_rope_scaling)
 
 __all__ = [
     "LlamaBlock", "LlamaError", "KVCache", "lib", "llama_block_create", "llama_block_create_scaled",
@@ -30,6 +31,9 @@ __all__ = [
     "llama_block_poll_error", "llama_block_last_error", "llama_block_selftest_wait_timeout", "Trace", "llama_block_set_stage_events", "llama_block_launch_count", "HostMapped",
     "llama_embed", "llama_lmhead_workspace_bytes",
     "llama_lmhead_argmax", "llama_lmhead_argmax_noalloc", "llama_sample", "llama_rmsnorm", "LLAMA_BF16", "LLAMA_F32",
+    "PagedCache", "PagedCacheList", "llama_paged_plan", "llama_paged_release", "llama_paged_store",
+    "llama_paged_attention", "llama_paged_attention_workspace_bytes", "llama_block_decode_paged",
+    "llama_beam_select", "llama_beam_select_workspace_bytes", "llama_beam_reorder",
 ]
 
 
@@ -161,6 +165,11 @@ def llama_block_decode_seqpos(h, x, batch, kv: llama_kv_cache, pos_seq, y, ws, w
                                               ws_bytes, _stream(stream)), "llama_block_decode_seqpos")
 
 
+def llama_block_decode_paged(h, x, batch, kv: llama_paged_cache, table, pos_seq, y, ws, ws_bytes, stream=None) -> None:
+    _check(h, lib().llama_block_decode_paged(h, _ptr(x), batch, C.byref(kv), _ptr(table), table.shape[1], _ptr(pos_seq),
+                                             _ptr(y), _ptr(ws), ws_bytes, _stream(stream)), "llama_block_decode_paged")
+
+
 def llama_block_set_stage_events(h, events) -> None:
     """events: None, or a list of LLAMA_BLOCK_STAGES + 1 torch.cuda.Event (enable_timing=True)."""
     if events is None:
@@ -264,6 +273,189 @@ def llama_sample(logits, batch, vocab, temperature, top_k, top_p, uniforms, ids,
         raise LlamaError(rc, "llama_sample")
 
 
+# ----------------------------------------------------------------------------- paged cache and beam search
+
+def _arg(t, name: str, dtype: torch.dtype, least: int, device=None):
+    """The address of a contiguous CUDA tensor of `dtype` with at least `least` elements
+    on `device` (default: the current one)."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if not t.is_cuda or t.get_device() != (torch.cuda.current_device() if device is None else device):
+        raise ValueError(f"{name} must live on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.numel() < least:
+        raise ValueError(f"{name}: {least} elements needed, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _err_arg(err_dev, device):
+    return None if err_dev is None else _arg(err_dev, "err_dev", torch.int32, 1, device)
+
+
+class PagedCache:
+    """One layer's paged K and V: [n_pages, n_kv_heads, page_size, head_dim] each
+    (caller-owned torch tensors)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        if k.shape != v.shape or k.dim() != 4 or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must be alike: [n_pages, n_kv_heads, page_size, head_dim]")
+        self.k, self.v = k, v
+        self.dtype = k.dtype
+        self.device = k.get_device() if k.is_cuda else -1
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k.shape
+        self.code = _dtype_code(k.dtype)
+        self.c = llama_paged_cache(_ptr(k), _ptr(v), self.n_pages, self.page_size)
+        self.ref = C.byref(self.c)
+
+
+class PagedCacheList:
+    """The caches of a stack's layers, addressed by one block table."""
+
+    def __init__(self, caches):
+        caches = list(caches)
+        if not caches:
+            raise ValueError("at least one layer")
+        first = caches[0]
+        if any(c.k.shape != first.k.shape or c.dtype != first.dtype or c.device != first.device for c in caches):
+            raise ValueError("the layers' caches must be alike")
+        if len({c.c.k for c in caches} | {c.c.v for c in caches}) != 2 * len(caches):
+            raise ValueError("the layers' buffers must be distinct")
+        self.caches, self.first = caches, first
+        self.c = (llama_paged_cache * len(caches))(*[c.c for c in caches])
+
+    def __len__(self):
+        return len(self.caches)
+
+    def __getitem__(self, i):
+        return self.caches[i]
+
+
+def _table_arg(table, name, rows, device):
+    if table.dim() != 2 or table.shape[0] < rows:
+        raise ValueError(f"{name} must be [{rows} rows or more, pages per row]")
+    return _arg(table, name, torch.int32, 0, device)
+
+
+def llama_paged_plan(start, count, page_size: int, n_pages: int, free_pages, pool, table, slots, pool_out=None,
+                     err_dev=None, stream=None) -> None:
+    """Block tables and slot maps: request b, holding start[b] positions, receives count[b] more; the pages
+    they need come from the stack free_pages[: pool[0]].  slots [batch, tokens], table [batch, pages per row];
+    pool_out defaults to pool (in place)."""
+    dev = torch.cuda.current_device()
+    batch = start.numel()
+    if slots.dim() != 2 or slots.shape[0] != batch or count.numel() != batch:
+        raise ValueError("start, count [batch] and slots [batch, tokens] must agree")
+    out = pool if pool_out is None else pool_out
+    rc = lib().llama_paged_plan(_arg(start, "start", torch.int32, batch, dev), _arg(count, "count", torch.int32, batch, dev),
+                                batch, slots.shape[1], page_size, n_pages,
+                                _arg(free_pages, "free_pages", torch.int32, n_pages, dev),
+                                _arg(pool, "pool", torch.int32, 2, dev), _arg(out, "pool_out", torch.int32, 2, dev),
+                                _table_arg(table, "table", batch, dev), table.shape[1],
+                                _arg(slots, "slots", torch.int32, 0, dev), _err_arg(err_dev, dev), _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_paged_plan")
+
+
+def llama_paged_release(start, count, page_size: int, n_pages: int, free_pages, pool, table, pool_out=None,
+                        err_dev=None, stream=None) -> None:
+    """The pages that a plan with the same start and count took go back on the stack."""
+    dev = torch.cuda.current_device()
+    batch = start.numel()
+    if count.numel() != batch:
+        raise ValueError("start and count [batch] must agree")
+    out = pool if pool_out is None else pool_out
+    rc = lib().llama_paged_release(_arg(start, "start", torch.int32, batch, dev),
+                                   _arg(count, "count", torch.int32, batch, dev), batch, page_size, n_pages,
+                                   _arg(free_pages, "free_pages", torch.int32, n_pages, dev),
+                                   _arg(pool, "pool", torch.int32, 2, dev), _arg(out, "pool_out", torch.int32, 2, dev),
+                                   _table_arg(table, "table", batch, dev), table.shape[1], _err_arg(err_dev, dev),
+                                   _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_paged_release")
+
+
+def llama_paged_store(k, v, slots, kv: PagedCache, src_pos: int = 0, err_dev=None, stream=None) -> None:
+    """Rows src_pos + t of the contiguous k, v [batch, n_kv_heads, src_seq, head_dim] to the pages of kv, at
+    slots [batch, tokens] (negative: skipped)."""
+    dev = kv.device
+    if k.dim() != 4 or k.shape != v.shape or k.shape[1] != kv.n_kv_heads or k.shape[3] != kv.head_dim:
+        raise ValueError("k, v must be [batch, n_kv_heads, src_seq, head_dim] of the cache's heads")
+    if slots.dim() != 2 or slots.shape[0] > k.shape[0]:
+        raise ValueError("slots must be [batch, tokens]")
+    _current(dev)
+    rc = lib().llama_paged_store(_arg(k, "k", kv.dtype, 0, dev), _arg(v, "v", kv.dtype, 0, dev), slots.shape[0],
+                                 slots.shape[1], k.shape[2], src_pos, _arg(slots, "slots", torch.int32, 0, dev),
+                                 kv.n_kv_heads, kv.head_dim, kv.code, kv.ref, _err_arg(err_dev, dev), _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_paged_store")
+
+
+def _current(device: int) -> None:
+    if device != torch.cuda.current_device():
+        raise ValueError("the cache's device is not the current device")
+
+
+def llama_paged_attention_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_len) -> int:
+    return int(lib().llama_paged_attention_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_len))
+
+
+def llama_paged_attention(q, kv: PagedCache, table, lens, max_len: int, o, ws, err_dev=None, stream=None) -> None:
+    """o[b] = attention of q[b] [n_heads, head_dim] over the first lens[b] positions of sequence b (0: zeros)."""
+    dev = kv.device
+    if q.dim() != 3 or q.shape[2] != kv.head_dim or o.shape != q.shape:
+        raise ValueError("q and o must be [batch, n_heads, head_dim] of the cache's heads")
+    batch, n_heads = q.shape[0], q.shape[1]
+    _current(dev)
+    rc = lib().llama_paged_attention(_arg(q, "q", kv.dtype, 0, dev), batch, n_heads, kv.n_kv_heads, kv.head_dim, kv.code,
+                                     kv.ref, _table_arg(table, "table", batch, dev), table.shape[1],
+                                     _arg(lens, "lens", torch.int32, batch, dev), max_len, _arg(o, "o", kv.dtype, 0, dev),
+                                     _arg(ws, "ws", torch.uint8, 0, dev), ws.numel(), _err_arg(err_dev, dev),
+                                     _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_paged_attention")
+
+
+def llama_beam_select_workspace_bytes(groups, beams, vocab, n_out) -> int:
+    return int(lib().llama_beam_select_workspace_bytes(groups, beams, vocab, n_out))
+
+
+def llama_beam_select(logits, scores, beams: int, n_out: int, parents, tokens, out_scores, ws, last=None, eos: int = -1,
+                      stream=None) -> None:
+    """The n_out best continuations of each group of `beams` rows of logits [groups * beams, vocab] (fp32), given
+    the rows' cumulative scores; rows whose last token is eos have ended.  Outputs [groups, n_out]."""
+    dev = torch.cuda.current_device()
+    if logits.dim() != 2 or beams < 1 or logits.shape[0] % beams:
+        raise ValueError("logits must be [groups * beams, vocab]")
+    rows, vocab = logits.shape
+    groups = rows // beams
+    n = groups * n_out
+    rc = lib().llama_beam_select(_arg(logits, "logits", torch.float32, 0, dev), groups, beams, vocab,
+                                 _arg(scores, "scores", torch.float32, rows, dev),
+                                 None if last is None else _arg(last, "last", torch.int32, rows, dev), eos, n_out,
+                                 _arg(parents, "parents", torch.int32, n, dev), _arg(tokens, "tokens", torch.int32, n, dev),
+                                 _arg(out_scores, "out_scores", torch.float32, n, dev),
+                                 _arg(ws, "ws", torch.uint8, 0, dev), ws.numel(), _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_beam_select")
+
+
+def llama_beam_reorder(parents, beams: int, lens, table, caches: PagedCacheList, err_dev=None, stream=None) -> None:
+    """Rows of table, and the unfilled last pages of every layer's cache, follow parents [groups * beams] in place."""
+    f = caches.first
+    dev = f.device
+    rows = parents.numel()
+    if beams < 1 or rows % beams:
+        raise ValueError("parents must be [groups * beams]")
+    _current(dev)
+    rc = lib().llama_beam_reorder(_arg(parents, "parents", torch.int32, 0, dev), rows // beams, beams,
+                                  _arg(lens, "lens", torch.int32, rows, dev), _table_arg(table, "table", rows, dev),
+                                  table.shape[1], caches.c, len(caches), f.n_kv_heads, f.head_dim, f.code,
+                                  _err_arg(err_dev, dev), _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_beam_reorder")
+
+
 # ----------------------------------------------------------------------------- convenience
 
 class KVCache:
@@ -337,6 +529,16 @@ class LlamaBlock:
     def decode_seqpos(self, x, kv: KVCache, pos_seq, y, ws, stream=None):
         """pos_seq: int32 CUDA tensor [batch], sequence b at position pos_seq[b]."""
         llama_block_decode_seqpos(self.h, x, x.shape[0], kv.c, pos_seq, y, ws, ws.numel(), stream)
+
+    def decode_paged(self, x, kv: "PagedCache", table, pos_seq, y, ws, stream=None):
+        """One step on a paged cache: sequence b at position pos_seq[b], its pages in row b of table
+        [batch, pages per row] (int32 CUDA tensors)."""
+        if kv.n_kv_heads != self.dims.n_kv_heads or kv.head_dim != self.dims.head_dim or \
+                kv.dtype != self._keep["wq"].dtype:
+            raise ValueError("the paged cache's heads or type are not the block's")
+        _table_arg(table, "table", x.shape[0], None)
+        _arg(pos_seq, "pos_seq", torch.int32, x.shape[0])
+        llama_block_decode_paged(self.h, x, x.shape[0], kv.c, table, pos_seq, y, ws, ws.numel(), stream)
 
     def poll_error(self, stream=None) -> int:
         return llama_block_poll_error(self.h, stream)

@@ -14,6 +14,7 @@ LLAMA_ERR_POS_RANGE = -3
 LLAMA_ERR_WORKSPACE = -4
 LLAMA_ERR_CUDA = -5
 LLAMA_ERR_DEVICE_TIMEOUT = -6
+LLAMA_ERR_NO_PAGES = -7
 LLAMA_F32 = 0
 LLAMA_BF16 = 1
 LLAMA_BLOCK_INTERMEDIATES = 6
@@ -25,6 +26,7 @@ ERROR_NAMES = {
     LLAMA_ERR_WORKSPACE: "LLAMA_ERR_WORKSPACE",
     LLAMA_ERR_CUDA: "LLAMA_ERR_CUDA",
     LLAMA_ERR_DEVICE_TIMEOUT: "LLAMA_ERR_DEVICE_TIMEOUT",
+    LLAMA_ERR_NO_PAGES: "LLAMA_ERR_NO_PAGES",
 }
 
 
@@ -45,6 +47,10 @@ class llama_rope_scaling(C.Structure):
 
 class llama_kv_cache(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("batch", C.c_int32), ("max_seq", C.c_int32)]
+
+
+class llama_paged_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("n_pages", C.c_int32), ("page_size", C.c_int32)]
 
 
 # name -> (restype, argtypes); the exact set of symbols include/llama_block.h declares
@@ -84,6 +90,24 @@ SIGNATURES = {
                                               C.c_int, C.c_float, C.c_void_p, C.c_void_p, C.c_void_p]),
     "llama_sample": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_float, C.c_int, C.c_float, C.c_void_p,
                                C.c_void_p, C.c_void_p]),
+    "llama_paged_plan": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                   C.c_void_p, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "llama_paged_release": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p,
+                                      C.c_void_p, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p]),
+    "llama_paged_store": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int,
+                                    C.c_int, C.c_int, C.POINTER(llama_paged_cache), C.c_void_p, C.c_void_p]),
+    "llama_paged_attention_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int]),
+    "llama_paged_attention": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
+                                        C.POINTER(llama_paged_cache), C.c_void_p, C.c_int, C.c_void_p, C.c_int,
+                                        C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+    "llama_block_decode_paged": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.POINTER(llama_paged_cache), C.c_void_p,
+                                           C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "llama_beam_select_workspace_bytes": (C.c_size_t, [C.c_int, C.c_int, C.c_int, C.c_int]),
+    "llama_beam_select": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_int,
+                                    C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p]),
+    "llama_beam_reorder": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_int,
+                                     C.POINTER(llama_paged_cache), C.c_int, C.c_int, C.c_int, C.c_int, C.c_void_p,
+                                     C.c_void_p]),
     "llama_rmsnorm": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_float, C.c_int,
                                 C.c_void_p]),
 }

@@ -161,7 +161,7 @@ int check_kv(llama_block b, const llama_kv_cache* kv, int batch, int last_pos) {
 // (T = 1 at `pos`, or at *pos_dev).
 int run_block(llama_block b, const void* x, int B, int T, const llama_kv_cache* kv, int start_pos,
               const int32_t* pos_dev, void* y, void* ws, size_t ws_bytes, void* stream_v, bool decode,
-              const int32_t* pos_seq = nullptr) {
+              const int32_t* pos_seq = nullptr, const PageTable* pages = nullptr) {
     const auto& d = b->dims;
     cudaStream_t s = (cudaStream_t)stream_v;
     const int M = B * T;
@@ -174,7 +174,9 @@ int run_block(llama_block b, const void* x, int B, int T, const llama_kv_cache* 
     if (cudaGetDevice(&cur) != cudaSuccess) return fail(b, LLAMA_ERR_CUDA, "cudaGetDevice failed");
     if (cur != b->device) return fail(b, LLAMA_ERR_INVALID_ARG, "the handle's device is not the current device");
     w = layout(b, B, T, (uint8_t*)ws, decode);
-    const int max_pos = std::min(d.max_seq, kv->max_seq);
+    // on pages (kv: n_pages "sequences" of page_size rows) a table row bounds the positions
+    const int max_pos =
+        pages ? (int)std::min<long long>(d.max_seq, (long long)pages->stride << pages->shift) : std::min(d.max_seq, kv->max_seq);
     cudaError_t e;
     // kernels enqueued by this call (each launcher below issues one; decode attention two)
     int n_launch = 0;
@@ -210,6 +212,7 @@ int run_block(llama_block b, const void* x, int B, int T, const llama_kv_cache* 
     at.start_pos = start_pos;
     at.pos_dev = pos_dev;
     at.pos_seq = pos_seq;
+    if (pages) at.pages = *pages;
     at.max_pos = max_pos;
     at.dtype = d.dtype;
     at.partial = w.attn_partial;
@@ -246,6 +249,7 @@ int run_block(llama_block b, const void* x, int B, int T, const llama_kv_cache* 
         eq.start_pos = start_pos;
         eq.pos_dev = pos_dev;
         eq.pos_seq = pos_seq;
+        if (pages) eq.pages = *pages;
         eq.max_pos = max_pos;
         eq.cos_tab = b->cos_tab;
         eq.sin_tab = b->sin_tab;
@@ -263,7 +267,10 @@ int run_block(llama_block b, const void* x, int B, int T, const llama_kv_cache* 
         if (gemm_needs_reduce(pq, PATH_AUTO)) LLAMA_TRY(reduce(pq, eq, EPI_QKV), "qkv_reduce");
         // 3. attention (tensor cores when the group size divides 128; one choice per handle)
         mark();
-        if (attention_tc_supported(d.n_heads, d.n_kv_heads, d.head_dim)) {
+        if (pages) {
+            LLAMA_TRY(launch_attention_paged(at, s), "attention_paged");
+            ++n_launch;   // and its combine
+        } else if (attention_tc_supported(d.n_heads, d.n_kv_heads, d.head_dim)) {
             if (decode) {
                 LLAMA_TRY(launch_attention_tc_decode(at, 0, s), "attention_decode");
                 ++n_launch;   // and its combine
@@ -584,6 +591,30 @@ extern "C" int llama_block_decode_seqpos(llama_block b, const void* x, int batch
     int rc = check_kv(b, kv, batch, 0);
     if (rc != LLAMA_OK) return rc;
     return run_block(b, x, batch, 1, kv, 0, nullptr, y, ws, ws_bytes, stream, true, pos_seq);
+}
+
+extern "C" int llama_block_decode_paged(llama_block b, const void* x, int batch, const llama_paged_cache* kv,
+                                        const int32_t* table, int table_stride, const int32_t* pos_seq, void* y,
+                                        void* ws, size_t ws_bytes, void* stream) {
+    if (!b) return LLAMA_ERR_INVALID_ARG;
+    if (batch < 0) return fail(b, LLAMA_ERR_INVALID_ARG, "negative batch");
+    const auto& d = b->dims;
+    // as llama_block_decode_seqpos
+    if (d.dtype != LLAMA_BF16 || !attention_tc_supported(d.n_heads, d.n_kv_heads, d.head_dim) ||
+        d.n_heads / d.n_kv_heads > 8 || batch > 32)
+        return fail(b, LLAMA_ERR_UNSUPPORTED_DIMS, "per-sequence positions need the bf16 weight-streaming decode path");
+    const int rc = paged_cache_check(kv, d.n_kv_heads, d.head_dim, d.dtype);
+    if (rc != LLAMA_OK) return fail(b, rc, "paged cache: null, misaligned or of an unsupported geometry");
+    if (batch == 0) return LLAMA_OK;
+    if (!x || !y || !table || !pos_seq || table_stride <= 0 || !aligned16(x) || !aligned16(y))
+        return fail(b, LLAMA_ERR_INVALID_ARG, "x / y / table / pos_seq null or x / y not 16-byte aligned");
+    const llama_kv_cache flat{kv->k, kv->v, kv->n_pages, kv->page_size};
+    PageTable pages;
+    pages.table = table;
+    pages.stride = table_stride;
+    pages.n_pages = kv->n_pages;
+    pages.shift = page_shift(kv->page_size);
+    return run_block(b, x, batch, 1, &flat, 0, nullptr, y, ws, ws_bytes, stream, true, pos_seq, &pages);
 }
 
 extern "C" int llama_block_poll_error(llama_block b, void* stream) {

@@ -19,6 +19,7 @@
 
 #include "attn_fold.cuh"
 #include "internal.h"
+#include "paged.cuh"
 
 namespace llama {
 
@@ -287,6 +288,95 @@ __global__ void __launch_bounds__(32) k_attn_decode_combine(const AttnK a) {
     TRACE(trace_cta(TR_ATTN_COMBINE, tr0, tr1);)
 }
 
+// ----------------------------------------------------------------------------- decode on a paged cache
+// The same chunk partial over keys whose rows are found through the block table: a
+// chunk of 128 keys lies in 128 / page_size pages (one, from 128-key pages on).  Pages
+// behind a sequence's last key are not looked up.  One CTA per (chunk, KV head,
+// sequence); for the shapes the tensor-core kernel does not take (fp32, groups that do
+// not divide 128, more than 8 query heads per KV head).
+struct PagedK {
+    AttnK a;
+    PageTable t;
+    int pos_off;   // see paged_keys
+};
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(kThreads) k_attn_paged_chunks(const PagedK p) {
+    using TL = Tile<T, DH>;
+    constexpr int DPL = TL::DPL;
+    constexpr int VPR = DH / TL::VEC;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ int s_page[kAttnChunk / 16];
+    T* Ks = reinterpret_cast<T*>(smem_raw);
+    T* Vs = Ks + kAttnChunk * TL::LD;
+    float* qs = reinterpret_cast<float*>(Vs + kAttnChunk * TL::LD);
+    const AttnK& a = p.a;
+
+    ptx_wait();
+    const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+    const int n_rep = a.n_heads / a.n_kv_heads;
+    bool bad;
+    const int keys = paged_keys(a.pos_seq[b], p.pos_off, a.max_pos, bad);
+    if (bad && threadIdx.x == 0 && c == 0 && g == 0) record_error(a.err, LLAMA_ERR_POS_RANGE);
+    const int key0 = c * kAttnChunk;
+    if (key0 >= keys) return;
+    const int last = keys - 1;
+    const int shift = p.t.shift, ps = 1 << shift;
+    const int n_pages = (min(kAttnChunk, keys - key0) + ps - 1) >> shift;
+    if (threadIdx.x < n_pages) s_page[threadIdx.x] = page_of(p.t, b, (key0 >> shift) + threadIdx.x, a.err);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const T* q = reinterpret_cast<const T*>(a.q);
+    const size_t qld = (size_t)a.n_heads * DH;
+    for (int i = threadIdx.x; i < n_rep * DH; i += kThreads) {
+        const int r = i / DH, d = i % DH;
+        qs[i] = to_f(q[(size_t)b * qld + (size_t)(g * n_rep + r) * DH + d]);
+    }
+    __syncthreads();
+    const T* kc = reinterpret_cast<const T*>(a.kc);
+    const T* vc = reinterpret_cast<const T*>(a.vc);
+    for (int v = threadIdx.x; v < kAttnChunk * VPR; v += kThreads) {
+        const int j = v / VPR, col = (v % VPR) * TL::VEC;
+        const int key = key0 + j;
+        const int page = key <= last ? s_page[(key >> shift) - (key0 >> shift)] : -1;
+        const size_t row = page < 0 ? 0 : (((size_t)page * a.n_kv_heads + g) << shift) + (key & (ps - 1));
+        cp_async16(Ks + j * TL::LD + col, kc + row * DH + col, page >= 0);
+        cp_async16(Vs + j * TL::LD + col, vc + row * DH + col, page >= 0);
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    const int jmax = min(kAttnChunk - 1, last - key0);
+    for (int r = warp; r < n_rep; r += kWarps) {
+        float m, l, o[DPL];
+        chunk_partial<T, DH>(qs + r * DH, Ks, Vs, jmax, a.scale_log2, m, l, o);
+        float* dst = a.partial + ((((size_t)b * a.n_kv_heads + g) * a.n_chunks + c) * n_rep + r) * part_stride(DH);
+#pragma unroll
+        for (int e = 0; e < DPL; ++e) dst[lane * DPL + e] = o[e];
+        if (lane == 0) {
+            dst[DH] = m;
+            dst[DH + 1] = l;
+        }
+    }
+}
+
+template <typename T, int DH>
+__global__ void __launch_bounds__(32) k_attn_paged_combine(const PagedK p) {
+    const AttnK& a = p.a;
+    const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x;
+    ptx_wait();
+    bool bad;
+    const int keys = paged_keys(a.pos_seq[b], p.pos_off, a.max_pos, bad);
+    const int n_rep = a.n_heads / a.n_kv_heads;
+    const int g = h / n_rep, r = h % n_rep;
+    T* dst = reinterpret_cast<T*>(a.o) + (size_t)b * a.n_heads * DH + (size_t)h * DH;
+    if (keys == 0) {   // no key to attend: a row of zeros
+#pragma unroll
+        for (int e = 0; e < DH / 32; ++e) from_f(dst + lane * (DH / 32) + e, 0.f);
+        return;
+    }
+    const float* base = a.partial + (((size_t)b * a.n_kv_heads + g) * a.n_chunks * n_rep + r) * part_stride(DH);
+    fold_row<T, DH>(base, (size_t)n_rep * part_stride(DH), (keys - 1) / kAttnChunk + 1, lane, dst);
+}
+
 template <typename T, int DH>
 size_t smem_bytes(int rows) {
     return 2 * (size_t)kAttnChunk * Tile<T, DH>::LD * sizeof(T) + (size_t)rows * DH * sizeof(float);
@@ -355,9 +445,59 @@ cudaError_t combine_impl(const AttnArgs& a, cudaStream_t s) {
     return combine_launch<T, DH>(make_k(a), s);
 }
 
+PagedK make_paged(const AttnArgs& a) {
+    PagedK p{};
+    p.a = make_k(a);
+    p.t = a.pages;
+    p.pos_off = a.pos_off;
+    return p;
+}
+
+template <typename T, int DH>
+cudaError_t paged_combine_impl(const AttnArgs& a, cudaStream_t s) {
+    auto kern = k_attn_paged_combine<T, DH>;
+    cudaError_t r = kernel_setup_once((const void*)kern, setup_prefer_shared);
+    if (r != cudaSuccess) return r;
+    return launch_pdl(kern, dim3(a.n_heads, a.batch), dim3(32), 0, s, make_paged(a));
+}
+
+template <typename T, int DH>
+cudaError_t paged_decode_impl(const AttnArgs& a, cudaStream_t s) {
+    auto kern = k_attn_paged_chunks<T, DH>;
+    cudaError_t r = kernel_setup_once((const void*)kern, [](const void* k) {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<T, DH>(kRowsMax));
+    });
+    if (r != cudaSuccess) return r;
+    r = launch_pdl(kern, dim3(a.n_chunks, a.n_kv_heads, a.batch), dim3(kThreads),
+                   smem_bytes<T, DH>(a.n_heads / a.n_kv_heads), s, make_paged(a));
+    if (r != cudaSuccess) return r;
+    return paged_combine_impl<T, DH>(a, s);
+}
+
 }  // namespace
 
 LLAMA_TRACE_UNIT(attn_simt)
+
+cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s) {
+    if (a.dtype == LLAMA_BF16) return a.head_dim == 128 ? paged_combine_impl<bf16, 128>(a, s) : cudaErrorInvalidValue;
+    switch (a.head_dim) {
+        case 32: return paged_combine_impl<float, 32>(a, s);
+        case 64: return paged_combine_impl<float, 64>(a, s);
+        case 128: return paged_combine_impl<float, 128>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s) {
+    if (a.batch <= 0) return cudaSuccess;
+    if (a.dtype == LLAMA_BF16) return a.head_dim == 128 ? paged_decode_impl<bf16, 128>(a, s) : cudaErrorInvalidValue;
+    switch (a.head_dim) {
+        case 32: return paged_decode_impl<float, 32>(a, s);
+        case 64: return paged_decode_impl<float, 64>(a, s);
+        case 128: return paged_decode_impl<float, 128>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
 
 size_t attn_decode_partial_bytes(int batch, int n_kv_heads, int n_chunks, int n_rep, int head_dim) {
     return (size_t)batch * n_kv_heads * n_chunks * n_rep * part_stride(head_dim) * sizeof(float);

@@ -193,8 +193,10 @@ __device__ __forceinline__ void epi_store_cols(const GemmKArgs& a, int tile, int
                         record_error(e.err, LLAMA_ERR_POS_RANGE);
                     } else {
                         const bf16 r = __float2bfloat16_rn(v);
+                        int cb = b, row_in = pos;
                         if (kind == 0) qp[(size_t)(c0 + j) * q_stride] = r;
-                        else cp[(size_t)b * seq_stride + (size_t)pos * 128] = r;
+                        else if (!e.pages.table || paged_row(e, cb, row_in))
+                            cp[(size_t)cb * seq_stride + (size_t)row_in * 128] = r;
                     }
                 }
                 if (++t == T) { t = 0; ++b; }

@@ -3,6 +3,7 @@
 #include <string>
 
 #include "common.cuh"
+#include "paged.cuh"
 
 namespace llama {
 
@@ -28,12 +29,21 @@ struct GemmEpi {
     int start_pos = 0;                              // position of token t = base + t
     const int* pos_dev = nullptr;                   // if set, base = *pos_dev
     const int* pos_seq = nullptr;                   // decode (T = 1): token n at position pos_seq[n]
+    PageTable pages;                                // if .table is set (with pos_seq): kc, vc are pages
     int max_pos = 0;                                // positions must be < max_pos
     const float* cos_tab = nullptr;                 // [max_pos, 64]
     const float* sin_tab = nullptr;
     bool rope_later = false;                        // QKV: store q, k unrotated (launch_rope_inplace follows)
     int* err = nullptr;
 };
+
+// The (page, row) in which sequence b keeps position pos, in place of (b, pos); false
+// (recorded) if its table has no such page.
+__device__ __forceinline__ bool paged_row(const GemmEpi& e, int& b, int& pos) {
+    b = page_of(e.pages, b, pos >> e.pages.shift, e.err);
+    pos &= (1 << e.pages.shift) - 1;
+    return b >= 0;
+}
 
 // One projection: Y[M, F] = X[M, K] . W^T with W given as up to three row
 // blocks (wq / wk / wv) or as the gate/up pair (dual).
@@ -113,6 +123,8 @@ struct AttnArgs {
     int start_pos = 0;
     const int* pos_dev = nullptr;
     const int* pos_seq = nullptr;       // decode: sequence b at position pos_seq[b] (device)
+    PageTable pages;                    // decode: if .table is set (with pos_seq), kc and vc are pages
+    int pos_off = 0;                    // paged: 0, or -1 when pos_seq holds numbers of keys (paged_keys)
     int max_pos = 0;
     int dtype = LLAMA_BF16;
     float* partial = nullptr;           // decode: [B, Hkv, n_chunks, n_rep, head_dim + 4]
@@ -124,6 +136,12 @@ cudaError_t launch_attention_prefill(const AttnArgs& a, cudaStream_t s);   // CU
 cudaError_t launch_attention_decode(const AttnArgs& a, cudaStream_t s);    // CUDA cores, + combine
 // Ascending fold of the decode chunk partials into o (shared by both decode kernels).
 cudaError_t launch_attention_combine(const AttnArgs& a, cudaStream_t s);
+// Decode attention over a paged cache (pos_seq and pages set): CUDA cores, + combine.
+// A sequence without keys, or with a position out of range (recorded), gets a row of zeros.
+cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s);
+// LLAMA_OK, or why the pages of kv cannot be used with these heads.
+int paged_cache_check(const llama_paged_cache* kv, int n_kv_heads, int head_dim, int dtype);
 // Tensor-core attention (bf16, head_dim 128, n_heads / n_kv_heads dividing 128).
 bool attention_tc_supported(int n_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_attention_tc_prefill(const AttnArgs& a, cudaStream_t s);

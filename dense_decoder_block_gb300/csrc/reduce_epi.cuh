@@ -93,8 +93,16 @@ __device__ __forceinline__ Qkv4 epi4_qkv_prepare(const GemmEpi& e, int n, int f0
         p.c1 = __ldg(e.cos_tab + (size_t)pos * kRopeMaxPairs + i0 + 1);
         p.s1 = __ldg(e.sin_tab + (size_t)pos * kRopeMaxPairs + i0 + 1);
     }
-    if (kind == 0) p.dst = e.out + (size_t)n * (e.n_heads * 128) + head * 128 + row0;
-    else p.dst = ((kind == 1) ? e.kc : e.vc) + (((size_t)b * e.n_kv_heads + head) * e.kv_seq + pos) * 128 + row0;
+    if (kind == 0) {
+        p.dst = e.out + (size_t)n * (e.n_heads * 128) + head * 128 + row0;
+    } else {
+        int cb = b, cp = pos;
+        if (e.pages.table && !paged_row(e, cb, cp)) {
+            p.dst = nullptr;
+            return p;
+        }
+        p.dst = ((kind == 1) ? e.kc : e.vc) + (((size_t)cb * e.n_kv_heads + head) * e.kv_seq + cp) * 128 + row0;
+    }
     return p;
 }
 

@@ -49,6 +49,7 @@ extern "C" {
 #define LLAMA_ERR_WORKSPACE (-4)        /* workspace missing or too small */
 #define LLAMA_ERR_CUDA (-5)             /* a CUDA runtime call failed */
 #define LLAMA_ERR_DEVICE_TIMEOUT (-6)   /* a bounded device-side wait expired */
+#define LLAMA_ERR_NO_PAGES (-7)         /* the page pool holds too few (or no room for the) pages */
 
 typedef enum { LLAMA_F32 = 0, LLAMA_BF16 = 1 } llama_dtype;
 
@@ -331,6 +332,129 @@ int llama_lmhead_argmax_noalloc(const void* h, int batch, int h_stride, const vo
  * LLAMA_ERR_INVALID_ARG.  No workspace, nothing allocated. */
 int llama_sample(const float* logits, int batch, int vocab, float temperature, int top_k, float top_p,
                  const float* uniforms, int32_t* ids, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged KV cache: serving ragged requests from one pool of pages.  The pages give
+ * the cache's contents ("Llama 3 8B · Prepare Q, K, V", Explanation: K and V per
+ * position at KV-head size) and no layout; paging is a deployment variant.
+ *
+ * Shared by the calls below: positions, lengths, tables, slots and counts are
+ * int32 device arrays.  err_dev (device int32, may be NULL) receives the first
+ * error that a kernel finds; the caller clears it.  All tensors live on the
+ * current device.  Calls that read or write the same cache, table or pool must be
+ * ordered by the caller (one stream, or events).
+ * ------------------------------------------------------------------------- */
+
+/* One layer's cache: k, v [n_pages, n_kv_heads, page_size, head_dim], page_size a
+ * power of two in 16 .. 1024, n_pages * page_size * n_kv_heads < 2^31.  Position p
+ * of a sequence lies in row p % page_size of page table[p / page_size] of its block
+ * table row.  bf16 caches have head_dim 128, fp32 caches 32, 64 or 128. */
+typedef struct {
+    void *k, *v;
+    int32_t n_pages, page_size;
+} llama_paged_cache;
+
+/* Block tables and slot maps of a batch of requests.  Request b holds positions
+ * 0 .. start[b] - 1 and receives count[b] new ones (0 .. tokens):
+ *   - it needs ceil((start + count) / page_size) pages and holds ceil(start /
+ *     page_size); the difference is taken from the stack of free pages, requests
+ *     in order and each request's pages in order, from the top entry
+ *     free_pages[pool[0] - 1] downward, into the following entries of its row of
+ *     table [batch, table_stride];
+ *   - slots [batch, tokens] receives page * page_size + row of each new position
+ *     start[b] + t, and -1 for t >= count[b].
+ * pool is {number of free pages, 0}; pool_out receives the new one and may be pool.
+ * Entries of table that are not filled, and free_pages, are left as they are.  A
+ * request with start < 0, count outside 0 .. tokens or more positions than its
+ * table row holds gets no page and slots of -1 (LLAMA_ERR_POS_RANGE in err_dev);
+ * with too few free pages for all requests nothing is taken and every slot is -1
+ * (LLAMA_ERR_NO_PAGES); a page id outside [0, n_pages) gives slots of -1
+ * (LLAMA_ERR_INVALID_ARG). */
+int llama_paged_plan(const int32_t* start, const int32_t* count, int batch, int tokens, int page_size, int n_pages,
+                     const int32_t* free_pages, const int32_t* pool, int32_t* pool_out, int32_t* table,
+                     int table_stride, int32_t* slots, int32_t* err_dev, void* stream);
+
+/* The inverse of llama_paged_plan with the same start and count: the pages that
+ * it took go back on the stack, in the order that restores it exactly (free_pages
+ * has n_pages entries).  start = 0 and count = the length gives back all pages of
+ * a request.  Nothing is given back when the stack has no room for all of them
+ * (LLAMA_ERR_NO_PAGES); a request out of range is left out (LLAMA_ERR_POS_RANGE).
+ * Every page is released once: pages that several rows share (beams) are released
+ * through the row that planned them. */
+int llama_paged_release(const int32_t* start, const int32_t* count, int batch, int page_size, int n_pages,
+                        int32_t* free_pages, const int32_t* pool, int32_t* pool_out, const int32_t* table,
+                        int table_stride, int32_t* err_dev, void* stream);
+
+/* Rows of a contiguous cache k, v [batch, n_kv_heads, src_seq, head_dim] (as
+ * llama_block_prefill leaves them) to their pages: row src_pos + t of sequence b
+ * goes to slot slots[b][t], t < tokens.  A negative slot is skipped, a slot beyond
+ * the cache is skipped and recorded (LLAMA_ERR_INVALID_ARG).  Slots must differ
+ * from one another; rows that no slot names are left as they are. */
+int llama_paged_store(const void* k, const void* v, int batch, int tokens, int src_seq, int src_pos,
+                      const int32_t* slots, int n_kv_heads, int head_dim, int dtype, const llama_paged_cache* kv,
+                      int32_t* err_dev, void* stream);
+
+/* Attention of one new token per sequence over its pages: q, o [batch, n_heads,
+ * head_dim]; sequence b attends its first lens[b] positions (the new token's among
+ * them), query head h reads KV head h / (n_heads / n_kv_heads) ("Llama 3.1 70B",
+ * Grouped-Query Attention; scores scaled by 1/sqrt(head_dim)).  lens[b] = 0 gives a
+ * row of zeros.  max_len bounds the lengths (it sizes the workspace): a length
+ * outside 0 .. max_len, or beyond the table row, is recorded (LLAMA_ERR_POS_RANGE)
+ * and gives a row of zeros; a page id outside [0, n_pages) among the pages that a
+ * sequence attends is recorded (LLAMA_ERR_INVALID_ARG) and leaves that sequence's
+ * row undefined.  Cache rows and table entries behind the length are not used,
+ * whatever they hold.  At most 64 query heads per KV head. */
+size_t llama_paged_attention_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_dim, int max_len);
+int llama_paged_attention(const void* q, int batch, int n_heads, int n_kv_heads, int head_dim, int dtype,
+                          const llama_paged_cache* kv, const int32_t* table, int table_stride, const int32_t* lens,
+                          int max_len, void* o, void* workspace, size_t workspace_bytes, int32_t* err_dev,
+                          void* stream);
+
+/* llama_block_decode_seqpos on a paged cache: sequence b at position pos_seq[b],
+ * its rows found through row b of table [batch, table_stride]; the page of the
+ * position must be in the table (llama_paged_plan).  The limits
+ * are the same; a page id outside [0, n_pages) is recorded in the handle's error
+ * word (LLAMA_ERR_INVALID_ARG; that cache row is not written, y undefined).  Rows of
+ * table may share pages that no position of the call is written to. */
+int llama_block_decode_paged(llama_block blk, const void* x, int batch, const llama_paged_cache* kv,
+                             const int32_t* table, int table_stride, const int32_t* pos_seq, void* y,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Beam search ("How Llama 3.1 Generates the Next Token", Sampling, names greedy
+ * choice and sampling; beam search keeps the best few continuations instead).
+ * ------------------------------------------------------------------------- */
+
+/* The n_out best continuations of each group's beams.  logits [groups * beams,
+ * vocab] fp32, scores [groups * beams] the beams' cumulative log probabilities
+ * (-inf: the beam takes no part).  Token v after beam k has the score
+ *   scores[k] + logits[k][v] - log sum_u e^(logits[k][u]);
+ * a beam with last[k] == eos has ended: its only continuation is eos, at scores[k]
+ * (last may be NULL: no beam ends).  Outputs [groups, n_out] in decreasing score,
+ * equal scores by increasing beam and then token: parents (row of the beam, in
+ * 0 .. groups * beams - 1), tokens, out_scores.  Candidates are compared in fp64.
+ * Logits must be finite or -inf (probability 0), scores too; continuations of score
+ * -inf are listed only when the others are fewer than n_out.  1 <= beams <= 32,
+ * 1 <= n_out <= 64, n_out <= vocab <= 2^20, groups * beams <= 65535; otherwise
+ * LLAMA_ERR_INVALID_ARG. */
+size_t llama_beam_select_workspace_bytes(int groups, int beams, int vocab, int n_out);
+int llama_beam_select(const float* logits, int groups, int beams, int vocab, const float* scores,
+                      const int32_t* last, int eos, int n_out, int32_t* parents, int32_t* tokens, float* out_scores,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* The beams' states follow the chosen parents, in place: row i of table [groups *
+ * beams, table_stride] continues row parents[i] of the same group.  The beams of a
+ * group have one length lens[i], i.e. c = lens / page_size full pages and r = lens %
+ * page_size rows in the page after them.  Entries 0 .. c-1 of row i become those of
+ * its parent (beams share full pages, which are not written again); if r > 0, rows
+ * 0 .. r-1 of page table[i][c] become those of the parent's page, in the caches of
+ * all n_layers (1 .. 128; distinct buffers of one n_pages and page_size).  Entries
+ * from c on stay: they are the row's own pages.  A group whose parents lie outside
+ * it, whose lengths differ or exceed the table, or whose rows share the page to be
+ * filled is left as it was (LLAMA_ERR_INVALID_ARG in err_dev).  beams <= 32. */
+int llama_beam_reorder(const int32_t* parents, int groups, int beams, const int32_t* lens, int32_t* table,
+                       int table_stride, const llama_paged_cache* caches, int n_layers, int n_kv_heads, int head_dim,
+                       int dtype, int32_t* err_dev, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Step-level entry points (the block's individual steps, for unit tests and
