@@ -490,6 +490,10 @@ cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s) {
     if (a.batch <= 0) return cudaSuccess;
+    // where the contiguous decode takes the tensor cores (8 query rows a tile)
+    if (a.dtype == LLAMA_BF16 && attention_tc_supported(a.n_heads, a.n_kv_heads, a.head_dim) &&
+        a.n_heads / a.n_kv_heads <= 8)
+        return launch_attention_tc_paged(a, s);
     if (a.dtype == LLAMA_BF16) return a.head_dim == 128 ? paged_decode_impl<bf16, 128>(a, s) : cudaErrorInvalidValue;
     switch (a.head_dim) {
         case 32: return paged_decode_impl<float, 32>(a, s);

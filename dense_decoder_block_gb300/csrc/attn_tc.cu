@@ -49,6 +49,8 @@ struct TcArgs {
     int batch, tokens, n_heads, n_kv_heads, kv_seq, start_pos, max_pos;
     const int* pos_dev;
     const int* pos_seq;  // decode: sequence b at position pos_seq[b] (the k_attn_tc_dec kernel only)
+    PageTable pages;     // paged decode: kc, vc are pages (k_attn_tc_dec<true>)
+    int pos_off;         // paged decode: see paged_keys
     float scale_log2;
     const bf16* q;       // decode: [B, Hq * 128]
     bf16* o;             // prefill: [B * T, Hq * 128]
@@ -1039,6 +1041,13 @@ __device__ __forceinline__ void tmem_ld_quarter(uint32_t taddr, int q, float (&o
     }
 }
 
+// PAGED: the same units over a paged cache.  The map's rows are those of all pages
+// ([n_pages][n_kv_heads][page_size]) and its box one page (of at most 128 rows) of 64
+// columns, so a chunk arrives as 128 / page_size boxes per half, issued by as many
+// lanes of the producer warp; pages behind the last key are not copied and what the
+// stage holds in their place is masked (scores) or zeroed (values).  A sequence may
+// have no key, and so no unit.
+template <bool PAGED>
 __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_constant__ CUtensorMap mK,
                                                                 const __grid_constant__ CUtensorMap mV,
                                                                 const TcArgs a) {
@@ -1074,9 +1083,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
             int run = 0, bad = 0;
             for (int b0 = 0; b0 < a.batch; b0 += 32) {
                 const int b = b0 + lane;
-                const int p = b < a.batch ? a.pos_seq[b] : 0;
-                const bool in = b < a.batch && p >= 0 && p < a.max_pos;
-                if (b < a.batch && !in) bad = 1;
+                int p = b < a.batch ? a.pos_seq[b] : 0;
+                bool in = b < a.batch && p >= 0 && p < a.max_pos;
+                if constexpr (PAGED) {   // a sequence out of range has no unit; the others run
+                    bool out = false;
+                    p = b < a.batch ? paged_keys(p, a.pos_off, a.max_pos, out) - 1 : -1;
+                    in = p >= 0;
+                    if (out) bad = 1;
+                } else if (b < a.batch && !in) {
+                    bad = 1;
+                }
                 int nt = in ? p / kAttnChunk + 1 : 0;
 #pragma unroll
                 for (int off = 1; off < 32; off <<= 1) {
@@ -1098,7 +1114,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         __syncthreads();
         if (s_bad) {
             if (threadIdx.x == 0 && blockIdx.x == 0) record_error(a.err, LLAMA_ERR_POS_RANGE);
-            return;
+            if (!PAGED) return;
         }
         dm.pre = s_pre;
         dm.spos = s_pos;
@@ -1116,7 +1132,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
     const int u_begin = (int)(((long)n_units * blockIdx.x) / gridDim.x);
     const int u_end = (int)(((long)n_units * (blockIdx.x + 1)) / gridDim.x);
     const int n_iter = u_end - u_begin;
-    if (n_iter <= 0) return;
+    if (n_iter <= 0) {
+        if (PAGED) ptx::griddep_wait();   // with no unit at all the grid still must not end before the one it follows
+        return;
+    }
     int* err = a.err;
 
     if (threadIdx.x == 0) {
@@ -1145,7 +1164,54 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
-    if (warp == kDecSlots || warp == kDecSlots + 2) {
+    if (PAGED && (warp == kDecSlots || warp == kDecSlots + 2)) {
+        // ------------------------------------------------------------------ TMA producers (K, V), whole warps
+        const bool is_k = (warp == kDecSlots);
+        const CUtensorMap* map = is_k ? &mK : &mV;
+        uint64_t* full = is_k ? k_full : v_full;
+        uint64_t* empty = is_k ? k_empty : v_empty;
+        uint8_t* ring = sm + (is_k ? D_OFF_K : D_OFF_V);
+        const int n_st = is_k ? kDecStagesK : kDecStagesV;
+        const int shift = a.pages.shift, ps = 1 << shift, box = min(ps, kAttnChunk);
+        if (lane == 0) ptx::prefetch_tmap(map);
+        const uint64_t pol = ptx::policy_evict_first();
+        bool waited = false;
+        int issued = 0;
+        // lane = (page of the chunk, half): its page id is read a unit ahead of its copy
+        const int mine = lane >> 1, half = lane & 1;
+        auto pages_of = [&](const DecUnit& d) {
+            return (min(kAttnChunk, d.pos + 1 - d.c * kAttnChunk) + box - 1) / box;
+        };
+        auto lookup = [&](int i) -> int {
+            if (i >= n_iter) return 0;
+            const DecUnit d = dec_unit(dm, u_begin + i);
+            if (mine >= pages_of(d)) return 0;
+            const int id = page_of(a.pages, d.b, (d.c * kAttnChunk >> shift) + mine, is_k && half == 0 ? err : nullptr);
+            return max(id, 0);   // recorded; the row is undefined, the copy stays inside the cache
+        };
+        int next = lookup(0);
+        for (int i = 0; i < n_iter; ++i, ++issued) {
+            const int st = i % n_st;
+            int go = 1;
+            if (lane == 0 && i >= n_st) go = ptx::mbar_wait(&empty[st], ((i / n_st) - 1) & 1, err);
+            if (!__shfl_sync(0xffffffffu, go, 0)) break;
+            const DecUnit d = dec_unit(dm, u_begin + i);
+            if (!waited && d.c == d.nt - 1) {   // this chunk holds the row the QKV step writes
+                ptx::griddep_wait();
+                waited = true;
+            }
+            const int n = pages_of(d), id = next;
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], n * box * 256);
+            __syncwarp();
+            if (mine < n)
+                ptx::tma_load_2d_hint(ring + st * 2 * kSub + half * kSub + mine * box * 128, map, &full[st], half * 64,
+                                      ((id * a.n_kv_heads + d.g) << shift) + (d.c * kAttnChunk & (ps - 1)), pol);
+            next = lookup(i + 1);
+        }
+        if (lane == 0)
+            for (int i = max(0, issued - n_st); i < issued; ++i)
+                ptx::mbar_wait_drain(&full[i % n_st], (i / n_st) & 1);
+    } else if (!PAGED && (warp == kDecSlots || warp == kDecSlots + 2)) {
         // ------------------------------------------------------------------ TMA producers (K, V)
         if (lane == 0) {
             const bool is_k = (warp == kDecSlots);
@@ -1384,6 +1450,8 @@ TcArgs make_args(const AttnArgs& a) {
     k.max_pos = a.max_pos;
     k.pos_dev = a.pos_dev;
     k.pos_seq = a.pos_seq;
+    k.pages = a.pages;
+    k.pos_off = a.pos_off;
     k.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
     k.q = (const bf16*)a.q;
     k.o = (bf16*)a.o;
@@ -1447,12 +1515,12 @@ cudaError_t launch_attention_tc_decode(const AttnArgs& a, int chunks_per_cta, cu
         // persistent: one CTA per SM (units assigned on the device from the position)
         const int n_sm = device_sm_count();
         const long max_units = (long)a.batch * a.n_kv_heads * a.n_chunks;
-        cudaError_t r = kernel_setup_once((const void*)k_attn_tc_dec, [](const void* kern) {
+        cudaError_t r = kernel_setup_once((const void*)k_attn_tc_dec<false>, [](const void* kern) {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, D_SMEM_BYTES);
         });
         if (r != cudaSuccess) return r;
         dim3 grid((unsigned)std::min<long>(max_units, n_sm));
-        r = launch_pdl(k_attn_tc_dec, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);
+        r = launch_pdl(k_attn_tc_dec<false>, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);
         if (r != cudaSuccess) return r;
         return launch_attention_combine(a, s);
     }
@@ -1467,6 +1535,35 @@ cudaError_t launch_attention_tc_decode(const AttnArgs& a, int chunks_per_cta, cu
     r = launch_pdl(kern, grid, dim3(kThreads), SMEM_BYTES, s, mk, mv, k);
     if (r != cudaSuccess) return r;
     return launch_attention_combine(a, s);
+}
+
+cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s) {
+    if (a.batch <= 0) return cudaSuccess;
+    const int ps = 1 << a.pages.shift;
+    const uint64_t rows = (uint64_t)a.pages.n_pages * a.n_kv_heads * ps;
+    CUtensorMap mk, mv;
+    if (!make_tmap_bf16(&mk, a.kc, rows, 128, std::min(ps, kAttnChunk), nullptr) ||
+        !make_tmap_bf16(&mv, a.vc, rows, 128, std::min(ps, kAttnChunk), nullptr))
+        return cudaErrorInvalidValue;
+    cudaError_t r = kernel_setup_once((const void*)k_attn_tc_dec<true>, [](const void* kern) {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, D_SMEM_BYTES);
+    });
+    if (r != cudaSuccess) return r;
+    // a launch maps its units from at most kSeqPosMax lengths
+    const int n_rep = a.n_heads / a.n_kv_heads;
+    for (int b0 = 0; b0 < a.batch; b0 += kSeqPosMax) {
+        TcArgs k = make_args(a);
+        k.batch = std::min(a.batch - b0, kSeqPosMax);
+        k.pos_seq += b0;
+        k.pages.table += (size_t)b0 * a.pages.stride;
+        k.q += (size_t)b0 * a.n_heads * 128;
+        k.partial += (size_t)b0 * a.n_kv_heads * a.n_chunks * n_rep * kPartStride;
+        const long max_units = (long)k.batch * a.n_kv_heads * a.n_chunks;
+        const dim3 grid((unsigned)std::min<long>(max_units, device_sm_count()));
+        r = launch_pdl(k_attn_tc_dec<true>, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);
+        if (r != cudaSuccess) return r;
+    }
+    return launch_attention_paged_combine(a, s);
 }
 
 }  // namespace llama

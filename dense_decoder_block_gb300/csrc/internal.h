@@ -139,6 +139,8 @@ cudaError_t launch_attention_combine(const AttnArgs& a, cudaStream_t s);
 // Decode attention over a paged cache (pos_seq and pages set): CUDA cores, + combine.
 // A sequence without keys, or with a position out of range (recorded), gets a row of zeros.
 cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s);
+// Tensor cores (bf16, attention_tc_supported, at most 8 query heads per KV head), + combine.
+cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s);
 // LLAMA_OK, or why the pages of kv cannot be used with these heads.
 int paged_cache_check(const llama_paged_cache* kv, int n_kv_heads, int head_dim, int dtype);

@@ -403,7 +403,8 @@ int llama_paged_store(const void* k, const void* v, int batch, int tokens, int s
  * and gives a row of zeros; a page id outside [0, n_pages) among the pages that a
  * sequence attends is recorded (LLAMA_ERR_INVALID_ARG) and leaves that sequence's
  * row undefined.  Cache rows and table entries behind the length are not used,
- * whatever they hold.  At most 64 query heads per KV head. */
+ * whatever they hold.  At most 64 query heads per KV head.  The result is, bit for
+ * bit, the attention that llama_block_decode computes from the same rows. */
 size_t llama_paged_attention_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_dim, int max_len);
 int llama_paged_attention(const void* q, int batch, int n_heads, int n_kv_heads, int head_dim, int dtype,
                           const llama_paged_cache* kv, const int32_t* table, int table_stride, const int32_t* lens,
@@ -412,8 +413,8 @@ int llama_paged_attention(const void* q, int batch, int n_heads, int n_kv_heads,
 
 /* llama_block_decode_seqpos on a paged cache: sequence b at position pos_seq[b],
  * its rows found through row b of table [batch, table_stride]; the page of the
- * position must be in the table (llama_paged_plan).  The limits
- * are the same; a page id outside [0, n_pages) is recorded in the handle's error
+ * position must be in the table (llama_paged_plan).  Same result, bit for bit, and
+ * the same limits; a page id outside [0, n_pages) is recorded in the handle's error
  * word (LLAMA_ERR_INVALID_ARG; that cache row is not written, y undefined).  Rows of
  * table may share pages that no position of the call is written to. */
 int llama_block_decode_paged(llama_block blk, const void* x, int batch, const llama_paged_cache* kv,

@@ -1,6 +1,6 @@
 """The paged KV cache on the GPU: plan, release, store and the attention of one new
-token, against plain references (tests/paged_ref.py), and what the paged decode step of
-a block records."""
+token, against plain references (tests/paged_ref.py), and the paged decode step of a
+block against its contiguous one, bit for bit."""
 import numpy as np
 import pytest
 import torch
@@ -360,6 +360,57 @@ def test_attention_on_another_stream_and_in_graphs():
 
 
 # ----------------------------------------------------------------------------- the block's decode step
+
+@pytest.mark.parametrize("dims", [workloads.BlockDims(512, 8, 2, 128, 1024), workloads.BlockDims(1024, 8, 1, 128, 512),
+                                  workloads.BlockDims(256, 2, 2, 128, 256),
+                                  workloads.BlockDims(1024, 96, 12, 128, 256)],
+                         ids=["group4", "group8", "group1", "one-segment-qkv"])
+@pytest.mark.parametrize("ps", [16, 128])
+def test_paged_decode_step_equals_the_contiguous_one(dims, ps):
+    """Ragged prompts prefilled, planned, stored and decoded for 20 steps on pages: y and the attention
+    output equal the contiguous cache's, bit for bit; rows behind the positions stay NaN."""
+    ddb = _ddb()
+    B, T, max_seq, steps = 3, 130, 320, 20
+    lens = [130, 1, 97]
+    w, g = workloads.make_weights(dims, weight_std=0.03)
+    dev = torch.device(DEV)
+    blk = ddb.LlamaBlock(dims, {k: t.to(dev) for k, t in w.items()}, {k: t.to(dev) for k, t in g.items()}, max_seq)
+    x = workloads.make_x(B, T, dims.d_model).to(dev)
+    kc = torch.full((B, dims.n_kv_heads, max_seq, 128), float("nan"), dtype=torch.bfloat16, device=dev)
+    vc = kc.clone()
+    blk.prefill(x, ddb.KVCache(kc, vc), torch.empty_like(x), blk.workspace(B, T))
+    columns = ref.ceil_div(max_seq, ps)
+    n_pages = B * columns
+    pk = torch.full((n_pages, dims.n_kv_heads, ps, 128), float("nan"), dtype=torch.bfloat16, device=dev)
+    kv = ddb.PagedCache(pk, pk.clone())
+    free = torch.randperm(n_pages, generator=torch.Generator().manual_seed(1)).to(torch.int32).to(dev)
+    pool, err = _i32([n_pages, 0]), _i32([0])
+    table = torch.full((B, columns), -1, dtype=torch.int32, device=dev)
+    slots = torch.empty(B, T, dtype=torch.int32, device=dev)
+    pos = _i32(lens)
+    ddb.llama_paged_plan(torch.zeros_like(pos), pos, ps, n_pages, free, pool, table, slots, err_dev=err)
+    ddb.llama_paged_store(kc, vc, slots, kv, err_dev=err)
+    one, step_slots = torch.ones_like(pos), torch.empty(B, 1, dtype=torch.int32, device=dev)
+    ws, wp = blk.workspace(B, 1), blk.workspace(B, 1)
+    for s in range(steps):
+        xs = workloads.make_x(B, 1, dims.d_model, seed=50 + s).to(dev)
+        y, yp = torch.empty_like(xs), torch.empty_like(xs)
+        blk.decode_seqpos(xs, ddb.KVCache(kc, vc), pos, y, ws)
+        ddb.llama_paged_plan(pos, one, ps, n_pages, free, pool, table, step_slots, err_dev=err)
+        blk.decode_paged(xs, kv, table, pos, yp, wp)
+        torch.cuda.synchronize()
+        assert blk.poll_error() == 0 and int(err[0]) == 0
+        assert torch.equal(y, yp), f"step {s}"
+        # the step's attention alone, from its own q
+        mid = blk.intermediates(wp, B, 1)
+        o = _attend(ddb, mid["q"].reshape(B, dims.n_heads, 128).contiguous(), kv, table, (pos + 1).tolist(), max_seq)
+        assert torch.equal(o.view(B, -1), mid["o"])
+        pos.add_(1)
+    rows = torch.isnan(kv.k.float()).all(dim=3).all(dim=1).sum()
+    assert int(rows) == n_pages * ps - int(pos.sum())
+    ddb.llama_paged_release(torch.zeros_like(pos), pos, ps, n_pages, free, pool, table, err_dev=err)
+    assert pool.tolist() == [n_pages, 0] and sorted(free.tolist()) == list(range(n_pages)) and int(err[0]) == 0
+
 
 def test_paged_decode_step_records_bad_positions_and_pages():
     ddb = _ddb()
