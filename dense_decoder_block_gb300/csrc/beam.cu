@@ -10,11 +10,14 @@
 // normaliser shift all of them alike), so one pass over the logits gives everything:
 // k_beam_scan reads a slice of a row once, keeps it in registers, and leaves the slice's
 // maximum, its sum of exponentials and its n_out best (logit, token) pairs in order;
-// k_beam_merge joins a request's slices: normalisers in 64 bits from the slices' (m, s),
-// then n_out rounds of a tournament over the heads of the beams x slices sorted lists,
-// candidates compared by their 64-bit value and then by place.  Slice sums are fp32
-// (at most kSlice terms of at most 1, relative error below 1e-6); everything after them
-// is fp64, since an fp32 cumulative score rounds different logits to equal candidates.
+// k_beam_merge joins a request's slices.  Slice sums are fp32 (at most kSlice terms of at
+// most 1); everything after them is fp64, since an fp32 cumulative score rounds different
+// logits to equal candidates.
+//
+// Bound by the read of the logits.  Finding the best few must cost less than that: a bound
+// on the n_out-th largest, from the threads' maxima, leaves a few dozen candidates per
+// slice, which are ranked by counting the larger ones.  n_out rounds of a block-wide
+// maximum instead took 179 us for 256 rows of 128,256 logits (n_out = 16).
 #include <algorithm>
 
 #include "internal.h"
@@ -27,8 +30,11 @@ constexpr int kScanThreads = 256;
 constexpr int kScanWarps = kScanThreads / 32;
 constexpr int kPerThread = 32;                            // logits per thread
 constexpr int kSlice = kScanThreads * kPerThread;
+constexpr int kSplitsMax = (1 << 20) / kSlice;            // vocab <= 2^20
+constexpr int kScanCap = 1024;                            // candidates ranked per slice
 constexpr int kMergeThreads = 512;
 constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeCap = 2048;                           // candidates ranked per request
 constexpr int kBeamsMax = 32;
 constexpr int kOutMax = 64;
 constexpr unsigned kAll = 0xffffffffu;
@@ -79,9 +85,35 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k) {
     return ((unsigned long long)hi << 32) | lo;
 }
 
-__global__ void __launch_bounds__(kScanThreads) k_beam_scan(const BeamArgs a) {
-    __shared__ unsigned long long s_key[kScanWarps];
+// The q-th largest of the lanes' keys (equal keys counted one by one), q <= 32.
+template <typename K>
+__device__ __forceinline__ K warp_nth(K key, int q) {
+    const int lane = threadIdx.x & 31;
+    K top{};
+    for (int i = 0; i < q; ++i) {
+        if constexpr (sizeof(K) == 8) top = warp_max(key);
+        else top = __reduce_max_sync(kAll, key);
+        const unsigned who = __ballot_sync(kAll, key == top);
+        if (lane == __ffs(who) - 1) key = 0;
+    }
+    return top;
+}
+
+// 2^x on the special-function unit (ex2.approx.ftz: relative error 2^-22).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// VEC: rows of whole 16-byte vectors, read as such; a thread then holds runs of four.
+template <bool VEC>
+__global__ void __launch_bounds__(kScanThreads, 4) k_beam_scan(const BeamArgs a) {
+    __shared__ unsigned s_max[kScanWarps], s_nth[kScanWarps];
     __shared__ float s_sum[kScanWarps];
+    __shared__ unsigned long long s_list[kScanCap];
+    __shared__ unsigned long long s_key[kScanWarps];
+    __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.y, split = blockIdx.x;
     ptx::griddep_wait();
@@ -89,62 +121,105 @@ __global__ void __launch_bounds__(kScanThreads) k_beam_scan(const BeamArgs a) {
     if (!row_live(a, row)) return;
     const float* z = a.logits + (size_t)row * a.vocab;
     const int v0 = split * kSlice, n = min(kSlice, a.vocab - v0);
+    auto at = [&](int i) { return VEC ? (i >> 2) * (4 * kScanThreads) + tid * 4 + (i & 3) : tid + i * kScanThreads; };
     float x[kPerThread];
-    unsigned long long mine = 0;   // this thread's best remaining candidate
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        const int j = tid + i * kScanThreads;
-        x[i] = j < n ? __ldcg(z + v0 + j) : -INFINITY;
-    }
+        for (int i = 0; i < kPerThread; i += 4) {
+            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (at(i) < n) v = __ldcg(reinterpret_cast<const float4*>(z + v0 + at(i)));
+            x[i] = v.x;
+            x[i + 1] = v.y;
+            x[i + 2] = v.z;
+            x[i + 3] = v.w;
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-        const int j = tid + i * kScanThreads;
-        if (j < n) mine = max(mine, cand_key(x[i], v0 + j));
+        for (int i = 0; i < kPerThread; ++i) x[i] = at(i) < n ? __ldcg(z + v0 + at(i)) : -INFINITY;
     }
-    // the slice's maximum is its best candidate's logit
-    unsigned long long best = warp_max(mine);
-    if (lane == 0) s_key[warp] = best;
+    float most = x[0];
+#pragma unroll
+    for (int i = 1; i < kPerThread; ++i) most = fmaxf(most, x[i]);
+    // A lower bound of the slice's n_out-th largest logit: in every warp at least
+    // ceil(n_out / kScanWarps) threads have a logit of the warp's bound or more, so the
+    // smallest of the warps' bounds has n_out logits at or above it -- and, a thread in
+    // kScanWarps holding one of them, not many more.
+    const unsigned mine = at(0) < n ? ordered(most) : 0u;
+    const unsigned wmax = __reduce_max_sync(kAll, mine);
+    const unsigned nth = warp_nth(mine, (a.n_out + kScanWarps - 1) / kScanWarps);
+    if (lane == 0) {
+        s_max[warp] = wmax;
+        s_nth[warp] = nth;
+    }
+    if (tid == 0) s_n = 0;
     __syncthreads();
+    unsigned top_key = 0, bound = 0xffffffffu;
 #pragma unroll
-    for (int w = 0; w < kScanWarps; ++w) best = max(best, s_key[w]);
-    const float m = unordered((unsigned)(best >> 32));
+    for (int w = 0; w < kScanWarps; ++w) {
+        top_key = max(top_key, s_max[w]);
+        bound = min(bound, s_nth[w]);
+    }
+    // every logit at or above the bound goes to the list
+    if (mine >= bound) {
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i)
+            if (at(i) < n && ordered(x[i]) >= bound) {
+                const int p = atomicAdd(&s_n, 1);
+                if (p < kScanCap) s_list[p] = cand_key(x[i], v0 + at(i));
+            }
+    }
+    const float m = unordered(top_key);
     const float top = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) sum += exp2f((x[i] - top) * kLog2e);
+    for (int i = 0; i < kPerThread; ++i) sum += ex2((x[i] - top) * kLog2e);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     if (lane == 0) s_sum[warp] = sum;
     __syncthreads();
     const size_t slot = (size_t)row * a.splits + split;
+    unsigned long long* out = a.cand + slot * a.n_out;
     if (tid == 0) {
         sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kScanWarps; ++w) sum += s_sum[w];
         a.part[slot] = make_float2(m, sum);
     }
-    // n_out rounds: the best remaining candidate leaves, its thread finds its next one
+    const int found = s_n;
+    if (found <= kScanCap) {
+        // keys differ, so a key's place is the number of larger ones
+        for (int c = tid; c < found; c += kScanThreads) {
+            const unsigned long long k = s_list[c];
+            int rank = 0;
+            for (int i = 0; i < found; ++i) rank += s_list[i] > k;
+            if (rank < a.n_out) out[rank] = k;
+        }
+        for (int c = found + tid; c < a.n_out; c += kScanThreads) out[c] = 0;
+        return;
+    }
+    // Many equal logits (a mask, say): n_out rounds in which the best remaining
+    // candidate leaves and its thread finds its next one.
+    unsigned long long best = ~0ull, own = ~0ull;
     for (int o = 0; o < a.n_out; ++o) {
-        if (tid == 0) a.cand[slot * a.n_out + o] = best;
-        if (best != 0 && mine == best) {
-            mine = 0;
+        if (own == best) {   // the first round: every thread
+            own = 0;
 #pragma unroll
             for (int i = 0; i < kPerThread; ++i) {
-                const int j = tid + i * kScanThreads;
-                const unsigned long long k = cand_key(x[i], v0 + j);
-                if (j < n && k < best) mine = max(mine, k);
+                const unsigned long long k = cand_key(x[i], v0 + at(i));
+                if (at(i) < n && k < best) own = max(own, k);
             }
         }
-        best = warp_max(mine);
+        best = warp_max(own);
         __syncthreads();   // the keys of the round before were read
         if (lane == 0) s_key[warp] = best;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kScanWarps; ++w) best = max(best, s_key[w]);
+        if (tid == 0) out[o] = best;
     }
 }
 
-// A candidate in the tournament: decreasing value, then increasing place.
+// A candidate of the merge: decreasing value, then increasing place.
 struct Cand {
     unsigned long long value;   // ordered form; 0: none
     unsigned place;             // beam * vocab + token
@@ -160,89 +235,145 @@ __device__ __forceinline__ Cand warp_best(Cand c) {
     return {v, place};
 }
 
+// One CTA per request.  The scan's idea once more, on the beams x slices lists: the
+// bound comes from the lists' d-th keys (d = 1 unless there are fewer lists than
+// wanted candidates), the keys at or above it are gathered and ranked by counting.
 __global__ void __launch_bounds__(kMergeThreads) k_beam_merge(const BeamArgs a) {
     // a live beam's largest logit, and its score - log sum e^(z - largest): kept apart, since
     // next to a mask of the type's lowest value a score would be lost
     __shared__ float s_top[kBeamsMax];
     __shared__ double s_shift[kBeamsMax];
+    __shared__ int s_mode[kBeamsMax];       // 0: live, 1: ended, 2: at -inf
+    __shared__ unsigned long long s_nth[kMergeWarps];
+    __shared__ unsigned long long s_value[kMergeCap];
+    __shared__ unsigned s_place[kMergeCap];
     __shared__ Cand s_best[kMergeWarps];
+    __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = blockIdx.x;
     const int row0 = g * a.beams;
     ptx::griddep_wait();
+    if (tid == 0) s_n = 0;
     // normalisers: one warp per beam
     for (int k = warp; k < a.beams; k += kMergeWarps) {
         const int row = row0 + k;
+        const float score = __ldcg(a.scores + row);
+        if (lane == 0) {
+            s_mode[k] = score == -INFINITY ? 2 : row_ended(a, row) ? 1 : 0;
+            s_top[k] = 0.f;
+            s_shift[k] = score;
+        }
         if (!row_live(a, row)) continue;
         const float2* p = a.part + (size_t)row * a.splits;
+        float2 ms[kSplitsMax / 32];
         float m = -INFINITY;
-        for (int s = lane; s < a.splits; s += 32) m = fmaxf(m, __ldcg(p + s).x);
+#pragma unroll
+        for (int i = 0; i < kSplitsMax / 32; ++i) {
+            const int s = lane + 32 * i;
+            ms[i] = s < a.splits ? __ldcg(p + s) : make_float2(-INFINITY, 0.f);
+            m = fmaxf(m, ms[i].x);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        if (m == -INFINITY) continue;   // no token has a probability: every candidate is at -inf
         double sum = 0;
-        for (int s = lane; s < a.splits; s += 32) {
-            const float2 ms = __ldcg(p + s);
-            if (ms.x != -INFINITY) sum += (double)ms.y * exp((double)ms.x - (double)m);
-        }
+#pragma unroll
+        for (int i = 0; i < kSplitsMax / 32; ++i) sum += (double)(ms[i].y * ex2((ms[i].x - m) * kLog2e));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
         if (lane == 0) {
-            s_top[k] = m == -INFINITY ? 0.f : m;
-            s_shift[k] = m == -INFINITY ? 0. : (double)__ldcg(a.scores + row) - log(sum);
+            s_top[k] = m;
+            s_shift[k] = (double)score - log(sum);
         }
     }
     __syncthreads();
-    // Every list (a live beam's slice; a beam that ended or is at -inf) has one thread;
-    // list i + kMergeThreads, ... of a thread come after its list i in the same loop.
     const int lists = a.beams * a.splits;
-    constexpr int kLists = kBeamsMax * 128 / kMergeThreads;   // splits <= 128: vocab <= 2^20
-    unsigned char at[kLists];                                 // how many of the list are taken
-    Cand head[kLists];
     auto fetch = [&](int list, int pos) -> Cand {
-        if (pos >= a.n_out) return {0ull, 0xffffffffu};
-        const int k = list / a.splits, s = list - k * a.splits, row = row0 + k;
-        const double score = __ldcg(a.scores + row);
-        if (!row_live(a, row)) {
+        const int k = list / a.splits, s = list - k * a.splits;
+        const unsigned base = (unsigned)k * a.vocab;
+        if (s_mode[k] != 0) {
             if (s != 0) return {0ull, 0xffffffffu};
-            if (row_ended(a, row) && score != -INFINITY) {
+            if (s_mode[k] == 1) {
                 // (k, eos) first, then the tokens that do not follow an end, at -inf
-                if (pos == 0) return {ordered(score), (unsigned)k * a.vocab + a.eos};
+                if (pos == 0) return {ordered(s_shift[k]), base + a.eos};
                 const int v = pos - 1 < a.eos ? pos - 1 : pos;
-                return {ordered((double)-INFINITY), v < a.vocab ? (unsigned)k * a.vocab + v : 0xffffffffu};
+                return {ordered((double)-INFINITY), base + v};
             }
-            return {ordered((double)-INFINITY), (unsigned)k * a.vocab + pos};
+            return {ordered((double)-INFINITY), base + pos};
         }
-        const unsigned long long key = __ldcg(a.cand + ((size_t)row * a.splits + s) * a.n_out + pos);
+        const unsigned long long key = __ldcg(a.cand + ((size_t)(row0 + k) * a.splits + s) * a.n_out + pos);
         if (key == 0) return {0ull, 0xffffffffu};
         const double below = (double)unordered((unsigned)(key >> 32)) - (double)s_top[k];
-        return {ordered(below + s_shift[k]), (unsigned)k * a.vocab + ~(unsigned)key};
+        return {ordered(below + s_shift[k]), base + ~(unsigned)key};
     };
+    // list i belongs to warp i % kMergeWarps: at least `each` lists per warp
+    const int q = (a.n_out + kMergeWarps - 1) / kMergeWarps, each = lists / kMergeWarps;
+    const int d = each == 0 ? 1 : min(a.n_out, (q + min(each, 32) - 1) / min(each, 32));
+    unsigned long long mine = 0;
+    for (int i = lane * kMergeWarps + warp; i < lists; i += kMergeThreads) mine = max(mine, fetch(i, d - 1).value);
+    mine = warp_nth(mine, (q + d - 1) / d);
+    if (lane == 0) s_nth[warp] = mine;
+    __syncthreads();
+    unsigned long long bound = ~0ull;
 #pragma unroll
-    for (int i = 0; i < kLists; ++i) {
-        at[i] = 0;
-        head[i] = tid + i * kMergeThreads < lists ? fetch(tid + i * kMergeThreads, 0) : Cand{0ull, 0xffffffffu};
+    for (int w = 0; w < kMergeWarps; ++w) bound = min(bound, s_nth[w]);
+    // Candidates at -inf count only where the others are fewer than n_out (a first step's
+    // idle beams hold most of the lists' heads at -inf or empty, and so the bound down).
+    const int total = lists * a.n_out;
+    const unsigned long long lowest = ordered((double)-INFINITY);
+    bound = max(bound, lowest + 1);
+    int found;
+    while (true) {
+#pragma unroll 4
+        for (int i = tid; i < total; i += kMergeThreads) {
+            const int list = i / a.n_out;
+            const Cand c = fetch(list, i - list * a.n_out);
+            if (c.value >= bound) {
+                const int p = atomicAdd(&s_n, 1);
+                if (p < kMergeCap) {
+                    s_value[p] = c.value;
+                    s_place[p] = c.place;
+                }
+            }
+        }
+        __syncthreads();
+        found = s_n;
+        if (found >= a.n_out || bound == lowest) break;
+        __syncthreads();   // everyone has read the count
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        bound = lowest;
     }
+    auto emit = [&](int o, const Cand& c) {
+        const size_t at = (size_t)g * a.n_out + o;
+        a.parents[at] = row0 + (int)(c.place / (unsigned)a.vocab);
+        a.tokens[at] = (int)(c.place % (unsigned)a.vocab);
+        a.best[at] = (float)__longlong_as_double(
+            (long long)(c.value >> 63 ? c.value & 0x7fffffffffffffffull : ~c.value));
+    };
+    if (found <= kMergeCap) {
+        for (int c = tid; c < found; c += kMergeThreads) {
+            const Cand x{s_value[c], s_place[c]};
+            int rank = 0;
+            for (int i = 0; i < found; ++i) rank += better(Cand{s_value[i], s_place[i]}, x);
+            if (rank < a.n_out) emit(rank, x);
+        }
+        return;
+    }
+    // many equal candidates: n_out rounds over all keys below the last one taken
+    Cand last{~0ull, 0u};
     for (int o = 0; o < a.n_out; ++o) {
-        Cand mine{0ull, 0xffffffffu};
-#pragma unroll
-        for (int i = 0; i < kLists; ++i)
-            if (better(head[i], mine)) mine = head[i];
-        Cand best = warp_best(mine);
+        Cand best{0ull, 0xffffffffu};
+        for (int i = tid; i < total; i += kMergeThreads) {
+            const int list = i / a.n_out;
+            const Cand c = fetch(list, i - list * a.n_out);
+            if (better(last, c) && better(c, best)) best = c;
+        }
+        best = warp_best(best);
         __syncthreads();
         if (lane == 0) s_best[warp] = best;
         __syncthreads();
-        best = warp_best(lane < kMergeWarps ? s_best[lane] : Cand{0ull, 0xffffffffu});
-        if (tid == 0) {
-            const unsigned p = best.value ? best.place : 0u;
-            const unsigned long long u = best.value;
-            a.parents[(size_t)g * a.n_out + o] = row0 + (int)(p / (unsigned)a.vocab);
-            a.tokens[(size_t)g * a.n_out + o] = (int)(p % (unsigned)a.vocab);
-            a.best[(size_t)g * a.n_out + o] =
-                (float)__longlong_as_double((long long)(u >> 63 ? u & 0x7fffffffffffffffull : ~u));
-        }
-#pragma unroll
-        for (int i = 0; i < kLists; ++i)
-            if (best.value != 0 && head[i].value == best.value && head[i].place == best.place)
-                head[i] = fetch(tid + i * kMergeThreads, ++at[i]);
+        last = warp_best(lane < kMergeWarps ? s_best[lane] : Cand{0ull, 0xffffffffu});
+        if (tid == 0) emit(o, last);
     }
 }
 
@@ -289,7 +420,9 @@ extern "C" int llama_beam_select(const float* logits, int groups, int beams, int
     a.tokens = tokens;
     a.best = out_scores;
     cudaStream_t s = (cudaStream_t)stream;
-    if (launch_pdl(k_beam_scan, dim3(a.splits, groups * beams), dim3(kScanThreads), 0, s, a) != cudaSuccess)
+    const bool vec = vocab % 4 == 0 && ((uintptr_t)logits & 15) == 0;
+    if (launch_pdl(vec ? k_beam_scan<true> : k_beam_scan<false>, dim3(a.splits, groups * beams), dim3(kScanThreads), 0, s,
+                   a) != cudaSuccess)
         return LLAMA_ERR_CUDA;
     if (launch_pdl(k_beam_merge, dim3(groups), dim3(kMergeThreads), 0, s, a) != cudaSuccess) return LLAMA_ERR_CUDA;
     return LLAMA_OK;
