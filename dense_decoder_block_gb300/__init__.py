@@ -23,6 +23,8 @@ from ._native import (LLAMA_BF16, LLAMA_F32, LLAMA_OK, LLAMA_ERR_INVALID_ARG, LL
                       LLAMA_ERR_NO_PAGES, llama_block_dims, llama_block_weights, llama_kv_cache, llama_paged_cache,
                       llama_rope_scaling)
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 __all__ = [
     "LlamaBlock", "LlamaError", "KVCache", "lib", "llama_block_create", "llama_block_create_scaled",
     "llama_block_destroy",
@@ -78,8 +80,9 @@ def _ptr(t):
 
 
 def _stream(stream: Optional[torch.cuda.Stream] = None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    # the raw handle of the current stream: a torch.cuda.Stream object would take longer
+    # to build (3 us) than a launch
+    return stream.cuda_stream if stream is not None else _raw_stream(torch.cuda.current_device())
 
 
 def _dtype_code(dt: torch.dtype) -> int:
@@ -280,7 +283,7 @@ def _arg(t, name: str, dtype: torch.dtype, least: int, device=None):
     on `device` (default: the current one)."""
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if not t.is_cuda or t.get_device() != (torch.cuda.current_device() if device is None else device):
+    if t.get_device() != (torch.cuda.current_device() if device is None else device):   # -1 on the host
         raise ValueError(f"{name} must live on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
