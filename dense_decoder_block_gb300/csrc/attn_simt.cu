@@ -15,11 +15,13 @@
 // in the same order with the same function, so a decode row is bit-identical
 // to the prefill row at the same position.  Keys past the query's position are
 // neither scored nor loaded.
+#include <algorithm>
 #include <cfloat>
 
 #include "attn_fold.cuh"
 #include "internal.h"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace llama {
 
@@ -298,6 +300,7 @@ struct PagedK {
     AttnK a;
     PageTable t;
     int pos_off;   // see paged_keys
+    float2* part_ml;   // (m, l) of the partials (attn_paged_ml); a.partial: [b][head][chunk][DH]
 };
 
 template <typename T, int DH>
@@ -348,33 +351,172 @@ __global__ void __launch_bounds__(kThreads) k_attn_paged_chunks(const PagedK p) 
     for (int r = warp; r < n_rep; r += kWarps) {
         float m, l, o[DPL];
         chunk_partial<T, DH>(qs + r * DH, Ks, Vs, jmax, a.scale_log2, m, l, o);
-        float* dst = a.partial + ((((size_t)b * a.n_kv_heads + g) * a.n_chunks + c) * n_rep + r) * part_stride(DH);
+        const size_t slot = ((size_t)b * a.n_heads + g * n_rep + r) * a.n_chunks + c;
 #pragma unroll
-        for (int e = 0; e < DPL; ++e) dst[lane * DPL + e] = o[e];
-        if (lane == 0) {
-            dst[DH] = m;
-            dst[DH + 1] = l;
-        }
+        for (int e = 0; e < DPL; ++e) a.partial[slot * DH + lane * DPL + e] = o[e];
+        if (lane == 0) p.part_ml[slot] = make_float2(m, l);
     }
 }
 
+// The combine of a paged call: a CTA per query row, whose chunks are folded in ascending
+// order with the formula of attn_fold.cuh, bit for bit -- for any length.  A row's partials
+// are contiguous ([chunk][DH], and [chunk] (m, l) apart), so a stage of 32 chunks arrives by
+// one bulk copy, a ring of stages ahead, from a warp of its own.  The fold is a chain of one
+// multiply-add per chunk and column once each chunk's two scales are known, and those need
+// only the running maxima: the folding warps take them first, for up to kCombBlock chunks,
+// from a prefix maximum.  A lane folds two columns: a warp alone on its scheduler is bound
+// by its instructions and shared-memory reads per chunk (16 cycles; with one column a lane
+// and four warps 24, with packed two-column arithmetic 26).
+constexpr int kCombStage = 32;       // chunks per stage
+constexpr int kCombStages = 8;       // at most
+constexpr int kCombBlock = 1024;     // chunks whose scales are held at a time
+constexpr int comb_threads(int dh) { return dh >= 64 ? dh / 2 : 32; }   // that fold
+
 template <typename T, int DH>
-__global__ void __launch_bounds__(32) k_attn_paged_combine(const PagedK p) {
+__global__ void __launch_bounds__(comb_threads(DH) + 32) k_attn_paged_combine(const PagedK p, int n_stages, int n_scales) {
+    constexpr int kThr = DH >= 64 ? DH / 2 : 32, kCol = DH / kThr, kPer = kCombBlock / kThr;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    __shared__ float s_max[kThr / 32];
+    __shared__ uint64_t s_full[kCombStages], s_empty[kCombStages];
     const AttnK& a = p.a;
-    const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x;
-    ptx_wait();
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float* ring = reinterpret_cast<float*>(smem_raw);   // [stage][chunk][DH]
+    // per chunk: scale of the past, of the chunk, l times the latter -- an array each, read four
+    // chunks at a time
+    float* scale = ring + (size_t)n_stages * kCombStage * DH;
+    // lengths are set before the step, never by the kernels this one overlaps
     bool bad;
     const int keys = paged_keys(a.pos_seq[b], p.pos_off, a.max_pos, bad);
-    const int n_rep = a.n_heads / a.n_kv_heads;
-    const int g = h / n_rep, r = h % n_rep;
-    T* dst = reinterpret_cast<T*>(a.o) + (size_t)b * a.n_heads * DH + (size_t)h * DH;
+    if (tid == 0) {
+        for (int i = 0; i < n_stages; ++i) {
+            ptx::mbar_init(&s_full[i], 1);
+            ptx::mbar_init(&s_empty[i], kThr / 32);
+        }
+        ptx::fence_mbar_init();
+        ptx_launch_dependents();
+    }
+    __syncthreads();
+    ptx_wait();
+    T* dst = reinterpret_cast<T*>(a.o) + ((size_t)b * a.n_heads + h) * DH + tid * kCol;
     if (keys == 0) {   // no key to attend: a row of zeros
+        if (warp < kThr / 32)
 #pragma unroll
-        for (int e = 0; e < DH / 32; ++e) from_f(dst + lane * (DH / 32) + e, 0.f);
+            for (int e = 0; e < kCol; ++e) from_f(dst + e, 0.f);
         return;
     }
-    const float* base = a.partial + (((size_t)b * a.n_kv_heads + g) * a.n_chunks * n_rep + r) * part_stride(DH);
-    fold_row<T, DH>(base, (size_t)n_rep * part_stride(DH), (keys - 1) / kAttnChunk + 1, lane, dst);
+    const int n_chunks = (keys - 1) / kAttnChunk + 1;
+    const size_t row = ((size_t)b * a.n_heads + h) * a.n_chunks;   // (KV head, query row of its group) is the head
+    if (warp == kThr / 32) {
+        if (lane == 0) {
+            const float* part = a.partial + row * DH;
+            const int stages = (n_chunks + kCombStage - 1) / kCombStage;
+            int issued = 0;
+            for (; issued < stages; ++issued) {
+                const int at = issued % n_stages, n = min(kCombStage, n_chunks - issued * kCombStage);
+                if (issued >= n_stages && !ptx::mbar_wait(&s_empty[at], (issued / n_stages - 1) & 1, a.err)) break;
+                ptx::mbar_arrive_expect_tx(&s_full[at], n * DH * 4);
+                ptx::bulk_load(ring + (size_t)at * kCombStage * DH, part + (size_t)issued * kCombStage * DH, n * DH * 4,
+                               &s_full[at]);
+            }
+            // no copy may still be landing when the CTA leaves (all have landed unless a wait gave up)
+            for (int i = max(0, issued - n_stages); i < issued; ++i)
+                ptx::mbar_wait_drain(&s_full[i % n_stages], (i / n_stages) & 1);
+        }
+        return;
+    }
+    const float2* part_ml = p.part_ml + row;
+    // -0 + x == x for every x: the first chunk's scales (0, 1) give its partial itself
+    float M = -INFINITY, L = -0.f, O[2] = {-0.f, -0.f};
+    bool ok = true;
+    int at = 0, turn = 0;   // place in the ring, its parity
+    for (int block = 0; block < n_chunks; block += kCombBlock) {
+        const int nb = min(kCombBlock, n_chunks - block), per = (nb + kThr - 1) / kThr;
+        // this thread's chunks: block + tid * per + i, i < per
+        float m[kPer], l[kPer], most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int c = tid * per + i;
+            m[i] = -INFINITY;
+            if (i < per && c < nb) {
+                const float2 ml = __ldcg(part_ml + block + c);
+                m[i] = ml.x;
+                l[i] = ml.y;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) most = fmaxf(most, m[i]);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float v = __shfl_up_sync(kFull, most, o);
+            if (lane >= o) most = fmaxf(most, v);
+        }
+        ptx::named_bar_sync(1, kThr);   // the maxima and scales of the block before were read
+        if (lane == 31) s_max[warp] = most;
+        ptx::named_bar_sync(1, kThr);
+        float now = __shfl_up_sync(kFull, most, 1);
+        if (lane == 0) now = -INFINITY;
+        now = fmaxf(M, now);
+#pragma unroll
+        for (int w = 0; w < kThr / 32; ++w) {
+            if (w < warp) now = fmaxf(now, s_max[w]);
+            M = fmaxf(M, s_max[w]);
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int c = tid * per + i;
+            if (i < per && c < nb) {
+                const bool first = block + c == 0;
+                const float next = fmaxf(now, m[i]);
+                const float sa = first ? 0.f : exp2f(__fsub_rn(now, next)), sb = first ? 1.f : exp2f(__fsub_rn(m[i], next));
+                scale[c] = sa;
+                scale[n_scales + c] = sb;
+                scale[2 * n_scales + c] = __fmul_rn(l[i], sb);
+                now = next;
+            }
+        }
+        ptx::named_bar_sync(1, kThr);
+        for (int c0 = 0; c0 < nb; c0 += kCombStage) {
+            const int n = min(kCombStage, nb - c0);
+            ok = ok && ptx::mbar_wait(&s_full[at], turn, a.err);
+            const float* st = ring + (size_t)at * kCombStage * DH + tid * kCol;
+            const float* k = scale + c0;
+            auto step = [&](float ka, float kb, float kl, const float* x) {
+                L = __fmaf_rn(L, ka, kl);
+                if constexpr (kCol == 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(x);
+                    O[0] = __fmaf_rn(O[0], ka, __fmul_rn(v.x, kb));
+                    O[1] = __fmaf_rn(O[1], ka, __fmul_rn(v.y, kb));
+                } else {
+                    O[0] = __fmaf_rn(O[0], ka, __fmul_rn(x[0], kb));
+                }
+            };
+            if (n == kCombStage) {
+#pragma unroll
+                for (int c = 0; c < kCombStage; c += 4) {
+                    const float4 ka = *reinterpret_cast<const float4*>(k + c);
+                    const float4 kb = *reinterpret_cast<const float4*>(k + n_scales + c);
+                    const float4 kl = *reinterpret_cast<const float4*>(k + 2 * n_scales + c);
+                    step(ka.x, kb.x, kl.x, st + c * DH);
+                    step(ka.y, kb.y, kl.y, st + (c + 1) * DH);
+                    step(ka.z, kb.z, kl.z, st + (c + 2) * DH);
+                    step(ka.w, kb.w, kl.w, st + (c + 3) * DH);
+                }
+            } else {
+#pragma unroll 4
+                for (int c = 0; c < n; ++c) step(k[c], k[n_scales + c], k[2 * n_scales + c], st + c * DH);
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s_empty[at]);
+            if (++at == n_stages) {
+                at = 0;
+                turn ^= 1;
+            }
+        }
+    }
+    if (!ok) return;   // a wait gave up (recorded)
+    const float inv = __frcp_rn(L);
+#pragma unroll
+    for (int e = 0; e < kCol; ++e) from_f(dst + e, __fmul_rn(O[e], inv));
 }
 
 template <typename T, int DH>
@@ -450,15 +592,29 @@ PagedK make_paged(const AttnArgs& a) {
     p.a = make_k(a);
     p.t = a.pages;
     p.pos_off = a.pos_off;
+    p.part_ml = attn_paged_ml(a.partial, a.batch, a.n_heads, a.n_chunks, a.head_dim);
     return p;
 }
 
 template <typename T, int DH>
 cudaError_t paged_combine_impl(const AttnArgs& a, cudaStream_t s) {
     auto kern = k_attn_paged_combine<T, DH>;
-    cudaError_t r = kernel_setup_once((const void*)kern, setup_prefer_shared);
+    constexpr int kStage = kCombStage * DH * (int)sizeof(float), kScale = 3 * (int)sizeof(float);
+    cudaError_t r = kernel_setup_once((const void*)kern, [](const void* k) {
+        cudaError_t e = setup_prefer_shared(k);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       kCombStages * kStage + kCombBlock * kScale);
+    });
     if (r != cudaSuccess) return r;
-    return launch_pdl(kern, dim3(a.n_heads, a.batch), dim3(32), 0, s, make_paged(a));
+    // A ring for the longest row there can be.  One or two stages hold most decode lengths,
+    // and the more CTAs an SM takes the more rows are in flight; beyond that half a ring, or
+    // all of it where every row has an SM to itself.
+    const int need = (a.n_chunks + kCombStage - 1) / kCombStage;
+    const int most = (long)a.n_heads * a.batch <= device_sm_count() ? kCombStages : kCombStages / 2;
+    const int n_stages = std::min(need, most), scales = std::min(need * kCombStage, kCombBlock);
+    return launch_pdl(kern, dim3(a.n_heads, a.batch), dim3(comb_threads(DH) + 32), n_stages * kStage + scales * kScale, s,
+                      make_paged(a), n_stages, scales);
 }
 
 template <typename T, int DH>

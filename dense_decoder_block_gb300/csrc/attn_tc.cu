@@ -54,7 +54,8 @@ struct TcArgs {
     float scale_log2;
     const bf16* q;       // decode: [B, Hq * 128]
     bf16* o;             // prefill: [B * T, Hq * 128]
-    float* partial;      // decode: [B, Hkv, n_chunks, n_rep, kPartStride]
+    float* partial;      // decode: [B, Hkv, n_chunks, n_rep, kPartStride]; paged: [B, Hq, n_chunks, 128]
+    float2* part_ml;     // paged decode: (m, l) of the partials, [B, Hq, n_chunks]
     int n_chunks;        // decode: chunk slots per (sequence, KV head)
     int chunks_per_cta;  // decode
     int tq;              // prefill: tokens per query tile
@@ -1377,15 +1378,20 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
             // the slot is free again: prepare it for this warp's next unit before storing
             if (i + kDecSlots < n_iter) prepare(i + kDecSlots);
             if (valid) {
-                float* dst =
-                    a.partial + ((((size_t)d.b * a.n_kv_heads + d.g) * a.n_chunks + d.c) * n_rep + r) * kPartStride;
+                const size_t row = ((size_t)d.b * a.n_heads + d.g * n_rep + r) * a.n_chunks + d.c;   // paged
+                float* dst = PAGED ? a.partial + row * 128
+                                   : a.partial + ((((size_t)d.b * a.n_kv_heads + d.g) * a.n_chunks + d.c) * n_rep + r) * kPartStride;
 #pragma unroll
                 for (int q4 = 0; q4 < 8; ++q4)
                     *reinterpret_cast<float4*>(dst + q * 32 + 4 * q4) =
                         make_float4(ov[4 * q4], ov[4 * q4 + 1], ov[4 * q4 + 2], ov[4 * q4 + 3]);
                 if (q == 0) {
-                    dst[128] = m;
-                    dst[129] = l;
+                    if constexpr (PAGED) {
+                        a.part_ml[row] = make_float2(m, l);
+                    } else {
+                        dst[128] = m;
+                        dst[129] = l;
+                    }
                 }
             }
         }
@@ -1550,14 +1556,14 @@ cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s) {
     });
     if (r != cudaSuccess) return r;
     // a launch maps its units from at most kSeqPosMax lengths
-    const int n_rep = a.n_heads / a.n_kv_heads;
     for (int b0 = 0; b0 < a.batch; b0 += kSeqPosMax) {
         TcArgs k = make_args(a);
         k.batch = std::min(a.batch - b0, kSeqPosMax);
         k.pos_seq += b0;
         k.pages.table += (size_t)b0 * a.pages.stride;
         k.q += (size_t)b0 * a.n_heads * 128;
-        k.partial += (size_t)b0 * a.n_kv_heads * a.n_chunks * n_rep * kPartStride;
+        k.part_ml = attn_paged_ml(a.partial, a.batch, a.n_heads, a.n_chunks, 128) + (size_t)b0 * a.n_heads * a.n_chunks;
+        k.partial += (size_t)b0 * a.n_heads * a.n_chunks * 128;
         const long max_units = (long)k.batch * a.n_kv_heads * a.n_chunks;
         const dim3 grid((unsigned)std::min<long>(max_units, device_sm_count()));
         r = launch_pdl(k_attn_tc_dec<true>, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);

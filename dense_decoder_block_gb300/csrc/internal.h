@@ -136,6 +136,12 @@ cudaError_t launch_attention_prefill(const AttnArgs& a, cudaStream_t s);   // CU
 cudaError_t launch_attention_decode(const AttnArgs& a, cudaStream_t s);    // CUDA cores, + combine
 // Ascending fold of the decode chunk partials into o (shared by both decode kernels).
 cudaError_t launch_attention_combine(const AttnArgs& a, cudaStream_t s);
+// A paged call's chunk partials: [batch][n_heads][n_chunks][head_dim] fp32 and behind them the
+// (m, l) of each -- a row's partials in one piece, for the combine's bulk copies.  Together
+// no more than attn_decode_partial_bytes.
+inline float2* attn_paged_ml(float* partial, int batch, int n_heads, int n_chunks, int head_dim) {
+    return reinterpret_cast<float2*>(partial + (size_t)batch * n_heads * n_chunks * head_dim);
+}
 // Decode attention over a paged cache (pos_seq and pages set): CUDA cores, + combine.
 // A sequence without keys, or with a position out of range (recorded), gets a row of zeros.
 cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s);
