@@ -16,7 +16,9 @@ from typing import Callable, Dict, List, Optional, Sequence, Tuple
 
 import torch
 
-from . import (KVCache, LlamaBlock, llama_embed, llama_lmhead_argmax, llama_lmhead_workspace_bytes)
+from . import (KVCache, LlamaBlock, PagedCache, PagedCacheList, llama_beam_reorder, llama_beam_select,
+               llama_beam_select_workspace_bytes, llama_embed, llama_lmhead_argmax, llama_lmhead_workspace_bytes,
+               llama_paged_plan, llama_paged_release, llama_paged_store)
 
 
 class LlamaStack:
@@ -109,3 +111,143 @@ class LlamaStack:
             if rc:
                 return rc
         return 0
+
+
+class BeamSearch:
+    """Beam search on a stack: `beams` continuations of each of the stack's requests, at most `max_new` tokens,
+    on a paged cache.  A request's beams share the full pages of their common past; each owns the pages from its
+    first unfilled one on.  Row g * beams + k of every tensor is beam k of request g; groups * beams <= 32.
+
+        bs = BeamSearch(stack, beams=4, max_new=64, eos=2)
+        bs.begin(ids)                  # prompts [requests, T]: prefill, pages, the first tokens
+        for _ in range(63):
+            bs.step()                  # one more token per beam (capturable in a CUDA graph)
+        tokens, scores = bs.sequences()
+        bs.end()                       # the pages go back to the pool
+
+    eos < 0: no beam ends.  A beam that ended keeps its score and repeats eos."""
+
+    def __init__(self, stack: LlamaStack, beams: int, max_new: int, eos: int = -1, page_size: int = 16):
+        dims, dev, dt = stack.dims, stack.w_embed.device, stack.w_embed.dtype
+        groups = stack.batch
+        rows = groups * beams
+        if beams < 1 or rows > 32:
+            raise ValueError("requests x beams must be 1 to 32 rows")
+        if max_new < 1 or max_new >= stack.max_seq:
+            raise ValueError("max_new must leave room for a prompt in the stack's max_seq")
+        self.stack, self.beams, self.groups, self.rows = stack, beams, groups, rows
+        self.max_new, self.eos, self.page_size = max_new, eos, page_size
+        columns = -(-stack.max_seq // page_size)
+        # a request's prompt once and, per beam, the pages of max_new tokens and the unfilled one
+        self.n_pages = groups * (columns + beams * (-(-max_new // page_size) + 1))
+        shape = (self.n_pages, dims.n_kv_heads, page_size, dims.head_dim)
+        self.caches = PagedCacheList([PagedCache(torch.zeros(shape, dtype=dt, device=dev),
+                                                 torch.zeros(shape, dtype=dt, device=dev)) for _ in stack.blocks])
+
+        def i32(*size):
+            return torch.zeros(size, dtype=torch.int32, device=dev)
+
+        self.free = torch.arange(self.n_pages, dtype=torch.int32, device=dev)
+        self.pool = torch.tensor([self.n_pages, 0], dtype=torch.int32, device=dev)
+        self.table, self.home = i32(rows, columns), i32(rows, columns)   # home: the table as it was planned
+        self.start, self.count, self.pos = i32(rows), i32(rows), i32(rows)
+        self.err = i32(1)
+        self.logits = torch.empty(rows, stack.vocab, dtype=torch.float32, device=dev)
+        self.scores = torch.empty(rows, dtype=torch.float32, device=dev)
+        self.parents, self.tokens, self.greedy = i32(rows), i32(rows), i32(rows)
+        self.all_parents, self.all_tokens = i32(max_new, rows), i32(max_new, rows)
+        self.n = torch.zeros(1, dtype=torch.int64, device=dev)           # tokens chosen so far, on the device
+        self.steps = 0                                                   # ... and on the host (begin and step calls)
+        self.ws = torch.empty(stack.blocks[0].workspace_bytes(rows, 1), dtype=torch.uint8, device=dev)
+        self.head_ws = torch.empty(llama_lmhead_workspace_bytes(rows, dims.d_model, stack.vocab), dtype=torch.uint8,
+                                   device=dev)
+        self.select_ws = torch.empty(llama_beam_select_workspace_bytes(groups, beams, stack.vocab, beams),
+                                     dtype=torch.uint8, device=dev)
+        self.act = [torch.empty(rows, 1, dims.d_model, dtype=dt, device=dev) for _ in range(2)]
+        self.active = False
+
+    def _choose(self, last, stream) -> None:
+        # the best continuations; the states of the beams follow
+        llama_beam_select(self.logits, self.scores, self.beams, self.beams, self.parents, self.tokens, self.scores,
+                          self.select_ws, last=last, eos=self.eos, stream=stream)
+        with LlamaStack._on(stream):
+            self.all_parents.index_copy_(0, self.n, self.parents[None])
+            self.all_tokens.index_copy_(0, self.n, self.tokens[None])
+            self.n.add_(1)
+        llama_beam_reorder(self.parents, self.beams, self.pos, self.table, self.caches, err_dev=self.err, stream=stream)
+
+    def begin(self, ids: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """ids [requests, T] int32 on the device: prefill, pages for the prompts and max_new tokens, and the first
+        token of every beam."""
+        if self.active:
+            raise RuntimeError("end() the running search first")
+        st, ps, K = self.stack, self.page_size, self.beams
+        T = ids.shape[1]
+        if T + self.max_new > st.max_seq:
+            raise ValueError("prompt and max_new exceed the stack's max_seq")
+        st.prefill(ids, stream)
+        with LlamaStack._on(stream):
+            # beam 0 of a request holds the whole prompt, the others its unfilled page on
+            full = T // ps * ps
+            first = torch.arange(self.rows, device=ids.device) % K == 0
+            self.start.copy_(torch.where(first, 0, full))
+            self.count.copy_(torch.where(first, T + self.max_new, T - full + self.max_new))
+            self.pos.fill_(T)
+            slots = torch.empty(self.rows, T + self.max_new, dtype=torch.int32, device=ids.device)
+        llama_paged_plan(self.start, self.count, ps, self.n_pages, self.free, self.pool, self.table, slots,
+                         err_dev=self.err, stream=stream)
+        with LlamaStack._on(stream):
+            self.home.copy_(self.table)
+            prompt_slots = slots.view(self.groups, K, -1)[:, 0, :T].contiguous()
+        for cache, paged in zip(st.caches, self.caches.caches):
+            llama_paged_store(cache.k, cache.v, prompt_slots, paged, err_dev=self.err, stream=stream)
+        with LlamaStack._on(stream):
+            self.logits.view(self.groups, K, -1)[:, 0].copy_(st.logits)   # the other rows are not read
+            self.scores.copy_(torch.where(first, 0.0, float("-inf")))
+            self.n.zero_()
+            slots.record_stream(torch.cuda.current_stream())
+            prompt_slots.record_stream(torch.cuda.current_stream())
+        self.steps = 1
+        self.active = True
+        self._choose(None, stream)
+
+    def step(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """One more token for every beam.  Reads nothing on the host: a captured graph of it can be replayed, as
+        long as replays and calls together stay below max_new tokens."""
+        if not self.active:
+            raise RuntimeError("begin() first")
+        if self.steps >= self.max_new:
+            raise RuntimeError("max_new tokens were chosen")
+        st = self.stack
+        x, y = self.act
+        llama_embed(self.tokens, self.rows, st.w_embed, st.vocab, st.dims.d_model, x, self.err, stream)
+        for blk, cache in zip(st.blocks, self.caches.caches):
+            blk.decode_paged(x, cache, self.table, self.pos, y, self.ws, stream)
+            x, y = y, x
+        llama_lmhead_argmax(x, self.rows, st.dims.d_model, st.g_final, st.w_out, st.vocab, st.dims.d_model, st.dims.eps,
+                            self.greedy, self.logits, self.head_ws, self.head_ws.numel(), stream)
+        with LlamaStack._on(stream):
+            self.pos.add_(1)
+        self.steps += 1
+        self._choose(self.tokens if self.eos >= 0 else None, stream)
+
+    def sequences(self):
+        """(tokens [requests, beams, chosen], scores [requests, beams]), best first."""
+        n = int(self.n.item())
+        row = torch.arange(self.rows, device=self.pos.device)
+        out = torch.empty(self.rows, n, dtype=torch.int32, device=self.pos.device)
+        for t in range(n - 1, -1, -1):
+            out[:, t] = self.all_tokens[t][row]
+            row = self.all_parents[t][row].long()
+        return out.view(self.groups, self.beams, n), self.scores.view(self.groups, self.beams).clone()
+
+    def end(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Give the pages back."""
+        if self.active:
+            llama_paged_release(self.start, self.count, self.page_size, self.n_pages, self.free, self.pool, self.home,
+                                err_dev=self.err, stream=stream)
+            self.active = False
+
+    def poll_error(self) -> int:
+        rc = self.stack.poll_error()
+        return rc if rc else int(self.err.item())

@@ -433,7 +433,8 @@ int llama_block_decode_paged(llama_block blk, const void* x, int batch, const ll
  * a beam with last[k] == eos has ended: its only continuation is eos, at scores[k]
  * (last may be NULL: no beam ends).  Outputs [groups, n_out] in decreasing score,
  * equal scores by increasing beam and then token: parents (row of the beam, in
- * 0 .. groups * beams - 1), tokens, out_scores.  Candidates are compared in fp64.
+ * 0 .. groups * beams - 1), tokens, out_scores.  With n_out == beams, out_scores may
+ * be scores and tokens may be last.  Candidates are compared in fp64.
  * Logits must be finite or -inf (probability 0), scores too; continuations of score
  * -inf are listed only when the others are fewer than n_out.  1 <= beams <= 32,
  * 1 <= n_out <= 64, n_out <= vocab <= 2^20, groups * beams <= 65535; otherwise
