@@ -599,9 +599,8 @@ extern "C" int llama_block_decode_paged(llama_block b, const void* x, int batch,
     if (!b) return LLAMA_ERR_INVALID_ARG;
     if (batch < 0) return fail(b, LLAMA_ERR_INVALID_ARG, "negative batch");
     const auto& d = b->dims;
-    // as llama_block_decode_seqpos
-    if (d.dtype != LLAMA_BF16 || !attention_tc_supported(d.n_heads, d.n_kv_heads, d.head_dim) ||
-        d.n_heads / d.n_kv_heads > 8 || batch > 32)
+    // as llama_block_decode_seqpos, any group that the tensor-core attention takes
+    if (d.dtype != LLAMA_BF16 || !attention_tc_supported(d.n_heads, d.n_kv_heads, d.head_dim) || batch > 32)
         return fail(b, LLAMA_ERR_UNSUPPORTED_DIMS, "per-sequence positions need the bf16 weight-streaming decode path");
     const int rc = paged_cache_check(kv, d.n_kv_heads, d.head_dim, d.dtype);
     if (rc != LLAMA_OK) return fail(b, rc, "paged cache: null, misaligned or of an unsupported geometry");

@@ -4,6 +4,8 @@
 // block table (attn_simt.cu, attn_tc.cu): 128-key chunks spread over the SMs, each
 // leaving (m, l, o), and a combine that folds a row's chunks in ascending order -- so
 // the result does not depend on the batch, on the pages or on the split.
+#include <algorithm>
+
 #include "internal.h"
 
 using namespace llama;
@@ -33,6 +35,9 @@ extern "C" int llama_paged_attention(const void* q, int batch, int n_heads, int 
     const int rc = paged_cache_check(kv, n_kv_heads, head_dim, dtype);
     if (rc != LLAMA_OK) return rc;
     if (batch == 0) return LLAMA_OK;
+    // the kernels count (sequence, KV head, chunk) units of up to 1024 sequences, 8 query heads
+    // each, in 32 bits
+    if ((long long)std::min(batch, 1024) * n_heads * chunks_of(max_len) > INT32_MAX) return LLAMA_ERR_UNSUPPORTED_DIMS;
     if (!q || !o || !table || !lens || ((uintptr_t)q & 15) || ((uintptr_t)o & 15)) return LLAMA_ERR_INVALID_ARG;
     if (!ws || ws_bytes < llama_paged_attention_workspace_bytes(batch, n_heads, n_kv_heads, head_dim, max_len))
         return LLAMA_ERR_WORKSPACE;

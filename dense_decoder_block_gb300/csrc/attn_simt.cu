@@ -74,36 +74,38 @@ __device__ __forceinline__ void load_chunk(T* Ks, T* Vs, const T* kc, const T* v
     cp_async_wait_all();
 }
 
-// One warp: the partial of one query row (fp32 in smem) over one chunk.
-// jmax = last key index inside the chunk this row may see (0..127).
+// q . k of one key (a row of the chunk)
 template <typename T, int DH>
-__device__ __forceinline__ void chunk_partial(const float* q, const T* Ks, const T* Vs, int jmax, float scale_log2,
-                                              float& m_out, float& l_out, float (&o)[DH / 32]) {
+__device__ __forceinline__ float key_dot(const float* q, const T* kr) {
+    constexpr int VEC = Tile<T, DH>::VEC;
+    float acc = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < DH; d += VEC) {
+        T kv[VEC];
+        *reinterpret_cast<uint4*>(kv) = *reinterpret_cast<const uint4*>(kr + d);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc = __fmaf_rn(q[d + e], to_f(kv[e]), acc);
+    }
+    return acc;
+}
+
+// One warp: the weights of one query row (fp32 in smem) over one chunk, lane's keys
+// lane + 32 i, with their maximum and sum.  jmax = last key index inside the chunk this
+// row may see (0..127).
+template <typename T, int DH>
+__device__ __forceinline__ void chunk_weights(const float* q, const T* Ks, int jmax, float scale_log2, float& m_out,
+                                              float& l_out, float (&p)[4]) {
     using TL = Tile<T, DH>;
     const int lane = threadIdx.x & 31;
     float s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int j = lane + 32 * i;
-        if (j <= jmax) {
-            const T* kr = Ks + j * TL::LD;
-            float acc = 0.f;
-#pragma unroll 4
-            for (int d = 0; d < DH; d += TL::VEC) {
-                T kv[TL::VEC];
-                *reinterpret_cast<uint4*>(kv) = *reinterpret_cast<const uint4*>(kr + d);
-#pragma unroll
-                for (int e = 0; e < TL::VEC; ++e) acc = __fmaf_rn(q[d + e], to_f(kv[e]), acc);
-            }
-            s[i] = __fmul_rn(acc, scale_log2);
-        } else {
-            s[i] = -INFINITY;
-        }
+        s[i] = j <= jmax ? __fmul_rn(key_dot<T, DH>(q, Ks + j * TL::LD), scale_log2) : -INFINITY;
     }
     float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
-    float p[4];
     float l = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -112,7 +114,15 @@ __device__ __forceinline__ void chunk_partial(const float* q, const T* Ks, const
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) l = __fadd_rn(l, __shfl_xor_sync(kFull, l, off));
-    l = __shfl_sync(kFull, l, 0);
+    m_out = mx;
+    l_out = __shfl_sync(kFull, l, 0);
+}
+
+// ... and the weights' average of V, not normalised: lane owns dims lane * DPL ...
+template <typename T, int DH>
+__device__ __forceinline__ void chunk_average(const T* Vs, int jmax, const float (&p)[4], float (&o)[DH / 32]) {
+    using TL = Tile<T, DH>;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int e = 0; e < TL::DPL; ++e) o[e] = 0.f;
 #pragma unroll
@@ -128,8 +138,15 @@ __device__ __forceinline__ void chunk_partial(const float* q, const T* Ks, const
             for (int e = 0; e < TL::DPL; ++e) o[e] = __fmaf_rn(pj, to_f(vr[e]), o[e]);
         }
     }
-    m_out = mx;
-    l_out = l;
+}
+
+// One warp: the partial of one query row over one chunk.
+template <typename T, int DH>
+__device__ __forceinline__ void chunk_partial(const float* q, const T* Ks, const T* Vs, int jmax, float scale_log2,
+                                              float& m_out, float& l_out, float (&o)[DH / 32]) {
+    float p[4];
+    chunk_weights<T, DH>(q, Ks, jmax, scale_log2, m_out, l_out, p);
+    chunk_average<T, DH>(Vs, jmax, p, o);
 }
 
 struct AttnK {
@@ -293,68 +310,215 @@ __global__ void __launch_bounds__(32) k_attn_decode_combine(const AttnK a) {
 // ----------------------------------------------------------------------------- decode on a paged cache
 // The same chunk partial over keys whose rows are found through the block table: a
 // chunk of 128 keys lies in 128 / page_size pages (one, from 128-key pages on).  Pages
-// behind a sequence's last key are not looked up.  One CTA per (chunk, KV head,
-// sequence); for the shapes the tensor-core kernel does not take (fp32, groups that do
-// not divide 128, more than 8 query heads per KV head).
+// behind a sequence's last key are not looked up.  For the shapes the tensor-core kernel
+// does not take: fp32, and groups of query heads that do not divide 128.
+//
+// Persistent: a CTA walks a contiguous range of the units (sequence, KV head, chunk),
+// counted on the device from the lengths, so that a bound far above them costs nothing.
+// K and V have a buffer each: the next unit's K is copied while this one's weights average
+// V, its V while the next scores are taken.
 struct PagedK {
     AttnK a;
     PageTable t;
     int pos_off;   // see paged_keys
     float2* part_ml;   // (m, l) of the partials (attn_paged_ml); a.partial: [b][head][chunk][DH]
 };
+constexpr int kPagedSeqs = 1024;   // sequences per launch of the chunk kernel
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(kThreads) k_attn_paged_chunks(const PagedK p) {
+// WPR: warps per query row.  Small groups leave warps without a row, so a row's keys (of the
+// scores) and columns (of the average) are then shared by two or four warps -- each score,
+// weight and column is the same chain of operations, and a lane's four weights are added in
+// the same order, so the bits stay those of chunk_partial.
+template <typename T, int DH, int WPR>
+__global__ void __launch_bounds__(kThreads, 2) k_attn_paged_chunks(const PagedK p) {
     using TL = Tile<T, DH>;
     constexpr int DPL = TL::DPL;
     constexpr int VPR = DH / TL::VEC;
+    constexpr int RPW = WPR == 1 ? kRowsMax / kWarps : 1;   // rows per warp (WPR > 1: at most kWarps / WPR rows)
+    constexpr int kCols = (DPL + WPR - 1) / WPR;            // columns lane + 32 k per lane, k = sub, sub + WPR, ...
+    __shared__ __align__(16) float s_p[WPR == 1 ? 1 : kWarps / WPR][kAttnChunk];
+    __shared__ float s_mx[kWarps];
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    __shared__ int s_page[kAttnChunk / 16];
+    __shared__ int s_pre[kPagedSeqs + 1], s_keys[kPagedSeqs];   // units before each sequence, per KV head; its keys
+    __shared__ int s_page[2][kAttnChunk / 16];
     T* Ks = reinterpret_cast<T*>(smem_raw);
     T* Vs = Ks + kAttnChunk * TL::LD;
     float* qs = reinterpret_cast<float*>(Vs + kAttnChunk * TL::LD);
     const AttnK& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_rep = a.n_heads / a.n_kv_heads;
+    const int shift = p.t.shift, ps = 1 << shift;
+    const int row = warp / WPR, sub = warp % WPR;   // WPR > 1
 
     ptx_wait();
-    const int c = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
-    const int n_rep = a.n_heads / a.n_kv_heads;
-    bool bad;
-    const int keys = paged_keys(a.pos_seq[b], p.pos_off, a.max_pos, bad);
-    if (bad && threadIdx.x == 0 && c == 0 && g == 0) record_error(a.err, LLAMA_ERR_POS_RANGE);
-    const int key0 = c * kAttnChunk;
-    if (key0 >= keys) return;
-    const int last = keys - 1;
-    const int shift = p.t.shift, ps = 1 << shift;
-    const int n_pages = (min(kAttnChunk, keys - key0) + ps - 1) >> shift;
-    if (threadIdx.x < n_pages) s_page[threadIdx.x] = page_of(p.t, b, (key0 >> shift) + threadIdx.x, a.err);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const T* q = reinterpret_cast<const T*>(a.q);
-    const size_t qld = (size_t)a.n_heads * DH;
-    for (int i = threadIdx.x; i < n_rep * DH; i += kThreads) {
-        const int r = i / DH, d = i % DH;
-        qs[i] = to_f(q[(size_t)b * qld + (size_t)(g * n_rep + r) * DH + d]);
-    }
-    __syncthreads();
-    const T* kc = reinterpret_cast<const T*>(a.kc);
-    const T* vc = reinterpret_cast<const T*>(a.vc);
-    for (int v = threadIdx.x; v < kAttnChunk * VPR; v += kThreads) {
-        const int j = v / VPR, col = (v % VPR) * TL::VEC;
-        const int key = key0 + j;
-        const int page = key <= last ? s_page[(key >> shift) - (key0 >> shift)] : -1;
-        const size_t row = page < 0 ? 0 : (((size_t)page * a.n_kv_heads + g) << shift) + (key & (ps - 1));
-        cp_async16(Ks + j * TL::LD + col, kc + row * DH + col, page >= 0);
-        cp_async16(Vs + j * TL::LD + col, vc + row * DH + col, page >= 0);
-    }
-    cp_async_wait_all();
-    __syncthreads();
-    const int jmax = min(kAttnChunk - 1, last - key0);
-    for (int r = warp; r < n_rep; r += kWarps) {
-        float m, l, o[DPL];
-        chunk_partial<T, DH>(qs + r * DH, Ks, Vs, jmax, a.scale_log2, m, l, o);
-        const size_t slot = ((size_t)b * a.n_heads + g * n_rep + r) * a.n_chunks + c;
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < a.batch; b0 += 32) {
+            const int b = b0 + lane;
+            bool bad = false;
+            const int keys = b < a.batch ? paged_keys(__ldcg(a.pos_seq + b), p.pos_off, a.max_pos, bad) : 0;
+            int nt = (keys + kAttnChunk - 1) / kAttnChunk;
+            if (b < a.batch) s_keys[b] = keys;
+            if (bad && blockIdx.x == 0) record_error(a.err, LLAMA_ERR_POS_RANGE);
 #pragma unroll
-        for (int e = 0; e < DPL; ++e) a.partial[slot * DH + lane * DPL + e] = o[e];
-        if (lane == 0) p.part_ml[slot] = make_float2(m, l);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(kFull, nt, o);
+                if (lane >= o) nt += v;
+            }
+            if (b < a.batch) s_pre[b + 1] = run + nt;
+            run += __shfl_sync(kFull, nt, 31);
+        }
+        if (lane == 0) s_pre[0] = 0;
+    }
+    __syncthreads();
+    const int n_units = s_pre[a.batch] * a.n_kv_heads;   // below 2^31: checked on the host from the bound
+    const int u_begin = (int)((long)n_units * blockIdx.x / gridDim.x), u_end = (int)((long)n_units * (blockIdx.x + 1) / gridDim.x);
+
+    struct Unit {
+        int b, g, c, keys;   // keys of the sequence
+    };
+    auto unit = [&](int u) {
+        Unit d;
+        int lo = 0, hi = a.batch - 1;   // the last sequence whose units start at or before u
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_pre[mid] * a.n_kv_heads <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        const int nt = s_pre[lo + 1] - s_pre[lo], r = u - s_pre[lo] * a.n_kv_heads;
+        d.b = lo;
+        d.g = r / nt;
+        d.c = r - d.g * nt;
+        d.keys = s_keys[lo];
+        return d;
+    };
+    // the page ids of a unit's chunk (one thread each), visible after the next barrier
+    auto lookup = [&](const Unit& d, int* pages) {
+        const int key0 = d.c * kAttnChunk, n = (min(kAttnChunk, d.keys - key0) + ps - 1) >> shift;
+        if (threadIdx.x < n) pages[threadIdx.x] = page_of(p.t, d.b, (key0 >> shift) + threadIdx.x, a.err);
+    };
+    auto copy = [&](const Unit& d, const int* pages, const void* cache, T* to) {
+        const int key0 = d.c * kAttnChunk;
+        for (int v = threadIdx.x; v < kAttnChunk * VPR; v += kThreads) {
+            const int j = v / VPR, col = (v % VPR) * TL::VEC;
+            const int key = key0 + j;
+            const int page = key < d.keys ? pages[(key >> shift) - (key0 >> shift)] : -1;
+            const size_t row = page < 0 ? 0 : (((size_t)page * a.n_kv_heads + d.g) << shift) + (key & (ps - 1));
+            cp_async16(to + j * TL::LD + col, reinterpret_cast<const T*>(cache) + row * DH + col, page >= 0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    if (u_begin >= u_end) return;
+    Unit d = unit(u_begin);
+    int turn = 0;   // of s_page
+    lookup(d, s_page[0]);
+    __syncthreads();
+    copy(d, s_page[0], a.kc, Ks);
+    copy(d, s_page[0], a.vc, Vs);
+    int q_of = -1;   // (sequence, KV head) whose query rows are in qs
+    for (int u = u_begin; u < u_end; ++u) {
+        const bool more = u + 1 < u_end;
+        Unit next = d;
+        if (more) {
+            next = unit(u + 1);
+            lookup(next, s_page[turn ^ 1]);
+        }
+        if (d.b * a.n_kv_heads + d.g != q_of) {
+            q_of = d.b * a.n_kv_heads + d.g;
+            const T* q = reinterpret_cast<const T*>(a.q) + ((size_t)d.b * a.n_heads + (size_t)d.g * n_rep) * DH;
+            for (int i = threadIdx.x; i < n_rep * DH; i += kThreads) qs[i] = to_f(q[i]);
+        }
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // K landed (this thread's part), V may not have
+        __syncthreads();
+        const int jmax = min(kAttnChunk - 1, d.keys - 1 - d.c * kAttnChunk);
+        float w[RPW][4], m[RPW], l[RPW];
+        if constexpr (WPR == 1) {
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const int r = warp + i * kWarps;
+                if (r < n_rep) chunk_weights<T, DH>(qs + r * DH, Ks, jmax, a.scale_log2, m[i], l[i], w[i]);
+            }
+        } else if (row < n_rep) {
+            float s[4 / WPR], mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4 / WPR; ++i) {
+                const int j = lane + 32 * (sub * (4 / WPR) + i);
+                s[i] = j <= jmax ? __fmul_rn(key_dot<T, DH>(qs + row * DH, Ks + j * TL::LD), a.scale_log2) : -INFINITY;
+                mx = fmaxf(mx, s[i]);
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
+            if (lane == 0) s_mx[warp] = mx;
+            ptx::named_bar_sync(1 + row, 32 * WPR);
+#pragma unroll
+            for (int i = 0; i < WPR; ++i) mx = fmaxf(mx, s_mx[row * WPR + i]);
+#pragma unroll
+            for (int i = 0; i < 4 / WPR; ++i) {
+                const int j = lane + 32 * (sub * (4 / WPR) + i);
+                s_p[row][j] = j <= jmax ? exp2f(__fsub_rn(s[i], mx)) : 0.f;
+            }
+            ptx::named_bar_sync(1 + row, 32 * WPR);
+            m[0] = mx;
+            l[0] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[0] = __fadd_rn(l[0], s_p[row][lane + 32 * i]);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) l[0] = __fadd_rn(l[0], __shfl_xor_sync(kFull, l[0], off));
+        }
+        __syncthreads();   // K was read
+        if (more) copy(next, s_page[turn ^ 1], a.kc, Ks);
+        else asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");   // V landed
+        __syncthreads();
+        if constexpr (WPR == 1) {
+#pragma unroll
+            for (int i = 0; i < RPW; ++i) {
+                const int r = warp + i * kWarps;
+                if (r >= n_rep) break;
+                float o[DPL];
+                chunk_average<T, DH>(Vs, jmax, w[i], o);
+                const size_t slot = ((size_t)d.b * a.n_heads + (size_t)d.g * n_rep + r) * a.n_chunks + d.c;
+#pragma unroll
+                for (int e = 0; e < DPL; ++e) a.partial[slot * DH + lane * DPL + e] = o[e];
+                if (lane == 0) p.part_ml[slot] = make_float2(m[i], l[i]);
+            }
+        } else if (row < n_rep && sub < DPL) {
+            float o[kCols];
+#pragma unroll
+            for (int e = 0; e < kCols; ++e) o[e] = 0.f;
+            const T* v = Vs + lane + 32 * sub;
+            const float* wt = s_p[row];
+            int j = 0;
+            for (; j + 7 <= jmax; j += 8) {   // eight rows' words are read before the chain takes them
+                float x[8][kCols], k[8];
+#pragma unroll
+                for (int t = 0; t < 8; t += 4) *reinterpret_cast<float4*>(k + t) = *reinterpret_cast<const float4*>(wt + j + t);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e)
+                        if (sub + e * WPR < DPL) x[t][e] = to_f(v[(j + t) * TL::LD + 32 * WPR * e]);
+#pragma unroll
+                for (int t = 0; t < 8; ++t)
+#pragma unroll
+                    for (int e = 0; e < kCols; ++e)
+                        if (sub + e * WPR < DPL) o[e] = __fmaf_rn(k[t], x[t][e], o[e]);
+            }
+            for (; j <= jmax; ++j)
+#pragma unroll
+                for (int e = 0; e < kCols; ++e)
+                    if (sub + e * WPR < DPL) o[e] = __fmaf_rn(wt[j], to_f(v[j * TL::LD + 32 * WPR * e]), o[e]);
+            const size_t slot = ((size_t)d.b * a.n_heads + (size_t)d.g * n_rep + row) * a.n_chunks + d.c;
+#pragma unroll
+            for (int e = 0; e < kCols; ++e)
+                if (sub + e * WPR < DPL) a.partial[slot * DH + lane + 32 * (sub + WPR * e)] = o[e];
+            if (lane == 0 && sub == 0) p.part_ml[slot] = make_float2(m[0], l[0]);
+        }
+        __syncthreads();   // V was read
+        if (more) copy(next, s_page[turn ^ 1], a.vc, Vs);
+        d = next;
+        turn ^= 1;
     }
 }
 
@@ -617,17 +781,40 @@ cudaError_t paged_combine_impl(const AttnArgs& a, cudaStream_t s) {
                       make_paged(a), n_stages, scales);
 }
 
-template <typename T, int DH>
-cudaError_t paged_decode_impl(const AttnArgs& a, cudaStream_t s) {
-    auto kern = k_attn_paged_chunks<T, DH>;
+template <typename T, int DH, int WPR>
+cudaError_t paged_chunks_launch(const AttnArgs& a, cudaStream_t s) {
+    auto kern = k_attn_paged_chunks<T, DH, WPR>;
     cudaError_t r = kernel_setup_once((const void*)kern, [](const void* k) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<T, DH>(kRowsMax));
     });
     if (r != cudaSuccess) return r;
-    r = launch_pdl(kern, dim3(a.n_chunks, a.n_kv_heads, a.batch), dim3(kThreads),
-                   smem_bytes<T, DH>(a.n_heads / a.n_kv_heads), s, make_paged(a));
-    if (r != cudaSuccess) return r;
-    return paged_combine_impl<T, DH>(a, s);
+    const int n_rep = a.n_heads / a.n_kv_heads;
+    const size_t smem = smem_bytes<T, DH>(n_rep);
+    const int per_sm = smem <= 100 * 1024 ? 2 : 1;   // two CTAs by their registers
+    for (int b0 = 0; b0 < a.batch; b0 += kPagedSeqs) {
+        PagedK k = make_paged(a);
+        k.a.batch = std::min(a.batch - b0, kPagedSeqs);
+        k.a.pos_seq += b0;
+        k.t.table += (size_t)b0 * a.pages.stride;
+        k.a.q = (const T*)a.q + (size_t)b0 * a.n_heads * DH;
+        k.a.partial += (size_t)b0 * a.n_heads * a.n_chunks * DH;
+        k.part_ml += (size_t)b0 * a.n_heads * a.n_chunks;
+        const long max_units = (long)k.a.batch * a.n_kv_heads * a.n_chunks;
+        const dim3 grid((unsigned)std::min<long>(max_units, (long)device_sm_count() * per_sm));
+        r = launch_pdl(kern, grid, dim3(kThreads), smem, s, k);
+        if (r != cudaSuccess) return r;
+    }
+    return cudaSuccess;
+}
+
+template <typename T, int DH>
+cudaError_t paged_decode_impl(const AttnArgs& a, cudaStream_t s) {
+    const int n_rep = a.n_heads / a.n_kv_heads;
+    // warps per row: as many as leave every row of the group its own
+    const cudaError_t r = n_rep <= kWarps / 4   ? paged_chunks_launch<T, DH, 4>(a, s)
+                          : n_rep <= kWarps / 2 ? paged_chunks_launch<T, DH, 2>(a, s)
+                                                : paged_chunks_launch<T, DH, 1>(a, s);
+    return r != cudaSuccess ? r : paged_combine_impl<T, DH>(a, s);
 }
 
 }  // namespace
@@ -646,9 +833,8 @@ cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s) {
 
 cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s) {
     if (a.batch <= 0) return cudaSuccess;
-    // where the contiguous decode takes the tensor cores (8 query rows a tile)
-    if (a.dtype == LLAMA_BF16 && attention_tc_supported(a.n_heads, a.n_kv_heads, a.head_dim) &&
-        a.n_heads / a.n_kv_heads <= 8)
+    // where the contiguous decode takes the tensor cores
+    if (a.dtype == LLAMA_BF16 && attention_tc_supported(a.n_heads, a.n_kv_heads, a.head_dim))
         return launch_attention_tc_paged(a, s);
     if (a.dtype == LLAMA_BF16) return a.head_dim == 128 ? paged_decode_impl<bf16, 128>(a, s) : cudaErrorInvalidValue;
     switch (a.head_dim) {

@@ -1004,7 +1004,8 @@ struct DecMap {
     const int* spos;   // per-sequence positions (shared memory)
 };
 constexpr int kSeqPosMax = 1024;   // sequences per call with per-sequence positions
-__device__ __forceinline__ DecUnit dec_unit(const DecMap& m, int u) {
+// n_sub > 1 (per-sequence positions): n_kv counts sets of query heads, n_sub per KV head.
+__device__ __forceinline__ DecUnit dec_unit(const DecMap& m, int u, int n_sub = 1) {
     DecUnit d;
     if (m.pre == nullptr) {
         d.c = u % m.n_total;
@@ -1026,6 +1027,11 @@ __device__ __forceinline__ DecUnit dec_unit(const DecMap& m, int u) {
     const int r = u - m.pre[lo] * m.n_kv;
     d.g = r / d.nt;
     d.c = r - d.g * d.nt;
+    if (n_sub > 1) {   // a chunk's sets one after another: its K and V come from L2 after the first
+        const int head = d.g / n_sub, x = r - head * n_sub * d.nt;
+        d.c = x / n_sub;
+        d.g = head * n_sub + x - d.c * n_sub;
+    }
     d.pos = m.spos[lo];
     return d;
 }
@@ -1047,8 +1053,9 @@ __device__ __forceinline__ void tmem_ld_quarter(uint32_t taddr, int q, float (&o
 // columns, so a chunk arrives as 128 / page_size boxes per half, issued by as many
 // lanes of the producer warp; pages behind the last key are not copied and what the
 // stage holds in their place is masked (scores) or zeroed (values).  A sequence may
-// have no key, and so no unit.
-template <bool PAGED>
+// have no key, and so no unit.  Groups of 16, 32 and 64 query heads are taken as sets of
+// 8 rows (SETS; a row's arithmetic does not depend on the tile it sits in).
+template <bool PAGED, bool SETS>
 __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_constant__ CUtensorMap mK,
                                                                 const __grid_constant__ CUtensorMap mV,
                                                                 const TcArgs a) {
@@ -1073,10 +1080,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
     // The position comes from the host side (set before the step is launched), not
     // from the kernels this one overlaps; cache rows below it were written by
     // earlier steps.  Only q and the newest cache row need griddepcontrol.wait.
-    const int n_rep = a.n_heads / a.n_kv_heads;
+    const int group = a.n_heads / a.n_kv_heads;
+    const int n_rep = SETS ? 8 : group, n_sub = SETS ? group / 8 : 1, n_sets = a.n_kv_heads * n_sub;
     __shared__ int s_pre[kSeqPosMax + 1], s_pos[kSeqPosMax];
     __shared__ int s_bad;
-    DecMap dm{a.n_kv_heads, 0, 0, a.batch, nullptr, nullptr};
+    DecMap dm{n_sets, 0, 0, a.batch, nullptr, nullptr};
     int n_units;
     if (a.pos_seq) {
         // per-sequence positions: chunk counts and their prefix sums, one warp
@@ -1119,7 +1127,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         }
         dm.pre = s_pre;
         dm.spos = s_pos;
-        n_units = s_pre[a.batch] * a.n_kv_heads;
+        n_units = s_pre[a.batch] * n_sets;
     } else {
         const int pos = a.pos_dev ? *a.pos_dev : a.start_pos;
         if (pos < 0 || pos >= a.max_pos) {
@@ -1185,7 +1193,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         };
         auto lookup = [&](int i) -> int {
             if (i >= n_iter) return 0;
-            const DecUnit d = dec_unit(dm, u_begin + i);
+            const DecUnit d = dec_unit(dm, u_begin + i, n_sub);
             if (mine >= pages_of(d)) return 0;
             const int id = page_of(a.pages, d.b, (d.c * kAttnChunk >> shift) + mine, is_k && half == 0 ? err : nullptr);
             return max(id, 0);   // recorded; the row is undefined, the copy stays inside the cache
@@ -1196,7 +1204,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
             int go = 1;
             if (lane == 0 && i >= n_st) go = ptx::mbar_wait(&empty[st], ((i / n_st) - 1) & 1, err);
             if (!__shfl_sync(0xffffffffu, go, 0)) break;
-            const DecUnit d = dec_unit(dm, u_begin + i);
+            const DecUnit d = dec_unit(dm, u_begin + i, n_sub);
             if (!waited && d.c == d.nt - 1) {   // this chunk holds the row the QKV step writes
                 ptx::griddep_wait();
                 waited = true;
@@ -1206,7 +1214,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
             __syncwarp();
             if (mine < n)
                 ptx::tma_load_2d_hint(ring + st * 2 * kSub + half * kSub + mine * box * 128, map, &full[st], half * 64,
-                                      ((id * a.n_kv_heads + d.g) << shift) + (d.c * kAttnChunk & (ps - 1)), pol);
+                                      ((id * a.n_kv_heads + d.g / n_sub) << shift) + (d.c * kAttnChunk & (ps - 1)), pol);
             next = lookup(i + 1);
         }
         if (lane == 0)
@@ -1228,7 +1236,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
             for (int i = 0; i < n_iter; ++i, ++issued) {
                 const int st = i % n_st;
                 if (i >= n_st && !ptx::mbar_wait(&empty[st], ((i / n_st) - 1) & 1, err)) break;
-                const DecUnit d = dec_unit(dm, u_begin + i);
+                const DecUnit d = dec_unit(dm, u_begin + i, n_sub);
                 if (!waited && d.c == d.nt - 1) {   // this chunk holds the row the QKV step writes
                     ptx::griddep_wait();
                     TRACE(if (LLAMA_TRACE_ON && is_k) s_tr_release = trace_clock();)
@@ -1296,8 +1304,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         uint4 qreg[4];
         int qreg_bg = -1;
         auto fetch_q = [&](int i) {
-            const DecUnit d = dec_unit(dm, u_begin + i);
-            const int bg = d.b * a.n_kv_heads + d.g;
+            const DecUnit d = dec_unit(dm, u_begin + i, n_sub);
+            const int bg = d.b * n_sets + d.g;
             if (bg == q_bg || bg == qreg_bg) return;
 #pragma unroll
             for (int half = 0; half < 2; ++half)
@@ -1313,8 +1321,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
             qreg_bg = bg;
         };
         auto prepare = [&](int i) {
-            const DecUnit d = dec_unit(dm, u_begin + i);
-            const int bg = d.b * a.n_kv_heads + d.g;
+            const DecUnit d = dec_unit(dm, u_begin + i, n_sub);
+            const int bg = d.b * n_sets + d.g;
             if (bg != q_bg) {
                 fetch_q(i);
 #pragma unroll
@@ -1330,7 +1338,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         };
         if (slot < n_iter) prepare(slot);
         for (int i = slot, k = 0; i < n_iter; i += kDecSlots, ++k) {
-            const DecUnit d = dec_unit(dm, u_begin + i);
+            const DecUnit d = dec_unit(dm, u_begin + i, n_sub);
             const int st = i % kDecStagesV;   // the unit's V stage
             if (ok) ok = ptx::mbar_wait(&s_full[slot], k & 1, err);
             ptx::tc_fence_after();
@@ -1521,12 +1529,12 @@ cudaError_t launch_attention_tc_decode(const AttnArgs& a, int chunks_per_cta, cu
         // persistent: one CTA per SM (units assigned on the device from the position)
         const int n_sm = device_sm_count();
         const long max_units = (long)a.batch * a.n_kv_heads * a.n_chunks;
-        cudaError_t r = kernel_setup_once((const void*)k_attn_tc_dec<false>, [](const void* kern) {
+        cudaError_t r = kernel_setup_once((const void*)k_attn_tc_dec<false, false>, [](const void* kern) {
             return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, D_SMEM_BYTES);
         });
         if (r != cudaSuccess) return r;
         dim3 grid((unsigned)std::min<long>(max_units, n_sm));
-        r = launch_pdl(k_attn_tc_dec<false>, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);
+        r = launch_pdl(k_attn_tc_dec<false, false>, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);
         if (r != cudaSuccess) return r;
         return launch_attention_combine(a, s);
     }
@@ -1551,8 +1559,10 @@ cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s) {
     if (!make_tmap_bf16(&mk, a.kc, rows, 128, std::min(ps, kAttnChunk), nullptr) ||
         !make_tmap_bf16(&mv, a.vc, rows, 128, std::min(ps, kAttnChunk), nullptr))
         return cudaErrorInvalidValue;
-    cudaError_t r = kernel_setup_once((const void*)k_attn_tc_dec<true>, [](const void* kern) {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, D_SMEM_BYTES);
+    const int group = a.n_heads / a.n_kv_heads;
+    const auto kern = group > 8 ? k_attn_tc_dec<true, true> : k_attn_tc_dec<true, false>;
+    cudaError_t r = kernel_setup_once((const void*)kern, [](const void* k) {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, D_SMEM_BYTES);
     });
     if (r != cudaSuccess) return r;
     // a launch maps its units from at most kSeqPosMax lengths
@@ -1564,9 +1574,9 @@ cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s) {
         k.q += (size_t)b0 * a.n_heads * 128;
         k.part_ml = attn_paged_ml(a.partial, a.batch, a.n_heads, a.n_chunks, 128) + (size_t)b0 * a.n_heads * a.n_chunks;
         k.partial += (size_t)b0 * a.n_heads * a.n_chunks * 128;
-        const long max_units = (long)k.batch * a.n_kv_heads * a.n_chunks;
+        const long max_units = (long)k.batch * a.n_kv_heads * (group > 8 ? group / 8 : 1) * a.n_chunks;
         const dim3 grid((unsigned)std::min<long>(max_units, device_sm_count()));
-        r = launch_pdl(k_attn_tc_dec<true>, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);
+        r = launch_pdl(kern, grid, dim3(kDecThreads), D_SMEM_BYTES, s, mk, mv, k);
         if (r != cudaSuccess) return r;
     }
     return launch_attention_paged_combine(a, s);

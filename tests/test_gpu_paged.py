@@ -412,6 +412,46 @@ def test_paged_decode_step_equals_the_contiguous_one(dims, ps):
     assert pool.tolist() == [n_pages, 0] and sorted(free.tolist()) == list(range(n_pages)) and int(err[0]) == 0
 
 
+@pytest.mark.parametrize("dims", [workloads.BlockDims(512, 16, 1, 128, 256), workloads.BlockDims(256, 64, 1, 128, 256),
+                                  workloads.BlockDims(256, 64, 2, 128, 256)], ids=["group16", "group64", "group32"])
+def test_paged_decode_step_of_wide_groups(dims):
+    """Groups of more than 8 query heads, which the contiguous decode takes in a kernel of its own: the
+    same bits at a position all sequences share."""
+    ddb = _ddb()
+    B, P, max_seq, ps = 3, 300, 320, 16
+    w, g = workloads.make_weights(dims, weight_std=0.03)
+    dev = torch.device(DEV)
+    blk = ddb.LlamaBlock(dims, {k: t.to(dev) for k, t in w.items()}, {k: t.to(dev) for k, t in g.items()}, max_seq)
+    k, v = (t.to(dev) for t in workloads.make_cache(dims, B, max_seq, P, 1))
+    columns = max_seq // ps
+    pk = torch.zeros(B * columns, dims.n_kv_heads, ps, 128, dtype=torch.bfloat16, device=dev)
+    kv = ddb.PagedCache(pk, pk.clone())
+    table = torch.randperm(B * columns, generator=torch.Generator().manual_seed(2)).view(B, columns).to(torch.int32).to(dev)
+    t = torch.arange(P, device=dev)
+    slots = (table[:, t // ps] * ps + t % ps).to(torch.int32).contiguous()
+    ddb.llama_paged_store(k, v, slots, kv)
+    x = workloads.make_x(B, 1, dims.d_model).to(dev)
+    y, yp = torch.empty_like(x), torch.empty_like(x)
+    blk.decode(x, ddb.KVCache(k, v), P, y, blk.workspace(B, 1))
+    blk.decode_paged(x, kv, table, _i32([P] * B), yp, blk.workspace(B, 1))
+    torch.cuda.synchronize()
+    assert blk.poll_error() == 0 and torch.equal(y, yp)
+
+
+def test_attention_with_a_bound_far_above_the_lengths():
+    """The units are counted from the lengths: a bound of a million keys changes no bit."""
+    ddb = _ddb()
+    for shape in ("8b", "group3", "f32-64"):
+        dtype, Hq, Hkv, D = SHAPES[shape]
+        lens = [200, 0, 129]
+        _, pk, pv, table = _paged(lens, Hkv, D, 16, dtype, 12)
+        wide = torch.full((3, 1 << 16), -1, dtype=torch.int32, device=DEV)
+        wide[:, :table.shape[1]] = table
+        q = torch.randn(3, Hq, D, generator=torch.Generator().manual_seed(1)).to(dtype).to(DEV)
+        kv = ddb.PagedCache(pk, pv)
+        assert torch.equal(_attend(ddb, q, kv, table, lens, 200), _attend(ddb, q, kv, wide, lens, 1 << 20))
+
+
 def test_paged_decode_step_records_bad_positions_and_pages():
     ddb = _ddb()
     dims = workloads.BlockDims(512, 8, 2, 128, 1024)
