@@ -181,11 +181,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
 //
 // Both operands from shared memory.  A is K-major in two 64-column sub-tiles
 // A_SUB16 x 16 bytes apart (step ks at (ks / 4) sub-tiles + (ks % 4) * 32 bytes);
-// B likewise with B_SUB16, or MN-major (B_MN: step ks 16 rows = 2048 bytes on).
+// B likewise with B_SUB16, or MN-major (B_MN: step ks 16 rows on, B_SUB16 x 16 bytes).
 template <int A_SUB16, int B_SUB16, bool B_MN>
 __device__ __forceinline__ void umma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
 #define LLAMA_AOFF(ks) ((ks) / 4 * A_SUB16 + (ks) % 4 * 2)
-#define LLAMA_BOFF(ks) (B_MN ? (ks) * 128 : (ks) / 4 * B_SUB16 + (ks) % 4 * 2)
+#define LLAMA_BOFF(ks) (B_MN ? (ks) * B_SUB16 : (ks) / 4 * B_SUB16 + (ks) % 4 * 2)
     asm volatile(
         "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a<8>, b<8>;\n\t"
         "setp.ne.b32 pf, %3, %3;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ptx::mbar_wait(p_full, i & 1, err)) break;
                 if (i > 0 && !ptx::mbar_wait(oc_empty, (i - 1) & 1, err)) break;
                 ptx::tc_fence_after();
-                umma8_ss<kSub / 16, 0, true>(tmem + TM_OC, ptx::sw128_kmajor_desc(p_addr),
+                umma8_ss<kSub / 16, 128, true>(tmem + TM_OC, ptx::sw128_kmajor_desc(p_addr),
                                              ptx::sw128_mnmajor_desc(v_addr, kSub), IDESC_PV);
                 ptx::umma_commit(o_full);
                 ptx::umma_commit(&kv_empty[st]);
@@ -959,6 +959,15 @@ __device__ __forceinline__ void tma_load_chunk(void* dst, const CUtensorMap* map
         : "memory");
 }
 
+// A page's rows, from row group `group` on (see make_tmap_pages).
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int group, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(group), "l"(policy)
+        : "memory");
+}
+
 // Persistent decode attention for groups of n_rep <= 8 query heads.  The work
 // units are (sequence, KV head, chunk); CTA i walks a contiguous range of them.
 // Query and P tiles hold 8 rows; their descriptors use an 8-row-group stride of
@@ -986,8 +995,12 @@ static_assert(kDecSlots * 2048 <= D_OFF_P && D_OFF_P + kDecSlots * 2048 <= D_OFF
 static_assert(kDecSlots * 128 <= 512, "TMEM columns");
 constexpr int D_SMEM_BYTES = D_OFF_BAR + 256 + 1024;
 
+// A descriptor's distance between 8-row groups (stride byte offset) set to `bytes`.
+__device__ __forceinline__ uint64_t desc_with_stride(uint64_t desc, uint32_t bytes) {
+    return (desc & ~(0x3FFFull << 32)) | ((uint64_t)(bytes >> 4) << 32);
+}
 __device__ __forceinline__ uint64_t sw128_kmajor_desc_rows8(uint32_t smem_addr) {
-    return ptx::sw128_kmajor_desc(smem_addr) & ~(0x3FFFull << 32);   // stride byte offset 0
+    return desc_with_stride(ptx::sw128_kmajor_desc(smem_addr), 0);
 }
 
 // Decode units: (sequence b, KV head g, chunk c), c fastest, then g, then b.  With
@@ -1048,11 +1061,14 @@ __device__ __forceinline__ void tmem_ld_quarter(uint32_t taddr, int q, float (&o
     }
 }
 
-// PAGED: the same units over a paged cache.  The map's rows are those of all pages
-// ([n_pages][n_kv_heads][page_size]) and its box one page (of at most 128 rows) of 64
-// columns, so a chunk arrives as 128 / page_size boxes per half, issued by as many
-// lanes of the producer warp; pages behind the last key are not copied and what the
-// stage holds in their place is masked (scores) or zeroed (values).  A sequence may
+// PAGED: the same units over a paged cache.  A page (of at most 128 rows) is one TMA copy,
+// issued by a lane of its own of the producer warp: the cache is seen as [row groups of 8]
+// [2 halves of 64 columns][8 rows][64], so a chunk's pages lie one after another and every
+// 8-row group has its two halves side by side, 1024 bytes each, 2048 to the next group.
+// (Two copies per page, one per half, as the contiguous cache's sub-tiles would want: 16-row
+// pages then took 36.5 us where 128-row pages took 31.5, 8B batch 32 at 1000 keys.)  Pages
+// behind the last key are not copied and what the stage holds in their place is masked
+// (scores) or zeroed (values).  A sequence may
 // have no key, and so no unit.  Groups of 16, 32 and 64 query heads are taken as sets of
 // 8 rows (SETS; a row's arithmetic does not depend on the tile it sits in).
 template <bool PAGED, bool SETS>
@@ -1186,16 +1202,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         const uint64_t pol = ptx::policy_evict_first();
         bool waited = false;
         int issued = 0;
-        // lane = (page of the chunk, half): its page id is read a unit ahead of its copy
-        const int mine = lane >> 1, half = lane & 1;
+        // lane = page of the chunk: its id is read a unit ahead of its copy
         auto pages_of = [&](const DecUnit& d) {
             return (min(kAttnChunk, d.pos + 1 - d.c * kAttnChunk) + box - 1) / box;
         };
         auto lookup = [&](int i) -> int {
             if (i >= n_iter) return 0;
             const DecUnit d = dec_unit(dm, u_begin + i, n_sub);
-            if (mine >= pages_of(d)) return 0;
-            const int id = page_of(a.pages, d.b, (d.c * kAttnChunk >> shift) + mine, is_k && half == 0 ? err : nullptr);
+            if (lane >= pages_of(d)) return 0;
+            const int id = page_of(a.pages, d.b, (d.c * kAttnChunk >> shift) + lane, is_k ? err : nullptr);
             return max(id, 0);   // recorded; the row is undefined, the copy stays inside the cache
         };
         int next = lookup(0);
@@ -1212,9 +1227,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
             const int n = pages_of(d), id = next;
             if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], n * box * 256);
             __syncwarp();
-            if (mine < n)
-                ptx::tma_load_2d_hint(ring + st * 2 * kSub + half * kSub + mine * box * 128, map, &full[st], half * 64,
-                                      ((id * a.n_kv_heads + d.g / n_sub) << shift) + (d.c * kAttnChunk & (ps - 1)), pol);
+            if (lane < n) {
+                const int row = ((id * a.n_kv_heads + d.g / n_sub) << shift) + (d.c * kAttnChunk & (ps - 1));
+                tma_load_page(ring + st * 2 * kSub + lane * box * 256, map, &full[st], row >> 3, pol);
+            }
             next = lookup(i + 1);
         }
         if (lane == 0)
@@ -1262,8 +1278,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
                 const uint32_t p_addr = ptx::smem_u32(sm + D_OFF_P + slot * 2048);
                 if (!ptx::mbar_wait(&v_full[st], (j / kDecStagesV) & 1, err)) return false;
                 const uint32_t v_addr = ptx::smem_u32(sm + D_OFF_V + st * 2 * kSub);
-                umma8_ss<1024 / 16, 0, true>(tmem + slot * 128, sw128_kmajor_desc_rows8(p_addr),
-                                             ptx::sw128_mnmajor_desc(v_addr, kSub), IDESC_PV);
+                if constexpr (PAGED)
+                    umma8_ss<1024 / 16, 256, true>(tmem + slot * 128, sw128_kmajor_desc_rows8(p_addr),
+                                                   desc_with_stride(ptx::sw128_mnmajor_desc(v_addr, 1024), 2048), IDESC_PV);
+                else
+                    umma8_ss<1024 / 16, 128, true>(tmem + slot * 128, sw128_kmajor_desc_rows8(p_addr),
+                                                   ptx::sw128_mnmajor_desc(v_addr, kSub), IDESC_PV);
                 ptx::umma_commit(&o_full[slot]);
                 ptx::umma_commit(&v_empty[st]);
                 return true;
@@ -1276,8 +1296,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
                 ptx::tc_fence_after();
                 const uint32_t q_addr = ptx::smem_u32(sm + D_OFF_Q + slot * 2048);
                 const uint32_t k_addr = ptx::smem_u32(sm + D_OFF_K + st * 2 * kSub);
-                umma8_ss<1024 / 16, kSub / 16, false>(tmem + slot * 128, sw128_kmajor_desc_rows8(q_addr),
-                                                      ptx::sw128_kmajor_desc(k_addr), IDESC_S);
+                if constexpr (PAGED)
+                    umma8_ss<1024 / 16, 1024 / 16, false>(tmem + slot * 128, sw128_kmajor_desc_rows8(q_addr),
+                                                          desc_with_stride(ptx::sw128_kmajor_desc(k_addr), 2048), IDESC_S);
+                else
+                    umma8_ss<1024 / 16, kSub / 16, false>(tmem + slot * 128, sw128_kmajor_desc_rows8(q_addr),
+                                                          ptx::sw128_kmajor_desc(k_addr), IDESC_S);
                 ptx::umma_commit(&s_full[slot]);
                 ptx::umma_commit(&k_empty[st]);
                 if (i > 0) ok = issue_pv(i - 1);
@@ -1365,11 +1389,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
                 for (int r4 = 0; r4 < 4; ++r4) {
                     const int vr = lane + 32 * r4;
                     if (d.c * kAttnChunk + vr > d.pos) {
-                        uint8_t* vrow = sm + D_OFF_V + st * 2 * kSub + vr * 128;
+                        constexpr int kHalf = PAGED ? 1024 : kSub;   // to the row's other 64 columns
+                        uint8_t* vrow = sm + D_OFF_V + st * 2 * kSub +
+                                        (PAGED ? (vr >> 3) * 2048 + (vr & 7) * 128 : vr * 128);
 #pragma unroll
                         for (int c16 = 0; c16 < 8; ++c16) {
                             *reinterpret_cast<uint4*>(vrow + c16 * 16) = make_uint4(0, 0, 0, 0);
-                            *reinterpret_cast<uint4*>(vrow + kSub + c16 * 16) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(vrow + kHalf + c16 * 16) = make_uint4(0, 0, 0, 0);
                         }
                     }
                 }
@@ -1437,6 +1463,19 @@ bool make_tmap_kv_chunk(CUtensorMap* map, const void* base, uint64_t rows) {
     cuuint32_t box[3] = {64, 128, 2};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A paged K or V cache, `rows` rows of 128 bf16, as [rows / 8][2][8][64]; box: `box_rows` rows.
+bool make_tmap_pages(CUtensorMap* map, const void* base, uint64_t rows, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {64, 8, 2, rows / 8};
+    cuuint64_t strides[3] = {128 * 2, 64 * 2, 8 * 128 * 2};
+    cuuint32_t box[4] = {64, 8, 2, (cuuint32_t)box_rows / 8};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1556,8 +1595,8 @@ cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s) {
     const int ps = 1 << a.pages.shift;
     const uint64_t rows = (uint64_t)a.pages.n_pages * a.n_kv_heads * ps;
     CUtensorMap mk, mv;
-    if (!make_tmap_bf16(&mk, a.kc, rows, 128, std::min(ps, kAttnChunk), nullptr) ||
-        !make_tmap_bf16(&mv, a.vc, rows, 128, std::min(ps, kAttnChunk), nullptr))
+    if (!make_tmap_pages(&mk, a.kc, rows, std::min(ps, kAttnChunk)) ||
+        !make_tmap_pages(&mv, a.vc, rows, std::min(ps, kAttnChunk)))
         return cudaErrorInvalidValue;
     const int group = a.n_heads / a.n_kv_heads;
     const auto kern = group > 8 ? k_attn_tc_dec<true, true> : k_attn_tc_dec<true, false>;
