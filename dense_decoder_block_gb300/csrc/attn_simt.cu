@@ -17,6 +17,7 @@
 // neither scored nor loaded.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "attn_fold.cuh"
 #include "internal.h"
@@ -595,50 +596,54 @@ __global__ void __launch_bounds__(comb_threads(DH) + 32) k_attn_paged_combine(co
     int at = 0, turn = 0;   // place in the ring, its parity
     for (int block = 0; block < n_chunks; block += kCombBlock) {
         const int nb = min(kCombBlock, n_chunks - block), per = (nb + kThr - 1) / kThr;
-        // this thread's chunks: block + tid * per + i, i < per
-        float m[kPer], l[kPer], most = -INFINITY;
+        // this thread's chunks: block + tid * per + i, i < per <= N
+        auto take_scales = [&](auto count) {
+            constexpr int N = decltype(count)::value;
+            float m[N], l[N], most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = tid * per + i;
-            m[i] = -INFINITY;
-            if (i < per && c < nb) {
-                const float2 ml = __ldcg(part_ml + block + c);
+            for (int i = 0; i < N; ++i) {
+                const int c = tid * per + i;
+                const float2 ml = i < per && c < nb ? __ldcg(part_ml + block + c) : make_float2(-INFINITY, 0.f);
                 m[i] = ml.x;
                 l[i] = ml.y;
             }
-        }
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) most = fmaxf(most, m[i]);
+            for (int i = 0; i < N; ++i) most = fmaxf(most, m[i]);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const float v = __shfl_up_sync(kFull, most, o);
-            if (lane >= o) most = fmaxf(most, v);
-        }
-        ptx::named_bar_sync(1, kThr);   // the maxima and scales of the block before were read
-        if (lane == 31) s_max[warp] = most;
-        ptx::named_bar_sync(1, kThr);
-        float now = __shfl_up_sync(kFull, most, 1);
-        if (lane == 0) now = -INFINITY;
-        now = fmaxf(M, now);
-#pragma unroll
-        for (int w = 0; w < kThr / 32; ++w) {
-            if (w < warp) now = fmaxf(now, s_max[w]);
-            M = fmaxf(M, s_max[w]);
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = tid * per + i;
-            if (i < per && c < nb) {
-                const bool first = block + c == 0;
-                const float next = fmaxf(now, m[i]);
-                const float sa = first ? 0.f : exp2f(__fsub_rn(now, next)), sb = first ? 1.f : exp2f(__fsub_rn(m[i], next));
-                scale[c] = sa;
-                scale[n_scales + c] = sb;
-                scale[2 * n_scales + c] = __fmul_rn(l[i], sb);
-                now = next;
+            for (int o = 1; o < 32; o <<= 1) {
+                const float v = __shfl_up_sync(kFull, most, o);
+                if (lane >= o) most = fmaxf(most, v);
             }
-        }
-        ptx::named_bar_sync(1, kThr);
+            ptx::named_bar_sync(1, kThr);   // the maxima and scales of the block before were read
+            if (lane == 31) s_max[warp] = most;
+            ptx::named_bar_sync(1, kThr);
+            float now = __shfl_up_sync(kFull, most, 1);
+            if (lane == 0) now = -INFINITY;
+            now = fmaxf(M, now);
+#pragma unroll
+            for (int w = 0; w < kThr / 32; ++w) {
+                if (w < warp) now = fmaxf(now, s_max[w]);
+                M = fmaxf(M, s_max[w]);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = tid * per + i;
+                if (i < per && c < nb) {
+                    const bool first = block + c == 0;
+                    const float next = fmaxf(now, m[i]);
+                    const float sa = first ? 0.f : exp2f(__fsub_rn(now, next)), sb = first ? 1.f : exp2f(__fsub_rn(m[i], next));
+                    scale[c] = sa;
+                    scale[n_scales + c] = sb;
+                    scale[2 * n_scales + c] = __fmul_rn(l[i], sb);
+                    now = next;
+                }
+            }
+            ptx::named_bar_sync(1, kThr);
+        };
+        // short rows are not made to walk the longest one's unrolled rounds (1 us of a call)
+        if (per == 1) take_scales(std::integral_constant<int, 1>{});
+        else if (per <= 4) take_scales(std::integral_constant<int, 4>{});
+        else take_scales(std::integral_constant<int, kPer>{});
         for (int c0 = 0; c0 < nb; c0 += kCombStage) {
             const int n = min(kCombStage, nb - c0);
             ok = ok && ptx::mbar_wait(&s_full[at], turn, a.err);

@@ -413,10 +413,14 @@ int llama_paged_attention(const void* q, int batch, int n_heads, int n_kv_heads,
 
 /* llama_block_decode_seqpos on a paged cache: sequence b at position pos_seq[b],
  * its rows found through row b of table [batch, table_stride]; the page of the
- * position must be in the table (llama_paged_plan).  Same result, bit for bit, and
- * the same limits; a page id outside [0, n_pages) is recorded in the handle's error
- * word (LLAMA_ERR_INVALID_ARG; that cache row is not written, y undefined).  Rows of
- * table may share pages that no position of the call is written to. */
+ * position must be in the table (llama_paged_plan).  Same result, bit for bit, as
+ * on a contiguous cache.  For bf16 handles whose number of query heads per KV head
+ * divides 128 (at most 64), and batch <= 32; otherwise LLAMA_ERR_UNSUPPORTED_DIMS.
+ * A position outside [0, max_seq) or beyond the table row is recorded in the
+ * handle's error word (LLAMA_ERR_POS_RANGE), and so is a page id outside
+ * [0, n_pages) (LLAMA_ERR_INVALID_ARG): that sequence's cache row is not written
+ * and its y is undefined.  Rows of table may share pages that no position of the
+ * call is written to. */
 int llama_block_decode_paged(llama_block blk, const void* x, int batch, const llama_paged_cache* kv,
                              const int32_t* table, int table_stride, const int32_t* pos_seq, void* y,
                              void* workspace, size_t workspace_bytes, void* stream);

@@ -438,6 +438,36 @@ def test_paged_decode_step_of_wide_groups(dims):
     assert blk.poll_error() == 0 and torch.equal(y, yp)
 
 
+@pytest.mark.parametrize("dtype,dims", [
+    (torch.float32, workloads.TINY), (torch.float32, workloads.BlockDims(128, 4, 4, 32, 64)),
+    (torch.float32, workloads.BlockDims(128, 9, 1, 128, 64)), (torch.bfloat16, workloads.BlockDims(256, 6, 2, 128, 128)),
+    (torch.bfloat16, workloads.BlockDims(256, 5, 1, 128, 128)), (torch.bfloat16, workloads.BlockDims(256, 9, 1, 128, 128))],
+    ids=["f32-2x64", "f32-1x32", "f32-9x128", "bf16-3x128", "bf16-5x128", "bf16-9x128"])
+@pytest.mark.parametrize("P", [0, 127, 128, 700])
+def test_attention_bits_equal_the_blocks_cuda_core_decode(dtype, dims, P):
+    """The shapes that the tensor-core kernel does not take: the block's own decode attention, from its q."""
+    ddb = _ddb()
+    B, max_seq, ps = 2, 720, 16
+    w, g = workloads.make_weights(dims, dtype=dtype)
+    dev = torch.device(DEV)
+    blk = ddb.LlamaBlock(dims, {k: t.to(dev) for k, t in w.items()}, {k: t.to(dev) for k, t in g.items()}, max_seq)
+    k, v = (t.to(dev) for t in workloads.make_cache(dims, B, max_seq, P, 1, dtype=dtype))
+    x = workloads.make_x(B, 1, dims.d_model, dtype=dtype).to(dev)
+    ws = blk.workspace(B, 1)
+    blk.decode(x, ddb.KVCache(k, v), P, torch.empty_like(x), ws)
+    torch.cuda.synchronize()
+    assert blk.poll_error() == 0
+    mid = blk.intermediates(ws, B, 1)
+    columns = max_seq // ps
+    pk = torch.full((B * columns, dims.n_kv_heads, ps, dims.head_dim), float("nan"), dtype=dtype, device=dev)
+    kv = ddb.PagedCache(pk, pk.clone())
+    table = torch.randperm(B * columns, generator=torch.Generator().manual_seed(2)).view(B, columns).to(torch.int32).to(dev)
+    t = torch.arange(P + 1, device=dev)
+    ddb.llama_paged_store(k, v, (table[:, t // ps] * ps + t % ps).to(torch.int32).contiguous(), kv)
+    o = _attend(ddb, mid["q"].reshape(B, dims.n_heads, dims.head_dim).contiguous(), kv, table, [P + 1] * B, max_seq)
+    assert torch.equal(o.view(B, -1), mid["o"])
+
+
 def test_attention_with_a_bound_far_above_the_lengths():
     """The units are counted from the lengths: a bound of a million keys changes no bit."""
     ddb = _ddb()
