@@ -363,7 +363,8 @@ typedef struct {
  *     table [batch, table_stride];
  *   - slots [batch, tokens] receives page * page_size + row of each new position
  *     start[b] + t, and -1 for t >= count[b].
- * pool is {number of free pages, 0}; pool_out receives the new one and may be pool.
+ * pool is {number of free pages, 0}; pool_out receives the new one and may be pool
+ * (its second word must be 0 before a call and is 0 after it).
  * Entries of table that are not filled, and free_pages, are left as they are.  A
  * request with start < 0, count outside 0 .. tokens or more positions than its
  * table row holds gets no page and slots of -1 (LLAMA_ERR_POS_RANGE in err_dev);
