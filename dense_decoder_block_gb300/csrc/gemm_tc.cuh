@@ -119,7 +119,8 @@ __device__ __forceinline__ void epi_swiglu_row(bf16* dst, const float (&g)[CPT],
 // alias the inputs as far as the compiler knows, so a load per column after the
 // previous column's store costs one memory round trip per column.  Per element
 // the arithmetic is epi_store's.
-template <int EPI, int CPT>
+// PAGES: the K and V rows may go to pages (e.pages; decode only).
+template <int EPI, int CPT, bool PAGES = false>
 __device__ __forceinline__ void epi_store_cols(const GemmKArgs& a, int tile, int row, int n0, const float (&acc)[CPT],
                                                const float (&acc_up)[CPT], int n_cols = CPT) {
     const GemmEpi& e = a.e;
@@ -195,7 +196,7 @@ __device__ __forceinline__ void epi_store_cols(const GemmKArgs& a, int tile, int
                         const bf16 r = __float2bfloat16_rn(v);
                         int cb = b, row_in = pos;
                         if (kind == 0) qp[(size_t)(c0 + j) * q_stride] = r;
-                        else if (!e.pages.table || paged_row(e, cb, row_in))
+                        else if (!PAGES || !e.pages.table || paged_row(e, cb, row_in))
                             cp[(size_t)cb * seq_stride + (size_t)row_in * 128] = r;
                     }
                 }

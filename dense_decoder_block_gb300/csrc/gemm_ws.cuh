@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 continue;
             }
-            if (ok) epi_store_cols<EPI, CPT>(a, tile, row, ncol0, acc[0], acc[NACC - 1]);
+            if (ok) epi_store_cols<EPI, CPT, true>(a, tile, row, ncol0, acc[0], acc[NACC - 1]);
         }
     }
 

@@ -29,12 +29,12 @@ struct GemmEpi {
     int start_pos = 0;                              // position of token t = base + t
     const int* pos_dev = nullptr;                   // if set, base = *pos_dev
     const int* pos_seq = nullptr;                   // decode (T = 1): token n at position pos_seq[n]
-    PageTable pages;                                // if .table is set (with pos_seq): kc, vc are pages
     int max_pos = 0;                                // positions must be < max_pos
     const float* cos_tab = nullptr;                 // [max_pos, 64]
     const float* sin_tab = nullptr;
     bool rope_later = false;                        // QKV: store q, k unrotated (launch_rope_inplace follows)
     int* err = nullptr;
+    PageTable pages;                                // if .table is set (with pos_seq): kc, vc are pages
 };
 
 // The (page, row) in which sequence b keeps position pos, in place of (b, pos); false

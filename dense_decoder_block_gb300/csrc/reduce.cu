@@ -48,6 +48,7 @@ __device__ __forceinline__ unsigned long long griddep() {
 // chunks while the reduction runs.
 constexpr int kQkvThreads = 320;
 
+template <bool PAGED>
 __global__ void __launch_bounds__(kQkvThreads, 4) k_reduce_qkv(const ReduceArgs r) {
     TRACE(const unsigned long long tr0 = trace_stamp();)
     const int F4 = r.F / 4;
@@ -56,7 +57,7 @@ __global__ void __launch_bounds__(kQkvThreads, 4) k_reduce_qkv(const ReduceArgs 
     bool live = idx < n_items;
     int n = live ? idx / F4 : 0, f0 = live ? (idx - n * F4) * 4 : 0;
     Qkv4 p{};
-    if (live) p = epi4_qkv_prepare(r.e, n, f0);
+    if (live) p = epi4_qkv_prepare<PAGED>(r.e, n, f0);
     TRACE(const unsigned long long tr1 =) griddep();
     while (live) {
         float4 s, unused;
@@ -67,7 +68,7 @@ __global__ void __launch_bounds__(kQkvThreads, 4) k_reduce_qkv(const ReduceArgs 
         if (live) {
             n = idx / F4;
             f0 = (idx - n * F4) * 4;
-            p = epi4_qkv_prepare(r.e, n, f0);
+            p = epi4_qkv_prepare<PAGED>(r.e, n, f0);
         }
     }
     TRACE(trace_cta(TR_REDUCE_QKV, tr0, tr1);)
@@ -183,8 +184,8 @@ LLAMA_TRACE_UNIT(reduce)
 cudaError_t launch_reduce(const ReduceArgs& r, int kind, cudaStream_t s) {
     if (r.M <= 0) return cudaSuccess;
     if (r.F % 4) return cudaErrorInvalidValue;
-    auto kern = kind == EPI_QKV ? k_reduce_qkv : kind == EPI_RESID ? k_reduce_resid : kind == EPI_SWIGLU ? k_reduce_swiglu
-                                                                                                     : nullptr;
+    const auto qkv = r.e.pages.table ? k_reduce_qkv<true> : k_reduce_qkv<false>;
+    auto kern = kind == EPI_QKV ? qkv : kind == EPI_RESID ? k_reduce_resid : kind == EPI_SWIGLU ? k_reduce_swiglu : nullptr;
     if (!kern) return cudaErrorInvalidValue;
     cudaError_t e = kernel_setup_once((const void*)kern, setup_prefer_shared);
     if (e != cudaSuccess) return e;

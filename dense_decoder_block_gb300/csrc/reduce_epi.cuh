@@ -70,6 +70,8 @@ struct Qkv4 {
     bool rope;
 };
 
+// PAGED: k and v go to the page that e.pages has for the position.
+template <bool PAGED>
 __device__ __forceinline__ Qkv4 epi4_qkv_prepare(const GemmEpi& e, int n, int f0) {
     Qkv4 p{};
     const int tile = f0 / 128, row0 = f0 % 128;
@@ -97,7 +99,7 @@ __device__ __forceinline__ Qkv4 epi4_qkv_prepare(const GemmEpi& e, int n, int f0
         p.dst = e.out + (size_t)n * (e.n_heads * 128) + head * 128 + row0;
     } else {
         int cb = b, cp = pos;
-        if (e.pages.table && !paged_row(e, cb, cp)) {
+        if (PAGED && !paged_row(e, cb, cp)) {
             p.dst = nullptr;
             return p;
         }
