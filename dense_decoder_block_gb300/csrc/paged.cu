@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PlanArgs a) {
         __threadfence();
         ticket = atomicAdd(a.pool_out + 1, 1);
     }
-    const long long n_items = (long long)a.batch * a.width;
+    const long long n_items = RELEASE || a.tokens > 0 ? (long long)a.batch * a.width : 0;   // no slots: the requests are checked alone
     const long long i0 = (long long)blockIdx.x * kPlanItems;
     const long long i1 = i0 + kPlanItems < n_items ? i0 + kPlanItems : n_items;
     const int b_lo = i1 > i0 ? (int)(i0 / a.width) : 0;
@@ -402,7 +402,7 @@ extern "C" int llama_paged_plan(const int32_t* start, const int32_t* count, int 
     a.start = start;
     a.count = count;
     a.batch = batch;
-    a.width = std::max(tokens, 1);   // with no token columns every count must be 0: nothing is written
+    a.width = std::max(tokens, 1);
     a.tokens = tokens;
     a.shift = page_shift(page_size);
     a.n_pages = n_pages;
@@ -413,7 +413,6 @@ extern "C" int llama_paged_plan(const int32_t* start, const int32_t* count, int 
     a.stride = table_stride;
     a.slots = slots;
     a.err = err_dev;
-    if (tokens == 0) a.batch = 0;
     return run_plan<false>(a, (cudaStream_t)stream);
 }
 

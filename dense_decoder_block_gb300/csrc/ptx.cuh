@@ -73,12 +73,14 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 // Bounded wait.  Returns false (and sets *err) when the budget runs out or when
-// another thread of the grid already reported an error.  The error word is read
+// another thread of the grid already reported an expired wait (other errors -- a bad
+// page of one sequence, say -- do not stop the rest).  The error word is read
 // only once a wait has lasted kErrPollNs: every waiting warp of every CTA polling
 // one global address would keep that address's L2 slice busy and slow all the
 // loads that go through it.  err may be null: the wait is still bounded, it just
 // has nowhere to record the expiry.
 constexpr uint64_t kErrPollNs = 200000ull;   // 200 us
+constexpr int kTimeout = -6;                 // LLAMA_ERR_DEVICE_TIMEOUT
 __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, int* err, uint64_t budget_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
@@ -87,9 +89,9 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, in
         if (mbar_try_wait(bar, parity)) return true;
         if ((++spins & 63u) == 0) {
             const uint64_t dt = globaltimer() - t0;
-            if (err && dt > kErrPollNs && (spins & 4095u) == 0 && *((volatile int*)err) != 0) return false;
+            if (err && dt > kErrPollNs && (spins & 4095u) == 0 && *((volatile int*)err) == kTimeout) return false;
             if (dt > budget_ns) {
-                if (err) atomicCAS(err, 0, -6 /* LLAMA_ERR_DEVICE_TIMEOUT */);
+                if (err) atomicCAS(err, 0, kTimeout);
                 return false;
             }
         }

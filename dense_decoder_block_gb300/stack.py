@@ -232,7 +232,8 @@ class BeamSearch:
         self._choose(self.tokens if self.eos >= 0 else None, stream)
 
     def sequences(self):
-        """(tokens [requests, beams, chosen], scores [requests, beams]), best first."""
+        """(tokens [requests, beams, chosen], scores [requests, beams]), best first; waits for the device."""
+        torch.cuda.synchronize(self.pos.device)      # the calls may have gone to any stream
         n = int(self.n.item())
         row = torch.arange(self.rows, device=self.pos.device)
         out = torch.empty(self.rows, n, dtype=torch.int32, device=self.pos.device)
@@ -249,5 +250,6 @@ class BeamSearch:
             self.active = False
 
     def poll_error(self) -> int:
+        torch.cuda.synchronize(self.pos.device)
         rc = self.stack.poll_error()
         return rc if rc else int(self.err.item())

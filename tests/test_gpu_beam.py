@@ -101,6 +101,39 @@ def test_select_first_step_ended_and_masked_beams():
         _check(ddb, logits, scores, 4, 16, last, e)
 
 
+@pytest.mark.parametrize("vocab", [1024, 1000])
+def test_select_unaligned_logits_and_unread_rows(vocab):
+    """Logits one float off a 16-byte boundary; NaN in the rows of beams that are not read."""
+    ddb = _ddb()
+    logits, scores = _draw(8, vocab, 11)
+    scores[3] = float("-inf")
+    last = torch.zeros(8, dtype=torch.int32)
+    last[6] = 5
+    want = ref.beam_select(logits.double().numpy(), scores.double().numpy(), 4, 8, last.numpy(), 5)
+    logits[3] = float("nan")
+    logits[6] = float("nan")
+    buf = torch.empty(8 * vocab + 1, device=DEV)
+    off = buf[1:].view(8, vocab)
+    off.copy_(logits)
+    for x in (off, logits):
+        got = _select(ddb, x, scores, 4, 8, last, 5)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+def test_select_in_place():
+    """With as many candidates as beams the scores and last tokens may be overwritten."""
+    ddb = _ddb()
+    logits, scores = _draw(12, 5000, 14)
+    last = torch.zeros(12, dtype=torch.int32)
+    last[4] = 7
+    want = _select(ddb, logits, scores, 4, 4, last, 7)
+    ws = torch.empty(ddb.llama_beam_select_workspace_bytes(3, 4, 5000, 4), dtype=torch.uint8, device=DEV)
+    sc, tok, par = scores.to(DEV), last.to(DEV), torch.empty(12, dtype=torch.int32, device=DEV)
+    ddb.llama_beam_select(logits.to(DEV), sc, 4, 4, par, tok, sc, ws, last=tok, eos=7)
+    for a, b in zip((par, tok, sc), want):
+        assert np.array_equal(a.cpu().numpy().reshape(3, 4), b)
+
+
 def test_select_shared_workspace_and_graphs():
     ddb = _ddb()
     logits, scores = _draw(8, 30000, 8)

@@ -123,6 +123,31 @@ def test_plan_refuses_on_the_device():
     assert got[3] == n_free and got[4] == -7 and np.array_equal(got[2], free)
 
 
+def test_plan_unaligned_slots_and_no_token_columns():
+    ddb = _ddb()
+    start, count, tokens, ps = [3, 40, 0], [21, 0, 13], 21, 16
+    n_pages, table, free, n_free = _plan_state(start, count, tokens, ps, 4, 0, 5)
+    want = ref.plan(start, count, tokens, ps, n_pages, free, n_free, table)
+    t, p, err = _i32(table), _i32([n_free, 0]), _i32([0])
+    buf = torch.full((3 * tokens + 2,), -9, dtype=torch.int32, device=DEV)
+    slots = buf[1:1 + 3 * tokens].view(3, tokens)                       # rows off 16-byte boundaries
+    ddb.llama_paged_plan(_i32(start), _i32(count), ps, n_pages, _i32(free), p, t, slots, err_dev=err)
+    assert np.array_equal(slots.cpu().numpy(), want[1]) and np.array_equal(t.cpu().numpy(), want[0])
+    assert buf[0] == -9 and buf[-1] == -9 and p.tolist() == [want[3], 0]
+    # no token columns: a count above 0 is out of range, nothing is taken
+    none = torch.empty(3, 0, dtype=torch.int32, device=DEV)
+    p, t = _i32([n_free, 0]), _i32(table)
+    ddb.llama_paged_plan(_i32(start), _i32([0, 0, 0]), ps, n_pages, _i32(free), p, t, none, err_dev=err)
+    assert p.tolist() == [n_free, 0] and int(err[0]) == 0
+    ddb.llama_paged_plan(_i32(start), _i32(count), ps, n_pages, _i32(free), p, t, none, err_dev=err)
+    assert p.tolist() == [n_free, 0] and int(err[0]) == -3 and np.array_equal(t.cpu().numpy(), table)
+    # an empty batch passes the count on
+    out = _i32([-5, 0])
+    ddb.llama_paged_plan(_i32([]), _i32([]), ps, n_pages, _i32(free), p, t, torch.empty(0, 4, dtype=torch.int32, device=DEV),
+                         pool_out=out)
+    assert out.tolist() == [n_free, 0]
+
+
 def test_plan_replayed_as_a_graph_in_place():
     """64 replays of a captured one-token plan whose lengths the graph advances."""
     ddb = _ddb()
@@ -260,6 +285,47 @@ def test_attention_matches_reference(shape, case, ps):
         tol = ref.attention_tol(want, mass, reach, "bf16" if dtype is torch.bfloat16 else "f32", D, x)
         assert np.all(np.isfinite(got[b])), f"sequence {b} of {x} keys"
         assert np.all(np.abs(got[b] - want) <= tol), f"sequence {b} of {x} keys: {np.max(np.abs(got[b] - want) - tol)}"
+
+
+def test_pages_beyond_32_bit_offsets():
+    """A cache of 2.3e9 elements each for K and V: rows stored to, attended in and moved between pages at its
+    end give what a small cache gives."""
+    ddb = _ddb()
+    H, D, ps, n = 8, 128, 16, 140000
+    assert n * H * ps * D > 2 ** 31
+    gen = torch.Generator().manual_seed(5)
+    L, B = 150, 2
+    k, v = (torch.randn(B, H, L, D, generator=gen).to(torch.bfloat16).to(DEV) for _ in range(2))
+    q = torch.randn(B, 32, D, generator=gen).to(torch.bfloat16).to(DEV)
+    columns = 11
+    near = torch.arange(B * columns).view(B, columns)
+    out = []
+    for n_pages, table in ((B * columns, near), (n, n - 1 - near)):
+        pk = torch.zeros(n_pages, H, ps, D, dtype=torch.bfloat16, device=DEV)
+        kv = ddb.PagedCache(pk, torch.zeros_like(pk))
+        t = torch.arange(L)
+        slots = (table[:, t // ps] * ps + t % ps).to(torch.int32).contiguous().to(DEV)
+        tab, err = table.to(torch.int32).contiguous().to(DEV), _i32([0])
+        ddb.llama_paged_store(k, v, slots, kv, err_dev=err)
+        o = _attend(ddb, q, kv, tab, [L, L], L, err=err)
+        ddb.llama_beam_reorder(_i32([1, 0]), 2, _i32([L, L]), tab, ddb.PagedCacheList([kv]), err_dev=err)
+        o2 = _attend(ddb, q, kv, tab, [L, L], L, err=err)
+        assert int(err[0]) == 0
+        out.append((o, o2, tab.cpu()))
+        del pk, kv
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    assert not torch.equal(out[0][0], out[0][1]) and torch.equal(out[0][2], (n - 1 - out[1][2]).to(torch.int32))
+
+
+def test_attention_with_an_error_on_record():
+    """An error word that an earlier call set changes nothing."""
+    ddb = _ddb()
+    _, pk, pv, table = _paged([700, 20], 8, 128, 16, torch.bfloat16, 13)
+    kv = ddb.PagedCache(pk, pv)
+    q = torch.randn(2, 32, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    err = _i32([-7])
+    assert torch.equal(_attend(ddb, q, kv, table, [700, 20], 700, err=err), _attend(ddb, q, kv, table, [700, 20], 700))
+    assert int(err[0]) == -7
 
 
 def test_attention_wide_scores():
