@@ -539,6 +539,7 @@ class LlamaBlock:
         if kv.n_kv_heads != self.dims.n_kv_heads or kv.head_dim != self.dims.head_dim or \
                 kv.dtype != self._keep["wq"].dtype:
             raise ValueError("the paged cache's heads or type are not the block's")
+        _current(kv.device)
         _table_arg(table, "table", x.shape[0], None)
         _arg(pos_seq, "pos_seq", torch.int32, x.shape[0])
         llama_block_decode_paged(self.h, x, x.shape[0], kv.c, table, pos_seq, y, ws, ws.numel(), stream)

@@ -133,6 +133,11 @@ class BeamSearch:
         rows = groups * beams
         if beams < 1 or rows > 32:
             raise ValueError("requests x beams must be 1 to 32 rows")
+        group = dims.n_heads // dims.n_kv_heads
+        if dt != torch.bfloat16 or group > 64 or 128 % group:
+            raise ValueError("paged steps take bf16 blocks whose query heads per KV head divide 128 (at most 64)")
+        if beams > stack.vocab:
+            raise ValueError("more beams than tokens to choose from")
         if max_new < 1 or max_new >= stack.max_seq:
             raise ValueError("max_new must leave room for a prompt in the stack's max_seq")
         self.stack, self.beams, self.groups, self.rows = stack, beams, groups, rows
@@ -155,7 +160,8 @@ class BeamSearch:
         self.logits = torch.empty(rows, stack.vocab, dtype=torch.float32, device=dev)
         self.scores = torch.empty(rows, dtype=torch.float32, device=dev)
         self.parents, self.tokens, self.greedy = i32(rows), i32(rows), i32(rows)
-        self.all_parents, self.all_tokens = i32(max_new, rows), i32(max_new, rows)
+        # a row per token, and one for the tokens of replays beyond max_new (sequences refuses them)
+        self.all_parents, self.all_tokens = i32(max_new + 1, rows), i32(max_new + 1, rows)
         self.n = torch.zeros(1, dtype=torch.int64, device=dev)           # tokens chosen so far, on the device
         self.steps = 0                                                   # ... and on the host (begin and step calls)
         self.ws = torch.empty(stack.blocks[0].workspace_bytes(rows, 1), dtype=torch.uint8, device=dev)
@@ -171,8 +177,9 @@ class BeamSearch:
         llama_beam_select(self.logits, self.scores, self.beams, self.beams, self.parents, self.tokens, self.scores,
                           self.select_ws, last=last, eos=self.eos, stream=stream)
         with LlamaStack._on(stream):
-            self.all_parents.index_copy_(0, self.n, self.parents[None])
-            self.all_tokens.index_copy_(0, self.n, self.tokens[None])
+            at = self.n.clamp(max=self.max_new)
+            self.all_parents.index_copy_(0, at, self.parents[None])
+            self.all_tokens.index_copy_(0, at, self.tokens[None])
             self.n.add_(1)
         llama_beam_reorder(self.parents, self.beams, self.pos, self.table, self.caches, err_dev=self.err, stream=stream)
 
@@ -193,6 +200,7 @@ class BeamSearch:
             self.start.copy_(torch.where(first, 0, full))
             self.count.copy_(torch.where(first, T + self.max_new, T - full + self.max_new))
             self.pos.fill_(T)
+            self.table.fill_(-1)   # no page: a step beyond what is planned writes none
             slots = torch.empty(self.rows, T + self.max_new, dtype=torch.int32, device=ids.device)
         llama_paged_plan(self.start, self.count, ps, self.n_pages, self.free, self.pool, self.table, slots,
                          err_dev=self.err, stream=stream)
@@ -235,6 +243,8 @@ class BeamSearch:
         """(tokens [requests, beams, chosen], scores [requests, beams]), best first; waits for the device."""
         torch.cuda.synchronize(self.pos.device)      # the calls may have gone to any stream
         n = int(self.n.item())
+        if n > self.max_new:
+            raise RuntimeError("more than max_new tokens were chosen")
         row = torch.arange(self.rows, device=self.pos.device)
         out = torch.empty(self.rows, n, dtype=torch.int32, device=self.pos.device)
         for t in range(n - 1, -1, -1):
@@ -251,5 +261,6 @@ class BeamSearch:
 
     def poll_error(self) -> int:
         torch.cuda.synchronize(self.pos.device)
-        rc = self.stack.poll_error()
-        return rc if rc else int(self.err.item())
+        rc, own = self.stack.poll_error(), int(self.err.item())
+        self.err.zero_()
+        return rc if rc else own

@@ -164,3 +164,58 @@ def test_beam_search_refusals():
     bs = BeamSearch(st, 2, 50)
     with pytest.raises(ValueError):
         bs.begin(torch.zeros(2, 20, dtype=torch.int32, device=DEV))
+
+
+def test_beam_search_replayed_beyond_its_tokens():
+    """Replays beyond max_new write no page that no beam was given, report an error and give no sequences; the
+    next search is whole again."""
+    from dense_decoder_block_gb300.stack import BeamSearch
+    _, st = _stack(2, 64, 20)
+    ids = workloads.make_token_ids(2, 20, VOCAB, seed=5).to(DEV).to(torch.int32)
+    bs = BeamSearch(st, 4, 6)
+    bs.begin(ids)
+    for _ in range(5):
+        bs.step()
+    want = [t.clone() for t in bs.sequences()]
+    bs.end()
+    bs.begin(ids)
+    bs.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bs.step()
+    planned = set(bs.home[bs.home >= 0].tolist())
+    rest = [p for p in range(bs.n_pages) if p not in planned]
+    assert rest, "the pool has pages that no beam was given"
+    before = [(c.k[rest].clone(), c.v[rest].clone()) for c in bs.caches.caches]
+    for _ in range(20):                              # past the 6 tokens and the planned pages' 32 positions
+        graph.replay()
+    with pytest.raises(RuntimeError):
+        bs.sequences()
+    assert bs.poll_error() != 0
+    for c, (k, v) in zip(bs.caches.caches, before):
+        assert torch.equal(c.k[rest], k) and torch.equal(c.v[rest], v)
+    while bs.poll_error():                           # one block's word after the other
+        pass
+    bs.end()
+    assert bs.pool.tolist() == [bs.n_pages, 0]
+    bs.begin(ids)
+    for _ in range(5):
+        bs.step()
+    got = bs.sequences()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert bs.poll_error() == 0
+
+
+def test_beam_search_refuses_stacks_that_cannot_step():
+    from types import SimpleNamespace
+
+    from dense_decoder_block_gb300.stack import BeamSearch
+    _, st = _stack(2, 64, 20)
+    for heads, dtype, vocab in (((4, 2), torch.float32, VOCAB), ((12, 4), torch.bfloat16, VOCAB),
+                                ((4, 2), torch.bfloat16, 2)):
+        like = SimpleNamespace(dims=SimpleNamespace(n_heads=heads[0], n_kv_heads=heads[1]),
+                               w_embed=torch.zeros(1, dtype=dtype, device=DEV), batch=2, max_seq=64, vocab=vocab,
+                               blocks=st.blocks)
+        with pytest.raises(ValueError):
+            BeamSearch(like, 3, 4)
