@@ -189,9 +189,11 @@ class BeamSearch:
         if self.active:
             raise RuntimeError("end() the running search first")
         st, ps, K = self.stack, self.page_size, self.beams
+        if ids.dim() != 2 or ids.shape[0] != self.groups or ids.dtype != torch.int32:
+            raise ValueError(f"ids must be int32 [{self.groups}, T]")
         T = ids.shape[1]
-        if T + self.max_new > st.max_seq:
-            raise ValueError("prompt and max_new exceed the stack's max_seq")
+        if not 1 <= T <= st.prefill_tokens or T + self.max_new > st.max_seq:
+            raise ValueError("the prompt must fit the stack's prefill, and with max_new its max_seq")
         st.prefill(ids, stream)
         with LlamaStack._on(stream):
             # beam 0 of a request holds the whole prompt, the others its unfilled page on

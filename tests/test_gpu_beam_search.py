@@ -219,3 +219,15 @@ def test_beam_search_refuses_stacks_that_cannot_step():
                                blocks=st.blocks)
         with pytest.raises(ValueError):
             BeamSearch(like, 3, 4)
+
+
+@pytest.mark.parametrize("shape,dtype", [((1, 20), torch.int32), ((2, 20), torch.int64), ((2, 0), torch.int32),
+                                         ((2, 21), torch.int32), ((40,), torch.int32)])
+def test_beam_search_refuses_prompts(shape, dtype):
+    from dense_decoder_block_gb300.stack import BeamSearch
+    _, st = _stack(2, 64, 20)
+    bs = BeamSearch(st, 2, 4)
+    with pytest.raises(ValueError):
+        bs.begin(torch.zeros(shape, dtype=dtype, device=DEV))
+    with pytest.raises(RuntimeError):
+        bs.step()                                    # no search has begun
