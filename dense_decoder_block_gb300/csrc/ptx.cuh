@@ -74,7 +74,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 // Bounded wait.  Returns false (and sets *err) when the budget runs out or when
 // another thread of the grid already reported an expired wait (other errors -- a bad
-// page of one sequence, say -- do not stop the rest).  The error word is read
+// page of one sequence, say -- do not stop the rest).  An expired wait replaces whatever
+// the word holds, since it leaves every row of the call undefined and the other waiters
+// look for it; the other errors (record_error) only fill an empty word.  The word is read
 // only once a wait has lasted kErrPollNs: every waiting warp of every CTA polling
 // one global address would keep that address's L2 slice busy and slow all the
 // loads that go through it.  err may be null: the wait is still bounded, it just
@@ -91,7 +93,7 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* bar, uint32_t parity, in
             const uint64_t dt = globaltimer() - t0;
             if (err && dt > kErrPollNs && (spins & 4095u) == 0 && *((volatile int*)err) == kTimeout) return false;
             if (dt > budget_ns) {
-                if (err) atomicCAS(err, 0, kTimeout);
+                if (err) atomicExch(err, kTimeout);
                 return false;
             }
         }

@@ -199,8 +199,9 @@ int llama_block_decode_seqpos(llama_block blk, const void* x, int batch, const l
                               void* stream);
 
 /* Synchronise `stream`, read and clear the handle's device error word.
- * Returns LLAMA_OK or the code a kernel recorded (LLAMA_ERR_DEVICE_TIMEOUT,
- * LLAMA_ERR_POS_RANGE). */
+ * Returns LLAMA_OK or the first code that a kernel recorded (LLAMA_ERR_POS_RANGE;
+ * of paged steps also LLAMA_ERR_INVALID_ARG); LLAMA_ERR_DEVICE_TIMEOUT replaces
+ * any other code. */
 int llama_block_poll_error(llama_block blk, void* stream);
 
 /* Per-CTA timeline of the block's kernels (RMSNorm, the projections, their
@@ -340,7 +341,8 @@ int llama_sample(const float* logits, int batch, int vocab, float temperature, i
  *
  * Shared by the calls below: positions, lengths, tables, slots and counts are
  * int32 device arrays.  err_dev (device int32, may be NULL) receives the first
- * error that a kernel finds; the caller clears it.  All tensors live on the
+ * error that a kernel finds (LLAMA_ERR_DEVICE_TIMEOUT replaces any other); the
+ * caller clears it.  All tensors live on the
  * current device.  Calls that read or write the same cache, table or pool must be
  * ordered by the caller (one stream, or events).
  * ------------------------------------------------------------------------- */
