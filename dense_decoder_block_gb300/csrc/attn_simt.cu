@@ -549,7 +549,8 @@ __global__ void __launch_bounds__(comb_threads(DH) + 32) k_attn_paged_combine(co
     // per chunk: scale of the past, of the chunk, l times the latter -- an array each, read four
     // chunks at a time
     float* scale = ring + (size_t)n_stages * kCombStage * DH;
-    // lengths are set before the step, never by the kernels this one overlaps
+    // what wrote the lengths has completed: the kernel before this one starts it only after its
+    // own wait
     bool bad;
     const int keys = paged_keys(a.pos_seq[b], p.pos_off, a.max_pos, bad);
     if (tid == 0) {

@@ -1096,6 +1096,11 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
     // The position comes from the host side (set before the step is launched), not
     // from the kernels this one overlaps; cache rows below it were written by
     // earlier steps.  Only q and the newest cache row need griddepcontrol.wait.
+    // So in a block's step, where the projection before this kernel starts it only after its own
+    // wait.  A call of paged attention by itself follows whatever the stream holds -- a kernel
+    // that starts its dependents before it has written a length, a table entry or a cache row
+    // among them -- and reads nothing before it.
+    if (PAGED && a.pos_off < 0) ptx::griddep_wait();
     const int group = a.n_heads / a.n_kv_heads;
     const int n_rep = SETS ? 8 : group, n_sub = SETS ? group / 8 : 1, n_sets = a.n_kv_heads * n_sub;
     __shared__ int s_pre[kSeqPosMax + 1], s_pos[kSeqPosMax];
