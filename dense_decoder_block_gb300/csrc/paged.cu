@@ -26,10 +26,11 @@ namespace {
 // from L2) for the prefix sums it needs and takes a contiguous run of the items --
 // tokens of the slot map [batch][tokens], or table entries [batch][stride].  The
 // CTA that handles a fresh page's first token also writes that page's table entry.
-// All CTAs have read the free count when the last of them takes its ticket (the pool's
-// second word, returned to zero), and that one writes the new count: the pool may be
-// updated in place.  A million slots (256 requests of up to 4096 tokens) take 7.2 us, one
-// CTA's chain of round trips 5.2; the call's host side 12.
+// Which CTA may write the new count: of one CTA, that one; into other words than it is read
+// from, the first; in place under several CTAs none, since another may still be to read it:
+// k_paged_count follows.  (A ticket word beside the count could tell the last CTA, but only
+// where it was zero before the call.)  A million slots (256 requests of up to 4096 tokens) take
+// 7.2 us, one CTA's chain of round trips 5.2; the call's host side 12.
 constexpr int kPlanThreads = 256;
 constexpr int kPlanItems = 8 * kPlanThreads;   // items per CTA
 
@@ -40,8 +41,9 @@ struct PlanArgs {
     int tokens;              // plan: columns of the slot map (counts above it are refused); release: INT_MAX
     int shift, n_pages;
     int* free_pages;         // [n_pages]
-    const int* pool;         // {free pages, 0}
+    const int* pool;         // {free pages, not read}
     int* pool_out;
+    bool write_count;        // this launch writes pool_out
     int* table;
     int stride;
     int* slots;              // plan
@@ -60,6 +62,11 @@ __device__ __forceinline__ bool request_pages(const PlanArgs& a, int b, int& sta
     return ok;
 }
 
+__device__ __forceinline__ void write_pool(const PlanArgs& a, int n_free, long long moved, bool release) {
+    a.pool_out[0] = (int)(n_free + (release ? moved : -moved));
+    a.pool_out[1] = 0;
+}
+
 template <bool RELEASE>
 __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PlanArgs a) {
     __shared__ int s_start[kPlanItems + 2], s_count[kPlanItems + 2], s_off[kPlanItems + 2];   // requests of this CTA
@@ -67,14 +74,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PlanArgs a) {
     __shared__ int s_free;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     ptx::griddep_wait();
-    // the free count is read by one thread, which then takes its CTA's ticket: whoever draws
-    // the last one knows that every CTA has read the count
-    int ticket = 0;
-    if (tid == 0) {
-        s_free = __ldcg(a.pool);
-        __threadfence();
-        ticket = atomicAdd(a.pool_out + 1, 1);
-    }
+    if (tid == 0) s_free = __ldcg(a.pool);
     const long long n_items = RELEASE || a.tokens > 0 ? (long long)a.batch * a.width : 0;   // no slots: the requests are checked alone
     const long long i0 = (long long)blockIdx.x * kPlanItems;
     const long long i1 = i0 + kPlanItems < n_items ? i0 + kPlanItems : n_items;
@@ -198,10 +198,31 @@ __global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const PlanArgs a) {
             a.slots[i0 + e] = slot;
         }
     }
-    if (tid == 0 && ticket == (int)gridDim.x - 1) {
-        a.pool_out[0] = (int)(n_free + (enough ? (RELEASE ? total : -total) : 0));
-        a.pool_out[1] = 0;
+    if (a.write_count && blockIdx.x == 0 && tid == 0) write_pool(a, n_free, enough ? total : 0, RELEASE);
+}
+
+// The new count in place, behind a plan or release of several CTAs: the same sum, the same
+// conditions (recorded there).
+template <bool RELEASE>
+__global__ void __launch_bounds__(kPlanThreads) k_paged_count(const PlanArgs a) {
+    __shared__ unsigned long long s_total;
+    const int tid = threadIdx.x;
+    ptx::griddep_wait();
+    if (tid == 0) s_total = 0;
+    __syncthreads();
+    unsigned long long mine = 0;
+    for (int b = tid; b < a.batch; b += kPlanThreads) {
+        int start, count, held, fresh;
+        request_pages(a, b, start, count, held, fresh);
+        mine += fresh;
     }
+    atomicAdd(&s_total, mine);
+    __syncthreads();
+    if (tid > 0) return;
+    const int n_free = __ldcg(a.pool);
+    const long long total = (long long)s_total;
+    const bool enough = n_free >= 0 && n_free <= a.n_pages && (RELEASE ? total <= a.n_pages - n_free : total <= n_free);
+    write_pool(a, n_free, enough ? total : 0, RELEASE);
 }
 
 // ----------------------------------------------------------------------------- store
@@ -383,9 +404,18 @@ int run_plan(PlanArgs a, cudaStream_t s) {
     const long long items = (long long)a.batch * a.width;
     const long long ctas = std::max<long long>(1, (items + kPlanItems - 1) / kPlanItems);
     if (ctas > INT32_MAX) return LLAMA_ERR_INVALID_ARG;
-    return launch_pdl(k_paged_plan<RELEASE>, dim3((unsigned)ctas), dim3(kPlanThreads), 0, s, a) == cudaSuccess
-               ? LLAMA_OK
-               : LLAMA_ERR_CUDA;
+    a.write_count = ctas == 1 || a.pool_out != a.pool;
+    cudaError_t e = launch_pdl(k_paged_plan<RELEASE>, dim3((unsigned)ctas), dim3(kPlanThreads), 0, s, a);
+    if (e == cudaSuccess && !a.write_count) e = launch_pdl(k_paged_count<RELEASE>, dim3(1), dim3(kPlanThreads), 0, s, a);
+    return e == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
+}
+
+// The pool's two words, in place or apart: not one word's overlap of a pool that is read and one
+// that is written.
+bool pools_ok(const int32_t* pool, const int32_t* pool_out) {
+    if (!pool || !pool_out) return false;
+    const uintptr_t p = (uintptr_t)pool, q = (uintptr_t)pool_out;
+    return p == q || (p > q ? p - q : q - p) >= 2 * sizeof(int32_t);
 }
 
 }  // namespace
@@ -396,7 +426,7 @@ extern "C" int llama_paged_plan(const int32_t* start, const int32_t* count, int 
     if (batch < 0 || tokens < 0 || table_stride <= 0) return LLAMA_ERR_INVALID_ARG;
     const int rc = check_geometry(page_size, n_pages);
     if (rc != LLAMA_OK) return rc;
-    if (!pool || !pool_out) return LLAMA_ERR_INVALID_ARG;
+    if (!pools_ok(pool, pool_out)) return LLAMA_ERR_INVALID_ARG;
     if (batch > 0 && (!start || !count || !free_pages || !table || (tokens > 0 && !slots))) return LLAMA_ERR_INVALID_ARG;
     PlanArgs a{};
     a.start = start;
@@ -422,7 +452,7 @@ extern "C" int llama_paged_release(const int32_t* start, const int32_t* count, i
     if (batch < 0 || table_stride <= 0) return LLAMA_ERR_INVALID_ARG;
     const int rc = check_geometry(page_size, n_pages);
     if (rc != LLAMA_OK) return rc;
-    if (!pool || !pool_out) return LLAMA_ERR_INVALID_ARG;
+    if (!pools_ok(pool, pool_out)) return LLAMA_ERR_INVALID_ARG;
     if (batch > 0 && (!start || !count || !free_pages || !table)) return LLAMA_ERR_INVALID_ARG;
     PlanArgs a{};
     a.start = start;

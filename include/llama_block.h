@@ -365,8 +365,8 @@ typedef struct {
  *     table [batch, table_stride];
  *   - slots [batch, tokens] receives page * page_size + row of each new position
  *     start[b] + t, and -1 for t >= count[b].
- * pool is {number of free pages, 0}; pool_out receives the new one and may be pool
- * (its second word must be 0 before a call and is 0 after it).
+ * pool is {number of free pages, any value}; pool_out receives {the new number, 0}
+ * and may be pool (or two other words).
  * Entries of table that are not filled, and free_pages, are left as they are.  A
  * request with start < 0, count outside 0 .. tokens or more positions than its
  * table row holds gets no page and slots of -1 (LLAMA_ERR_POS_RANGE in err_dev);
