@@ -8,11 +8,20 @@
 //
 // Within a row the order of candidates is the order of its logits (the row's score and
 // normaliser shift all of them alike), so one pass over the logits gives everything:
-// k_beam_scan reads a slice of a row once, keeps it in registers, and leaves the slice's
-// maximum, its sum of exponentials and its n_out best (logit, token) pairs in order;
-// k_beam_merge joins a request's slices.  Slice sums are fp32 (at most kSlice terms of at
-// most 1); everything after them is fp64, since an fp32 cumulative score rounds different
-// logits to equal candidates.
+// k_beam_scan streams a slice of a row through shared memory in chunks, and leaves the
+// slice's maximum, its sum of exponentials and its n_out best (logit, token) pairs in order;
+// k_beam_merge joins a request's slices.
+//
+// A slice's sum (at most kChunksMax * kChunk = 32768 terms of at most 1) is fp32: a lane's
+// two sums add a chunk's 16 terms each, then the chunks; the lanes' and slices' sums are
+// joined in 2^36 fixed point and everything after them is fp64, since an fp32 cumulative score
+// rounds different logits to equal candidates.  In units of u = 2^-24 a term's relative error
+// is 4 (ex2) and, for its distance d from the row's maximum, 2.25 d (two roundings and the
+// rounded log2 e; d averages less than 14 where e^-d weighs 2^20 terms); its additions are 15 in
+// the chunk, 31 over the chunks and 1 of the lane's two sums; a chunk that raises the maximum
+// multiplies the sums by e^(old - new) (5, at most 31 times), as does the slices' join (6): in
+// all at most 4 + 32 + 15 + 31 + 1 + 155 + 6 = 244 u, below 2^-16 in the logarithm.  (One chain
+// through the slice, 512 additions, could be off by 2^-15.)
 //
 // Bound by the read of the logits (115 MB: 17 us at the copy rate) and by what is done to
 // each of them: both launches together take 31.7 us for 32 requests of 8 beams, 128,256
@@ -300,12 +309,15 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) k_beam_scan(const Bea
             }
             if (m != -INFINITY) {
                 const uint64_t down = pack2(-m, -m), scale = pack2(kLog2e, kLog2e);
+                uint64_t part = 0;   // of this chunk: chains of 16 terms and of 32 chunks, not one of 512
 #pragma unroll
                 for (int i = 0; i < kPerLane; i += 2) {
                     float y0, y1;
                     unpack2(mul2(add2(pack2(x[i], x[i + 1]), down), scale), y0, y1);
-                    sums = add2(sums, pack2(ex2(y0), ex2(y1)));
+                    const uint64_t e = pack2(ex2(y0), ex2(y1));
+                    part = i == 0 ? e : add2(part, e);
                 }
+                sums = add2(sums, part);
             }
             if ((c & (c + 1)) == 0) {   // 1, 2, 4, ... chunks
                 // a lane (a half) without a logit has none in any chunk: the row ends in its first

@@ -441,7 +441,10 @@ int llama_block_decode_paged(llama_block blk, const void* x, int batch, const ll
  * (last may be NULL: no beam ends).  Outputs [groups, n_out] in decreasing score,
  * equal scores by increasing beam and then token: parents (row of the beam, in
  * 0 .. groups * beams - 1), tokens, out_scores.  With n_out == beams, out_scores may
- * be scores and tokens may be last.  Candidates are compared in fp64.
+ * be scores and tokens may be last.  Candidates are compared in fp64; each row's
+ * log sum is within 2^-16 of the exact one (fp32 exponentials and sums) and the
+ * same for equal rows of a call, so candidates of different beams may change places
+ * where they are closer than 2^-15, a beam's own never do.
  * Logits must be finite or -inf (probability 0), scores too; continuations of score
  * -inf are listed only when the others are fewer than n_out.  1 <= beams <= 32,
  * 1 <= n_out <= 64, n_out <= vocab <= 2^20, groups * beams <= 65535; otherwise
