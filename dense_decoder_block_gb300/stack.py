@@ -140,11 +140,22 @@ class BeamSearch:
             raise ValueError("more beams than tokens to choose from")
         if max_new < 1 or max_new >= stack.max_seq:
             raise ValueError("max_new must leave room for a prompt in the stack's max_seq")
+        # what a call would refuse in the middle of a search, with pages taken and positions advanced
+        if eos >= stack.vocab:
+            raise ValueError("eos must be a token of the stack's vocabulary, or negative")
+        if stack.vocab > 1 << 20:
+            raise ValueError("the selection takes at most 2^20 tokens")
+        if not 16 <= page_size <= 1024 or page_size & (page_size - 1):
+            raise ValueError("page_size must be a power of two in 16 .. 1024")
+        if len(stack.blocks) > 128:
+            raise ValueError("the reordering takes at most 128 layers")
         self.stack, self.beams, self.groups, self.rows = stack, beams, groups, rows
         self.max_new, self.eos, self.page_size = max_new, eos, page_size
         columns = -(-stack.max_seq // page_size)
         # a request's prompt once and, per beam, the pages of max_new tokens and the unfilled one
         self.n_pages = groups * (columns + beams * (-(-max_new // page_size) + 1))
+        if self.n_pages * page_size * dims.n_kv_heads >= 1 << 31:
+            raise ValueError("the search needs more cache rows than pages can address")
         shape = (self.n_pages, dims.n_kv_heads, page_size, dims.head_dim)
         self.caches = PagedCacheList([PagedCache(torch.zeros(shape, dtype=dt, device=dev),
                                                  torch.zeros(shape, dtype=dt, device=dev)) for _ in stack.blocks])
