@@ -273,7 +273,14 @@ class BeamSearch:
             self.active = False
 
     def poll_error(self) -> int:
+        """The first code on record: of the blocks, of the prompt's ids, of the search's own calls.  A code is
+        cleared when it is returned, and not before."""
         torch.cuda.synchronize(self.pos.device)
-        rc, own = self.stack.poll_error(), int(self.err.item())
-        self.err.zero_()
-        return rc if rc else own
+        rc = self.stack.poll_error()
+        for word in (self.stack.err, self.err):
+            if rc == 0:
+                rc = int(word.item())
+                if rc:
+                    word.zero_()
+                    torch.cuda.synchronize(self.pos.device)
+        return rc
