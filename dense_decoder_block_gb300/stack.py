@@ -125,7 +125,8 @@ class BeamSearch:
         tokens, scores = bs.sequences()
         bs.end()                       # the pages go back to the pool
 
-    eos < 0: no beam ends.  A beam that ended keeps its score and repeats eos."""
+    eos < 0: no beam ends.  A beam that ended keeps its score and repeats eos.  The calls take any stream; those of
+    one search are ordered by the caller (one stream, or events)."""
 
     def __init__(self, stack: LlamaStack, beams: int, max_new: int, eos: int = -1, page_size: int = 16):
         dims, dev, dt = stack.dims, stack.w_embed.device, stack.w_embed.dtype
@@ -182,6 +183,8 @@ class BeamSearch:
                                      dtype=torch.uint8, device=dev)
         self.act = [torch.empty(rows, 1, dims.d_model, dtype=dt, device=dev) for _ in range(2)]
         self.active = False
+        # the calls may go to other streams than the one that filled all this
+        torch.cuda.current_stream(dev).synchronize()
 
     def _choose(self, last, stream) -> None:
         # the best continuations; the states of the beams follow
@@ -263,7 +266,9 @@ class BeamSearch:
         for t in range(n - 1, -1, -1):
             out[:, t] = self.all_tokens[t][row]
             row = self.all_parents[t][row].long()
-        return out.view(self.groups, self.beams, n), self.scores.view(self.groups, self.beams).clone()
+        scores = self.scores.view(self.groups, self.beams).clone()
+        torch.cuda.synchronize(self.pos.device)      # read before a next call on another stream writes
+        return out.view(self.groups, self.beams, n), scores
 
     def end(self, stream: Optional[torch.cuda.Stream] = None) -> None:
         """Give the pages back."""
