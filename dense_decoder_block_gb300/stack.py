@@ -47,6 +47,8 @@ class LlamaStack:
         self.ids = torch.zeros(batch, dtype=torch.int32, device=dev)   # the chosen ids (decode feeds them back)
         self.pos = torch.zeros(1, dtype=torch.int32, device=dev)       # the decode position, on the device
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)       # out-of-range ids from llama_embed
+        # prefill may go to another stream than the one that filled all this
+        torch.cuda.current_stream(dev).synchronize()
 
     @staticmethod
     def _on(stream):
