@@ -145,7 +145,7 @@ inline float2* attn_paged_ml(float* partial, int batch, int n_heads, int n_chunk
 // Decode attention over a paged cache (pos_seq and pages set): CUDA cores, + combine.
 // A sequence without keys, or with a position out of range (recorded), gets a row of zeros.
 cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s);
-// Tensor cores (bf16, attention_tc_supported, at most 8 query heads per KV head), + combine.
+// Tensor cores (bf16, attention_tc_supported, at most 64 query heads per KV head), + combine.
 cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s);
 // LLAMA_OK, or why the pages of kv cannot be used with these heads.

@@ -30,7 +30,7 @@ namespace {
 // from, the first; in place under several CTAs none, since another may still be to read it:
 // k_paged_count follows.  (A ticket word beside the count could tell the last CTA, but only
 // where it was zero before the call.)  A million slots (256 requests of up to 4096 tokens) take
-// 7.2 us, one CTA's chain of round trips 5.2; the call's host side 12.
+// 6.4 us, one CTA's chain of round trips 4.7; the call's host side 12.
 constexpr int kPlanThreads = 256;
 constexpr int kPlanItems = 8 * kPlanThreads;   // items per CTA
 

@@ -407,7 +407,9 @@ int llama_paged_store(const void* k, const void* v, int batch, int tokens, int s
  * sequence attends is recorded (LLAMA_ERR_INVALID_ARG) and leaves that sequence's
  * row undefined.  Cache rows and table entries behind the length are not used,
  * whatever they hold.  At most 64 query heads per KV head.  The result is, bit for
- * bit, the attention that llama_block_decode computes from the same rows. */
+ * bit, the attention that llama_block_decode computes from the same rows: where that
+ * runs on the tensor cores (bf16, groups that divide 128), softmax weights are rounded
+ * to bf16 before their product with V and their sum (both held in fp32). */
 size_t llama_paged_attention_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_dim, int max_len);
 int llama_paged_attention(const void* q, int batch, int n_heads, int n_kv_heads, int head_dim, int dtype,
                           const llama_paged_cache* kv, const int32_t* table, int table_stride, const int32_t* lens,
