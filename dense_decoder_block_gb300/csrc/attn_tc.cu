@@ -1144,7 +1144,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         __syncthreads();
         if (s_bad) {
             if (threadIdx.x == 0 && blockIdx.x == 0) record_error(a.err, LLAMA_ERR_POS_RANGE);
-            if (!PAGED) return;
+            if (!PAGED) {
+                ptx::griddep_wait();   // no grid completes before the ones in front of it
+                return;
+            }
         }
         dm.pre = s_pre;
         dm.spos = s_pos;
@@ -1153,6 +1156,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_attn_tc_dec(const __grid_con
         const int pos = a.pos_dev ? *a.pos_dev : a.start_pos;
         if (pos < 0 || pos >= a.max_pos) {
             if (threadIdx.x == 0 && blockIdx.x == 0) record_error(a.err, LLAMA_ERR_POS_RANGE);
+            ptx::griddep_wait();
             return;
         }
         dm.pos = pos;
