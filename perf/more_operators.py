@@ -189,7 +189,7 @@ def prepare(case, seed):
         if op == "fork":
             state["cache"] = ddb.PagedCacheList([ddb.PagedCache(k, v) for k, v in zip(state["pk"], state["pv"])])
             need = max(ddb.llama_paged_fork_workspace_bytes(state["src"].numel()),
-                       ddb.llama_paged_free_workspace_bytes(state["n_pages"]))
+                       ddb.llama_paged_free_workspace_bytes(state["src"].numel(), state["n_pages"]))
         state["ws"] = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
     return state
 
