@@ -36,6 +36,9 @@ __all__ = [
     "PagedCache", "PagedCacheList", "llama_paged_plan", "llama_paged_release", "llama_paged_store",
     "llama_paged_attention", "llama_paged_attention_workspace_bytes", "llama_block_decode_paged",
     "llama_beam_select", "llama_beam_select_workspace_bytes", "llama_beam_reorder",
+    "llama_paged_chunk_attention", "llama_paged_chunk_attention_workspace_bytes",
+    "llama_paged_fork", "llama_paged_fork_workspace_bytes", "llama_paged_free", "llama_paged_free_workspace_bytes",
+    "llama_token_logprobs",
 ]
 
 
@@ -296,6 +299,32 @@ def _err_arg(err_dev, device):
     return None if err_dev is None else _arg(err_dev, "err_dev", torch.int32, 1, device)
 
 
+def llama_token_logprobs(logits, tokens, logprobs, entropy=None, top_ids=None, top_logprobs=None, err_dev=None,
+                         stream=None) -> None:
+    """Log probabilities of tokens [rows] under fp32 logits [rows, vocab] (a negative token: the row is skipped), the
+    rows' entropies, and their top alternatives (top_ids, top_logprobs [rows, n]); tokens and logprobs may both be None."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    rows, vocab = logits.shape
+    if (tokens is None) != (logprobs is None) or (top_ids is None) != (top_logprobs is None):
+        raise ValueError("tokens and logprobs, top_ids and top_logprobs: both or neither")
+    if top_ids is not None and (top_ids.dim() != 2 or top_ids.shape[0] != rows or top_ids.shape != top_logprobs.shape):
+        raise ValueError("top_ids and top_logprobs must be [rows, alternatives]")
+    n = 0 if top_ids is None else top_ids.shape[1]
+    dev = torch.cuda.current_device()
+
+    def opt(t, name, dtype, least):
+        return None if t is None else _arg(t, name, dtype, least, dev)
+
+    rc = lib().llama_token_logprobs(_arg(logits, "logits", torch.float32, 0, dev), rows, vocab,
+                                    opt(tokens, "tokens", torch.int32, rows), n, opt(logprobs, "logprobs", torch.float32, rows),
+                                    opt(entropy, "entropy", torch.float32, rows), opt(top_ids, "top_ids", torch.int32, rows * n),
+                                    opt(top_logprobs, "top_logprobs", torch.float32, rows * n), _err_arg(err_dev, dev),
+                                    _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_token_logprobs")
+
+
 class PagedCache:
     """One layer's paged K and V: [n_pages, n_kv_heads, page_size, head_dim] each
     (caller-owned torch tensors)."""
@@ -417,6 +446,78 @@ def llama_paged_attention(q, kv: PagedCache, table, lens, max_len: int, o, ws, e
                                      _stream(stream))
     if rc != LLAMA_OK:
         raise LlamaError(rc, "llama_paged_attention")
+
+
+def llama_paged_chunk_attention_workspace_bytes(batch, tokens, n_heads, n_kv_heads, head_dim, max_len) -> int:
+    return int(lib().llama_paged_chunk_attention_workspace_bytes(batch, tokens, n_heads, n_kv_heads, head_dim, max_len))
+
+
+def llama_paged_chunk_attention(q, kv: PagedCache, table, start, count, max_len: int, o, ws, err_dev=None,
+                                stream=None) -> None:
+    """o[b, t] = attention of q[b, t] [n_heads, head_dim] over positions 0 .. start[b] + t of sequence b, t < count[b]
+    (the other rows of o are left as they were); q, o [batch, tokens, n_heads, head_dim], start + count <= max_len."""
+    dev = kv.device
+    if q.dim() != 4 or q.shape[3] != kv.head_dim or o.shape != q.shape:
+        raise ValueError("q and o must be [batch, tokens, n_heads, head_dim] of the cache's heads")
+    batch, tokens, n_heads = q.shape[0], q.shape[1], q.shape[2]
+    _current(dev)
+    rc = lib().llama_paged_chunk_attention(_arg(q, "q", kv.dtype, 0, dev), batch, tokens, n_heads, kv.n_kv_heads, kv.head_dim,
+                                           kv.code, kv.ref, _table_arg(table, "table", batch, dev), table.shape[1],
+                                           _arg(start, "start", torch.int32, batch, dev),
+                                           _arg(count, "count", torch.int32, batch, dev), max_len,
+                                           _arg(o, "o", kv.dtype, 0, dev), _arg(ws, "ws", torch.uint8, 0, dev), ws.numel(),
+                                           _err_arg(err_dev, dev), _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_paged_chunk_attention")
+
+
+def llama_paged_fork_workspace_bytes(n) -> int:
+    return int(lib().llama_paged_fork_workspace_bytes(n))
+
+
+def llama_paged_fork(src, dst, lens, refs, free_pages, pool, table, caches: PagedCacheList, ws, pool_out=None,
+                     err_dev=None, stream=None) -> None:
+    """Row dst[i] of table continues the first lens[i] positions of row src[i]: full pages are shared (refs [n_pages]
+    counts the further holders of each), the unfilled one is copied to a page from the stack, in every layer."""
+    f = caches.first
+    dev = f.device
+    n = src.numel()
+    if dst.numel() != n or lens.numel() != n:
+        raise ValueError("src, dst and lens must agree")
+    _current(dev)
+    out = pool if pool_out is None else pool_out
+    rc = lib().llama_paged_fork(_arg(src, "src", torch.int32, n, dev), _arg(dst, "dst", torch.int32, n, dev),
+                                _arg(lens, "lens", torch.int32, n, dev), n, _arg(refs, "refs", torch.int32, f.n_pages, dev),
+                                _arg(free_pages, "free_pages", torch.int32, f.n_pages, dev),
+                                _arg(pool, "pool", torch.int32, 2, dev), _arg(out, "pool_out", torch.int32, 2, dev),
+                                _table_arg(table, "table", 1, dev), table.shape[0], table.shape[1], caches.c, len(caches),
+                                f.n_kv_heads, f.head_dim, f.code, _arg(ws, "ws", torch.uint8, 0, dev), ws.numel(),
+                                _err_arg(err_dev, dev), _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_paged_fork")
+
+
+def llama_paged_free_workspace_bytes(n, n_pages) -> int:
+    return int(lib().llama_paged_free_workspace_bytes(n, n_pages))
+
+
+def llama_paged_free(rows, lens, page_size: int, n_pages: int, refs, free_pages, pool, table, ws, pool_out=None,
+                     err_dev=None, stream=None) -> None:
+    """Rows rows[i] of table give up the pages of their first lens[i] positions; pages that no row holds any more go
+    back on the stack."""
+    dev = torch.cuda.current_device()
+    n = rows.numel()
+    if lens.numel() != n:
+        raise ValueError("rows and lens must agree")
+    out = pool if pool_out is None else pool_out
+    rc = lib().llama_paged_free(_arg(rows, "rows", torch.int32, n, dev), _arg(lens, "lens", torch.int32, n, dev), n, page_size,
+                                n_pages, _arg(refs, "refs", torch.int32, n_pages, dev),
+                                _arg(free_pages, "free_pages", torch.int32, n_pages, dev),
+                                _arg(pool, "pool", torch.int32, 2, dev), _arg(out, "pool_out", torch.int32, 2, dev),
+                                _table_arg(table, "table", 1, dev), table.shape[0], table.shape[1],
+                                _arg(ws, "ws", torch.uint8, 0, dev), ws.numel(), _err_arg(err_dev, dev), _stream(stream))
+    if rc != LLAMA_OK:
+        raise LlamaError(rc, "llama_paged_free")
 
 
 def llama_beam_select_workspace_bytes(groups, beams, vocab, n_out) -> int:

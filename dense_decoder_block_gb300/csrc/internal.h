@@ -150,6 +150,13 @@ cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s);
 // LLAMA_OK, or why the pages of kv cannot be used with these heads.
 int paged_cache_check(const llama_paged_cache* kv, int n_kv_heads, int head_dim, int dtype);
+// LLAMA_OK, or why a cache cannot have such pages.
+int paged_geometry_check(int page_size, int n_pages);
+// 16-byte vectors of a row (log2), or -1 for a type and head size the cache does not take.
+int paged_row_log_vec(int head_dim, int dtype);
+// The pool's two words, in place or apart: not one word's overlap of a pool that is read and one
+// that is written.
+bool paged_pools_ok(const int32_t* pool, const int32_t* pool_out);
 // Tensor-core attention (bf16, head_dim 128, n_heads / n_kv_heads dividing 128).
 bool attention_tc_supported(int n_heads, int n_kv_heads, int head_dim);
 cudaError_t launch_attention_tc_prefill(const AttnArgs& a, cudaStream_t s);

@@ -363,14 +363,15 @@ __global__ void __launch_bounds__(kReorderThreads) k_beam_reorder(const __grid_c
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
-// 16-byte vectors of a row (log2), or -1 for a type and head size the cache does not take.
-int row_log_vec(int head_dim, int dtype) {
+}  // namespace
+
+int paged_row_log_vec(int head_dim, int dtype) {
     if (dtype == LLAMA_BF16) return head_dim == 128 ? 4 : -1;
     if (dtype != LLAMA_F32) return -1;
     return head_dim == 32 ? 3 : head_dim == 64 ? 4 : head_dim == 128 ? 5 : -1;
 }
 
-int check_geometry(int page_size, int n_pages) {
+int paged_geometry_check(int page_size, int n_pages) {
     if (n_pages <= 0) return LLAMA_ERR_INVALID_ARG;
     if (!page_size_ok(page_size)) return LLAMA_ERR_UNSUPPORTED_DIMS;
     // slots are int32
@@ -378,14 +379,18 @@ int check_geometry(int page_size, int n_pages) {
     return LLAMA_OK;
 }
 
-}  // namespace
+bool paged_pools_ok(const int32_t* pool, const int32_t* pool_out) {
+    if (!pool || !pool_out) return false;
+    const uintptr_t p = (uintptr_t)pool, q = (uintptr_t)pool_out;
+    return p == q || (p > q ? p - q : q - p) >= 2 * sizeof(int32_t);
+}
 
 int paged_cache_check(const llama_paged_cache* kv, int n_kv_heads, int head_dim, int dtype) {
     if (!kv || !kv->k || !kv->v || !aligned16(kv->k) || !aligned16(kv->v)) return LLAMA_ERR_INVALID_ARG;
     if (dtype != LLAMA_BF16 && dtype != LLAMA_F32) return LLAMA_ERR_INVALID_ARG;
     if (n_kv_heads <= 0) return LLAMA_ERR_INVALID_ARG;
-    if (row_log_vec(head_dim, dtype) < 0) return LLAMA_ERR_UNSUPPORTED_DIMS;
-    const int rc = check_geometry(kv->page_size, kv->n_pages);
+    if (paged_row_log_vec(head_dim, dtype) < 0) return LLAMA_ERR_UNSUPPORTED_DIMS;
+    const int rc = paged_geometry_check(kv->page_size, kv->n_pages);
     if (rc != LLAMA_OK) return rc;
     // rows of the cache are addressed by int32 coordinates (TMA) and the heads by a grid dimension
     if (n_kv_heads > 65535 || (long long)kv->n_pages * kv->page_size * n_kv_heads > INT32_MAX)
@@ -410,23 +415,15 @@ int run_plan(PlanArgs a, cudaStream_t s) {
     return e == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
 }
 
-// The pool's two words, in place or apart: not one word's overlap of a pool that is read and one
-// that is written.
-bool pools_ok(const int32_t* pool, const int32_t* pool_out) {
-    if (!pool || !pool_out) return false;
-    const uintptr_t p = (uintptr_t)pool, q = (uintptr_t)pool_out;
-    return p == q || (p > q ? p - q : q - p) >= 2 * sizeof(int32_t);
-}
-
 }  // namespace
 
 extern "C" int llama_paged_plan(const int32_t* start, const int32_t* count, int batch, int tokens, int page_size,
                                 int n_pages, const int32_t* free_pages, const int32_t* pool, int32_t* pool_out,
                                 int32_t* table, int table_stride, int32_t* slots, int32_t* err_dev, void* stream) {
     if (batch < 0 || tokens < 0 || table_stride <= 0) return LLAMA_ERR_INVALID_ARG;
-    const int rc = check_geometry(page_size, n_pages);
+    const int rc = paged_geometry_check(page_size, n_pages);
     if (rc != LLAMA_OK) return rc;
-    if (!pools_ok(pool, pool_out)) return LLAMA_ERR_INVALID_ARG;
+    if (!paged_pools_ok(pool, pool_out)) return LLAMA_ERR_INVALID_ARG;
     if (batch > 0 && (!start || !count || !free_pages || !table || (tokens > 0 && !slots))) return LLAMA_ERR_INVALID_ARG;
     PlanArgs a{};
     a.start = start;
@@ -450,9 +447,9 @@ extern "C" int llama_paged_release(const int32_t* start, const int32_t* count, i
                                    int32_t* free_pages, const int32_t* pool, int32_t* pool_out, const int32_t* table,
                                    int table_stride, int32_t* err_dev, void* stream) {
     if (batch < 0 || table_stride <= 0) return LLAMA_ERR_INVALID_ARG;
-    const int rc = check_geometry(page_size, n_pages);
+    const int rc = paged_geometry_check(page_size, n_pages);
     if (rc != LLAMA_OK) return rc;
-    if (!pools_ok(pool, pool_out)) return LLAMA_ERR_INVALID_ARG;
+    if (!paged_pools_ok(pool, pool_out)) return LLAMA_ERR_INVALID_ARG;
     if (batch > 0 && (!start || !count || !free_pages || !table)) return LLAMA_ERR_INVALID_ARG;
     PlanArgs a{};
     a.start = start;
@@ -491,7 +488,7 @@ extern "C" int llama_paged_store(const void* k, const void* v, int batch, int to
     a.src_pos = src_pos;
     a.n_kv_heads = n_kv_heads;
     a.shift = page_shift(kv->page_size);
-    a.log_vec = row_log_vec(head_dim, dtype);
+    a.log_vec = paged_row_log_vec(head_dim, dtype);
     a.n_slots = (long long)kv->n_pages * kv->page_size;
     a.err = err_dev;
     const long long vecs = (long long)tokens << a.log_vec;
@@ -527,7 +524,7 @@ extern "C" int llama_beam_reorder(const int32_t* parents, int groups, int beams,
     a.shift = page_shift(caches[0].page_size);
     a.n_pages = caches[0].n_pages;
     a.n_kv_heads = n_kv_heads;
-    a.log_vec = row_log_vec(head_dim, dtype);
+    a.log_vec = paged_row_log_vec(head_dim, dtype);
     a.n_layers = n_layers;
     a.err = err_dev;
     const long long most = ((long long)n_kv_heads * (caches[0].page_size - 1)) << a.log_vec;   // vectors of one page

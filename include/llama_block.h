@@ -334,6 +334,24 @@ int llama_lmhead_argmax_noalloc(const void* h, int batch, int h_stride, const vo
 int llama_sample(const float* logits, int batch, int vocab, float temperature, int top_k, float top_p,
                  const float* uniforms, int32_t* ids, void* stream);
 
+/* Log probabilities of given tokens under fp32 logits [rows, vocab] ("How Llama 3.1
+ * Generates the Next Token", Softmax), with the entropy and the top alternatives:
+ *   logprobs[r] = logits[r][tokens[r]] - log sum_v e^(logits[r][v])
+ *   entropy[r]  = - sum_v p_v log p_v (natural logarithm; a logit of -inf adds nothing)
+ *   top_ids, top_logprobs [rows, n_top]: the n_top largest logits in decreasing order, equal
+ *     ones by increasing token, and their log probabilities.
+ * A row with tokens[r] < 0 takes no part: its logits are not read and its outputs are left
+ * as they were; one with tokens[r] >= vocab too, and it is recorded (LLAMA_ERR_INVALID_ARG in
+ * err_dev).  tokens may be NULL (every row takes part; logprobs is NULL too), entropy may be
+ * NULL, n_top 0 (top_ids and top_logprobs are then not used).  Logits of -inf have
+ * probability 0; a row of them alone has log probabilities of -inf, entropy 0 and the lowest
+ * tokens on top.  A row with a NaN or +inf gets NaN log probabilities and entropy, and tokens
+ * of its own vocabulary as alternatives.  Sums are held in fp32 per thread and in fp64 across
+ * threads; exponentials and logarithms are fp32 ones except the last.  0 <= n_top <= 32, n_top
+ * <= vocab <= 2^20. */
+int llama_token_logprobs(const float* logits, int rows, int vocab, const int32_t* tokens, int n_top, float* logprobs,
+                         float* entropy, int32_t* top_ids, float* top_logprobs, int32_t* err_dev, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Paged KV cache: serving ragged requests from one pool of pages.  The pages give
  * the cache's contents ("Llama 3 8B · Prepare Q, K, V", Explanation: K and V per
@@ -429,6 +447,71 @@ int llama_paged_attention(const void* q, int batch, int n_heads, int n_kv_heads,
 int llama_block_decode_paged(llama_block blk, const void* x, int batch, const llama_paged_cache* kv,
                              const int32_t* table, int table_stride, const int32_t* pos_seq, void* y,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* Attention of a chunk of new tokens per sequence over its pages: q, o [batch, tokens,
+ * n_heads, head_dim].  Sequence b has count[b] new tokens (0 .. tokens) at positions
+ * start[b] .. start[b] + count[b] - 1, the start and count of its llama_paged_plan; their
+ * keys and values are in the cache already (llama_paged_store).  Token t attends
+ * positions 0 .. start[b] + t; heads and scale as in llama_paged_attention.  Rows of o at
+ * t >= count[b] are left as they were, and those of q are not used.  max_len bounds
+ * start + count.  A sequence with start < 0, a count outside 0 .. tokens, or more positions
+ * than max_len or its table row holds is recorded (LLAMA_ERR_POS_RANGE) and its rows are left
+ * as they were; a page id outside [0, n_pages) among the pages that it attends is recorded
+ * (LLAMA_ERR_INVALID_ARG) and leaves that sequence's rows undefined.  Cache rows and table
+ * entries behind the last position are not used, and a token's row does not depend on the
+ * keys and values behind its position, whatever they hold (infinities and NaN included).  A
+ * row is NaN where no finite softmax exists.  bf16 (head_dim 128): products on the tensor
+ * cores, weights rounded to bf16 before their product with V and their sum (both held in
+ * fp32); fp32 (head_dim 32, 64, 128): fp32 throughout.  At most 64 query heads per KV
+ * head, batch * tokens < 2^31, batch <= 65535.  Where there are fewer query rows than the
+ * device has room for, the positions of a row are split and joined: the split follows from
+ * the call's sizes, starts and counts, so equal calls give equal bits, and a row's last bit
+ * may depend on the other sequences of the call. */
+size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads, int head_dim,
+                                                   int max_len);
+int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_heads, int n_kv_heads, int head_dim,
+                                int dtype, const llama_paged_cache* kv, const int32_t* table, int table_stride,
+                                const int32_t* start, const int32_t* count, int max_len, void* o, void* workspace,
+                                size_t workspace_bytes, int32_t* err_dev, void* stream);
+
+/* Samples of one prompt share its pages.  refs [n_pages] counts, for each page, the rows
+ * that hold it beside the first: all zeros at first, and of no concern to the calls above.
+ *
+ * Fork i (of n): row dst[i] of table [table_rows, table_stride] continues the first lens[i]
+ * positions of row src[i], c = lens / page_size full pages and r = lens % page_size rows of
+ * the page after them.  Entries 0 .. c-1 become those of the source row, and refs of each
+ * of these pages grows by one; if r > 0, entry c becomes a page from the top of the stack
+ * of free pages (in the order of the forks, as in llama_paged_plan) and receives rows
+ * 0 .. r-1 of the source's page c in the caches of all n_layers (as in
+ * llama_beam_reorder).  Other entries are left as they are.  pool and pool_out as in
+ * llama_paged_plan.  A fork whose rows lie outside the table, whose dst is listed twice or is
+ * also listed as a source is left out (LLAMA_ERR_INVALID_ARG in err_dev), one whose length
+ * lies outside 0 .. table_stride * page_size too (LLAMA_ERR_POS_RANGE); with too few free
+ * pages nothing is changed (LLAMA_ERR_NO_PAGES); an entry that is no page of the cache
+ * is recorded (LLAMA_ERR_INVALID_ARG), passed on and nothing else is done with it.  n <= 65535,
+ * table_rows <= 65536.  workspace: llama_paged_fork_workspace_bytes(n). */
+size_t llama_paged_fork_workspace_bytes(int n);
+int llama_paged_fork(const int32_t* src, const int32_t* dst, const int32_t* lens, int n, int32_t* refs,
+                     const int32_t* free_pages, const int32_t* pool, int32_t* pool_out, int32_t* table, int table_rows,
+                     int table_stride, const llama_paged_cache* caches, int n_layers, int n_kv_heads, int head_dim,
+                     int dtype, void* workspace, size_t workspace_bytes, int32_t* err_dev, void* stream);
+
+/* Rows rows[i] (of n) give up the pages of their first lens[i] positions: a page with
+ * further holders (refs > 0) loses one of them, a page without goes back on the stack.
+ * Several rows that hold a page may give it up in one call; it goes back at the last of
+ * them in the order of rows and of pages within a row, and the pages that go back lie on
+ * the stack in that order, the first on top: for rows without shared pages this is
+ * llama_paged_release with start = 0 and count = lens.  Entries of table are left as
+ * they are.  A row outside the table or listed twice is left out (LLAMA_ERR_INVALID_ARG),
+ * one with a length outside 0 .. table_stride * page_size too (LLAMA_ERR_POS_RANGE); an
+ * entry that is no page is recorded (LLAMA_ERR_INVALID_ARG) and skipped, and so is what a
+ * page is given up more often than it is held; when the stack has no room for all pages
+ * nothing is changed (LLAMA_ERR_NO_PAGES).  n * table_stride < 2^31, n <= 65536, table_rows <=
+ * 65536.  workspace: llama_paged_free_workspace_bytes(n, n_pages). */
+size_t llama_paged_free_workspace_bytes(int n, int n_pages);
+int llama_paged_free(const int32_t* rows, const int32_t* lens, int n, int page_size, int n_pages, int32_t* refs,
+                     int32_t* free_pages, const int32_t* pool, int32_t* pool_out, const int32_t* table, int table_rows,
+                     int table_stride, void* workspace, size_t workspace_bytes, int32_t* err_dev, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Beam search ("How Llama 3.1 Generates the Next Token", Sampling, names greedy
