@@ -5,25 +5,11 @@
 #include <algorithm>
 #include <cmath>
 
+#include "attn_chunk.cuh"
 #include "internal.h"
-#include "paged.cuh"
-#include "ptx.cuh"
 
 namespace llama {
 namespace {
-
-struct ChunkArgs {
-    const void* q;
-    void* o;
-    const void* kc;
-    const void* vc;
-    int batch, tokens, n_heads, n_kv_heads, max_pos;
-    const int* start;
-    const int* count;
-    PageTable pages;
-    float scale_log2;
-    int* err;
-};
 
 __device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f(float v) { return v; }
@@ -83,6 +69,8 @@ cudaError_t launch_rows(const ChunkArgs& a, cudaStream_t s) {
     return launch_pdl(k_attn_chunk_rows<T, DH>, dim3((unsigned)ctas, a.batch), dim3(256), 0, s, a);
 }
 
+size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }
+
 bool heads_ok(int n_heads, int n_kv_heads, int head_dim) {
     return n_heads > 0 && n_kv_heads > 0 && n_heads <= 65535 && n_heads % n_kv_heads == 0 &&
            n_heads / n_kv_heads <= 64 && (head_dim == 32 || head_dim == 64 || head_dim == 128);
@@ -96,7 +84,8 @@ using namespace llama;
 extern "C" size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads,
                                                               int head_dim, int max_len) {
     if (batch <= 0 || tokens <= 0 || max_len <= 0 || !heads_ok(n_heads, n_kv_heads, head_dim)) return 0;
-    return 16;
+    // two partials (m, l, o) of up to 128 rows for each CTA, and where the CTAs begin
+    return align16((size_t)kChunkMaxCtas * 128 * (head_dim + 2) * sizeof(float)) + kChunkMaxCtas * sizeof(int4);
 }
 
 extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_heads, int n_kv_heads,
@@ -132,9 +121,12 @@ extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens,
     a.max_pos = room < max_len ? (int)room : max_len;
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
     a.err = err_dev;
+    a.partial = (float*)ws;
+    a.part_ml = (float2*)(a.partial + (size_t)kChunkMaxCtas * 128 * head_dim);
+    a.cuts = (int4*)((uint8_t*)ws + align16((size_t)kChunkMaxCtas * 128 * (head_dim + 2) * sizeof(float)));
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (dtype == LLAMA_BF16) e = launch_rows<bf16, 128>(a, s);
+    if (dtype == LLAMA_BF16) { a.tq = 128 / (n_heads / n_kv_heads); e = launch_chunk_tc(a, head_dim, s); }
     else if (head_dim == 32) e = launch_rows<float, 32>(a, s);
     else if (head_dim == 64) e = launch_rows<float, 64>(a, s);
     else e = launch_rows<float, 128>(a, s);

@@ -1,0 +1,188 @@
+// The work of a chunk attention call, shared by its kernels: which keys of which query tile a CTA takes.
+//
+// A tile is `tq` consecutive new tokens of a sequence under one KV head (tq x the group's heads rows);
+// its work is the keys that its last token attends and a constant for starting and storing a tile.  All
+// tiles -- sequences in order, their KV heads, their tiles -- lie one after another on a line, and CTA i
+// of n takes the stretch [W i / n, W (i + 1) / n) of the line's length W, cut at chunks of
+// kAttnChunk keys (cut below): a tile that crosses the end of a stretch is shared by several CTAs, each of
+// which leaves the softmax partial (m, l, o) of its chunks, and a second kernel joins them.  Lengths
+// and counts are read on the device, so the balance holds for any mixture of sequences under any bound.
+#pragma once
+#include "common.cuh"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace llama {
+
+constexpr int kChunkSeqs = 1024;      // sequences of a launch
+constexpr int kChunkMaxCtas = 304;    // CTAs of a launch: two partials each (workspace)
+
+struct ChunkArgs {
+    const void* q;       // [batch, tokens, n_heads, head_dim]
+    void* o;
+    const void* kc;
+    const void* vc;
+    int batch, tokens, n_heads, n_kv_heads, max_pos;
+    const int* start;
+    const int* count;
+    PageTable pages;
+    float scale_log2;
+    int tq;              // tokens per tile
+    bool whole;          // tiles are not split
+    float* partial;      // [2 CTAs][head_dim / 4][rows] float4
+    float2* part_ml;     // [2 CTAs][rows]
+    int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it
+    int* err;
+};
+cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s);
+
+// Work of a tile in keys, beside the keys themselves: filling and draining the pipeline, q and o.
+constexpr int kTileKeys = 128;
+// The least chunks of a piece: what joining costs.
+constexpr int kMinPiece = 2;
+// The least work of a CTA (keys) for which another one is started.
+constexpr int kMinStretch = 512;
+
+// The sequences of a launch (shared memory).
+struct ChunkSeqs {
+    int start[kChunkSeqs], count[kChunkSeqs];
+    long long pre[kChunkSeqs + 1];   // work of the sequences before, one KV head
+};
+
+// Work of the first n tiles (all of tq tokens) of a sequence.
+__device__ __forceinline__ long long tiles_work(int start, int tq, int n) {
+    return (long long)n * (start + kTileKeys) + (long long)tq * n * (n + 1) / 2;
+}
+
+// Fills s (one warp).  A sequence whose words are out of range has no tile; `record`: it is recorded.
+__device__ __forceinline__ void chunk_seqs(const ChunkArgs& a, ChunkSeqs& s, bool record) {
+    const int lane = threadIdx.x & 31;
+    long long run = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int start = 0, count = 0;
+        if (b < a.batch) {
+            start = __ldcg(a.start + b);
+            count = __ldcg(a.count + b);
+            if (start < 0 || count < 0 || count > a.tokens || (long long)start + count > a.max_pos) {
+                if (record) record_error(a.err, LLAMA_ERR_POS_RANGE);
+                count = 0;
+            }
+            s.start[b] = start;
+            s.count[b] = count;
+        }
+        const int n = (count + a.tq - 1) / a.tq;
+        long long w = n > 0 ? tiles_work(start, a.tq, n - 1) + start + count + kTileKeys : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += v;
+        }
+        if (b < a.batch) s.pre[b + 1] = run + w;
+        run += __shfl_sync(0xffffffffu, w, 31);
+    }
+    if (lane == 0) s.pre[0] = 0;
+}
+
+// The chunk of a tile (n chunks, `work` in all) at which a stretch ends that ends `x` behind the tile's
+// beginning: 0 and n when the tile belongs to one side whole.
+__device__ __forceinline__ int chunk_cut(long long x, int n, long long work, bool whole) {
+    if (x <= 0) return 0;
+    if (x >= work) return n;
+    if (whole) return 2 * x >= work ? n : 0;
+    const int c = (int)((x + kAttnChunk / 2) / kAttnChunk);
+    return c < kMinPiece ? 0 : c > n - kMinPiece ? n : c;
+}
+
+// Chunks [c0, c1) of one tile.
+struct ChunkPiece {
+    int b, g, y;
+    int t0, t1;       // tokens
+    int pos0;         // position of t0
+    int kv_last;      // position of t1 - 1
+    int c0, c1, n;    // of n chunks
+};
+
+// A CTA's pieces in order.  Every role of a kernel walks them by itself.
+struct ChunkWalk {
+    const ChunkSeqs& s;
+    int batch, n_kv, tq;
+    bool whole;
+    long long w, w0, w1;   // beginning of the tile at hand, the stretch
+    int b, g, y, n_qt, start, count;
+
+    __device__ __forceinline__ ChunkWalk(const ChunkArgs& a, const ChunkSeqs& seqs, int cta, int n_ctas)
+        : s(seqs), batch(a.batch), n_kv(a.n_kv_heads), tq(a.tq), whole(a.whole) {
+        const long long total = s.pre[batch] * n_kv;
+        const int n = (int)min((long long)n_ctas, max(1ll, total / kMinStretch));
+        b = batch;
+        w = w0 = w1 = 0;
+        g = y = n_qt = start = count = 0;
+        if (cta >= n || total == 0) return;
+        w0 = total * cta / n;
+        w1 = total * (cta + 1) / n;
+        int lo = 0, hi = batch - 1;   // the last sequence that begins at or before w0: one with work
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s.pre[mid] * n_kv <= w0) lo = mid;
+            else hi = mid - 1;
+        }
+        b = lo;
+        load();
+        const long long one = s.pre[b + 1] - s.pre[b];
+        long long r = w0 - s.pre[b] * n_kv;
+        g = (int)(r / one);
+        r -= g * one;
+        lo = 0;
+        hi = n_qt - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tiles_work(start, tq, mid) <= r) lo = mid;
+            else hi = mid - 1;
+        }
+        y = lo;
+        w = w0 - r + tiles_work(start, tq, y);
+    }
+    __device__ __forceinline__ void load() {
+        start = s.start[b];
+        count = s.count[b];
+        n_qt = (count + tq - 1) / tq;
+    }
+    // The next piece; false behind the last.
+    __device__ __forceinline__ bool next(ChunkPiece& p) {
+        while (b < batch && w < w1) {
+            p.b = b;
+            p.g = g;
+            p.y = y;
+            p.t0 = y * tq;
+            p.t1 = min(p.t0 + tq, count);
+            p.pos0 = start + p.t0;
+            p.kv_last = start + p.t1 - 1;
+            p.n = p.kv_last / kAttnChunk + 1;
+            const long long work = p.kv_last + 1 + kTileKeys;
+            p.c0 = chunk_cut(w0 - w, p.n, work, whole);
+            p.c1 = chunk_cut(w1 - w, p.n, work, whole);
+            w += work;
+            if (++y == n_qt) {
+                y = 0;
+                if (++g == n_kv) {
+                    g = 0;
+                    do ++b;
+                    while (b < batch && s.count[b] == 0);
+                    if (b < batch) load();
+                }
+            }
+            if (p.c0 < p.c1) return true;
+        }
+        return false;
+    }
+    // Where the stretch begins: {b, g, tile, chunk}; chunk 0 when it begins with a tile.
+    __device__ __forceinline__ int4 begin() const {
+        if (b >= batch) return make_int4(0, 0, 0, 0);
+        const int kv_last = start + min((y + 1) * tq, count) - 1, n = kv_last / kAttnChunk + 1;
+        const int c = chunk_cut(w0 - w, n, (long long)kv_last + 1 + kTileKeys, whole);
+        return make_int4(b, g, y, c < n ? c : 0);
+    }
+};
+
+}  // namespace llama
