@@ -84,8 +84,8 @@ using namespace llama;
 extern "C" size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads,
                                                               int head_dim, int max_len) {
     if (batch <= 0 || tokens <= 0 || max_len <= 0 || !heads_ok(n_heads, n_kv_heads, head_dim)) return 0;
-    // two partials (m, l, o) of up to 128 rows for each CTA, and where the CTAs begin
-    return align16((size_t)kChunkMaxCtas * 128 * (head_dim + 2) * sizeof(float)) + kChunkMaxCtas * sizeof(int4);
+    // two partials (m, l, o) of up to 256 rows for each CTA, and where the CTAs begin
+    return align16((size_t)kChunkMaxCtas * 512 * (head_dim + 2) * sizeof(float)) + kChunkMaxCtas * sizeof(int4);
 }
 
 extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_heads, int n_kv_heads,
@@ -122,11 +122,11 @@ extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens,
     a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
     a.err = err_dev;
     a.partial = (float*)ws;
-    a.part_ml = (float2*)(a.partial + (size_t)kChunkMaxCtas * 128 * head_dim);
-    a.cuts = (int4*)((uint8_t*)ws + align16((size_t)kChunkMaxCtas * 128 * (head_dim + 2) * sizeof(float)));
+    a.part_ml = (float2*)(a.partial + (size_t)kChunkMaxCtas * 512 * head_dim);
+    a.cuts = (int4*)((uint8_t*)ws + align16((size_t)kChunkMaxCtas * 512 * (head_dim + 2) * sizeof(float)));
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
-    if (dtype == LLAMA_BF16) { a.tq = 128 / (n_heads / n_kv_heads); e = launch_chunk_tc(a, head_dim, s); }
+    if (dtype == LLAMA_BF16) e = launch_chunk_tc(a, head_dim, s);
     else if (head_dim == 32) e = launch_rows<float, 32>(a, s);
     else if (head_dim == 64) e = launch_rows<float, 64>(a, s);
     else e = launch_rows<float, 128>(a, s);

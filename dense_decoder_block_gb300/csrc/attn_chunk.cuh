@@ -1,12 +1,16 @@
 // The work of a chunk attention call, shared by its kernels: which keys of which query tile a CTA takes.
 //
 // A tile is `tq` consecutive new tokens of a sequence under one KV head (tq x the group's heads rows);
-// its work is the keys that its last token attends and a constant for starting and storing a tile.  All
-// tiles -- sequences in order, their KV heads, their tiles -- lie one after another on a line, and CTA i
-// of n takes the stretch [W i / n, W (i + 1) / n) of the line's length W, cut at chunks of
-// kAttnChunk keys (cut below): a tile that crosses the end of a stretch is shared by several CTAs, each of
-// which leaves the softmax partial (m, l, o) of its chunks, and a second kernel joins them.  Lengths
-// and counts are read on the device, so the balance holds for any mixture of sequences under any bound.
+// its work is the keys that its last token attends and a constant for starting and storing a tile.  Lengths
+// and counts are read on the device, so both ways of dealing tiles out hold for any mixture of sequences
+// under any bound:
+//   - many tiles (kRounds per CTA or more): whole tiles in rounds, the longest of a sequence first and every other round
+//     from the other end.  CTAs then walk the keys of a head at about the same time, and find them in L2
+//     (stretches of a line as below: 8192 tokens of 32 / 8 heads 920 us, in rounds 755, one tile a CTA at a time);
+//   - few: all tiles -- sequences in order, their KV heads, their tiles -- lie one after another on a line of length
+//     W, and CTA i of n takes the stretch [W i / n, W (i + 1) / n), cut at chunks of kAttnChunk keys (chunk_cut): a
+//     tile that crosses the end of a stretch is shared by several CTAs, each of which leaves the softmax
+//     partial (m, l, o) of its chunks, and a second kernel joins them.
 #pragma once
 #include "common.cuh"
 #include "paged.cuh"
@@ -15,7 +19,7 @@
 namespace llama {
 
 constexpr int kChunkSeqs = 1024;      // sequences of a launch
-constexpr int kChunkMaxCtas = 304;    // CTAs of a launch: two partials each (workspace)
+constexpr int kChunkMaxCtas = 152;    // CTAs of a launch: two partials each (workspace)
 
 struct ChunkArgs {
     const void* q;       // [batch, tokens, n_heads, head_dim]
@@ -28,9 +32,8 @@ struct ChunkArgs {
     PageTable pages;
     float scale_log2;
     int tq;              // tokens per tile
-    bool whole;          // tiles are not split
-    float* partial;      // [2 CTAs][head_dim / 4][rows] float4
-    float2* part_ml;     // [2 CTAs][rows]
+    float* partial;      // [2 CTAs][256 / rows of a part][head_dim / 4][rows of a part] float4
+    float2* part_ml;     // [2 CTAs][256]
     int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it
     int* err;
 };
@@ -42,11 +45,14 @@ constexpr int kTileKeys = 128;
 constexpr int kMinPiece = 2;
 // The least work of a CTA (keys) for which another one is started.
 constexpr int kMinStretch = 512;
+// Tiles per CTA from which on they are dealt out whole.
+constexpr int kRounds = 4;
 
 // The sequences of a launch (shared memory).
 struct ChunkSeqs {
-    int start[kChunkSeqs], count[kChunkSeqs];
     long long pre[kChunkSeqs + 1];   // work of the sequences before, one KV head
+    int start[kChunkSeqs], count[kChunkSeqs];
+    int tiles[kChunkSeqs + 1];       // tiles of the sequences before, one KV head
 };
 
 // Work of the first n tiles (all of tq tokens) of a sequence.
@@ -58,6 +64,7 @@ __device__ __forceinline__ long long tiles_work(int start, int tq, int n) {
 __device__ __forceinline__ void chunk_seqs(const ChunkArgs& a, ChunkSeqs& s, bool record) {
     const int lane = threadIdx.x & 31;
     long long run = 0;
+    int run_tiles = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
         int start = 0, count = 0;
@@ -73,23 +80,34 @@ __device__ __forceinline__ void chunk_seqs(const ChunkArgs& a, ChunkSeqs& s, boo
         }
         const int n = (count + a.tq - 1) / a.tq;
         long long w = n > 0 ? tiles_work(start, a.tq, n - 1) + start + count + kTileKeys : 0;
+        int t = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += v;
+            const int u = __shfl_up_sync(0xffffffffu, t, o);
+            if (lane >= o) {
+                w += v;
+                t += u;
+            }
         }
-        if (b < a.batch) s.pre[b + 1] = run + w;
+        if (b < a.batch) {
+            s.pre[b + 1] = run + w;
+            s.tiles[b + 1] = run_tiles + t;
+        }
         run += __shfl_sync(0xffffffffu, w, 31);
+        run_tiles += __shfl_sync(0xffffffffu, t, 31);
     }
-    if (lane == 0) s.pre[0] = 0;
+    if (lane == 0) {
+        s.pre[0] = 0;
+        s.tiles[0] = 0;
+    }
 }
 
 // The chunk of a tile (n chunks, `work` in all) at which a stretch ends that ends `x` behind the tile's
 // beginning: 0 and n when the tile belongs to one side whole.
-__device__ __forceinline__ int chunk_cut(long long x, int n, long long work, bool whole) {
+__device__ __forceinline__ int chunk_cut(long long x, int n, long long work) {
     if (x <= 0) return 0;
     if (x >= work) return n;
-    if (whole) return 2 * x >= work ? n : 0;
     const int c = (int)((x + kAttnChunk / 2) / kAttnChunk);
     return c < kMinPiece ? 0 : c > n - kMinPiece ? n : c;
 }
@@ -103,21 +121,25 @@ struct ChunkPiece {
     int c0, c1, n;    // of n chunks
 };
 
-// A CTA's pieces in order.  Every role of a kernel walks them by itself.
+// A CTA's pieces in order.
 struct ChunkWalk {
     const ChunkSeqs& s;
-    int batch, n_kv, tq;
-    bool whole;
+    int batch, n_kv, tq, cta, n_ctas;
+    bool rounds;
+    int j;                 // rounds: the next one
     long long w, w0, w1;   // beginning of the tile at hand, the stretch
     int b, g, y, n_qt, start, count;
 
-    __device__ __forceinline__ ChunkWalk(const ChunkArgs& a, const ChunkSeqs& seqs, int cta, int n_ctas)
-        : s(seqs), batch(a.batch), n_kv(a.n_kv_heads), tq(a.tq), whole(a.whole) {
+    __device__ __forceinline__ ChunkWalk(const ChunkArgs& a, const ChunkSeqs& seqs, int cta_, int n_ctas_)
+        : s(seqs), batch(a.batch), n_kv(a.n_kv_heads), tq(a.tq), cta(cta_), n_ctas(n_ctas_) {
         const long long total = s.pre[batch] * n_kv;
-        const int n = (int)min((long long)n_ctas, max(1ll, total / kMinStretch));
         b = batch;
+        j = 0;
         w = w0 = w1 = 0;
         g = y = n_qt = start = count = 0;
+        rounds = (long long)s.tiles[batch] * n_kv >= (long long)kRounds * n_ctas;
+        if (rounds) return;
+        const int n = (int)min((long long)n_ctas, max(1ll, total / kMinStretch));
         if (cta >= n || total == 0) return;
         w0 = total * cta / n;
         w1 = total * (cta + 1) / n;
@@ -148,20 +170,43 @@ struct ChunkWalk {
         count = s.count[b];
         n_qt = (count + tq - 1) / tq;
     }
+    __device__ __forceinline__ void tile(ChunkPiece& p) const {
+        p.b = b;
+        p.g = g;
+        p.y = y;
+        p.t0 = y * tq;
+        p.t1 = min(p.t0 + tq, count);
+        p.pos0 = start + p.t0;
+        p.kv_last = start + p.t1 - 1;
+        p.n = p.kv_last / kAttnChunk + 1;
+        p.c0 = 0;
+        p.c1 = p.n;
+    }
     // The next piece; false behind the last.
     __device__ __forceinline__ bool next(ChunkPiece& p) {
+        if (rounds) {
+            const long long l = (long long)j * n_ctas + (j & 1 ? n_ctas - 1 - cta : cta);
+            ++j;
+            if (l >= (long long)s.tiles[batch] * n_kv) return false;
+            int lo = 0, hi = batch - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((long long)s.tiles[mid] * n_kv <= l) lo = mid;
+                else hi = mid - 1;
+            }
+            b = lo;
+            load();
+            const int r = (int)(l - (long long)s.tiles[b] * n_kv);
+            g = r % n_kv;
+            y = n_qt - 1 - r / n_kv;
+            tile(p);
+            return true;
+        }
         while (b < batch && w < w1) {
-            p.b = b;
-            p.g = g;
-            p.y = y;
-            p.t0 = y * tq;
-            p.t1 = min(p.t0 + tq, count);
-            p.pos0 = start + p.t0;
-            p.kv_last = start + p.t1 - 1;
-            p.n = p.kv_last / kAttnChunk + 1;
+            tile(p);
             const long long work = p.kv_last + 1 + kTileKeys;
-            p.c0 = chunk_cut(w0 - w, p.n, work, whole);
-            p.c1 = chunk_cut(w1 - w, p.n, work, whole);
+            p.c0 = chunk_cut(w0 - w, p.n, work);
+            p.c1 = chunk_cut(w1 - w, p.n, work);
             w += work;
             if (++y == n_qt) {
                 y = 0;
@@ -176,11 +221,11 @@ struct ChunkWalk {
         }
         return false;
     }
-    // Where the stretch begins: {b, g, tile, chunk}; chunk 0 when it begins with a tile.
+    // Where the stretch begins: {b, g, tile, chunk}; chunk 0 when it begins with a tile.  Before the first next().
     __device__ __forceinline__ int4 begin() const {
         if (b >= batch) return make_int4(0, 0, 0, 0);
         const int kv_last = start + min((y + 1) * tq, count) - 1, n = kv_last / kAttnChunk + 1;
-        const int c = chunk_cut(w0 - w, n, (long long)kv_last + 1 + kTileKeys, whole);
+        const int c = chunk_cut(w0 - w, n, (long long)kv_last + 1 + kTileKeys);
         return make_int4(b, g, y, c < n ? c : 0);
     }
 };

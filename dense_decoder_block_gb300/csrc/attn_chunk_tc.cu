@@ -1,18 +1,24 @@
 // Attention of chunks of new tokens over a paged cache on the tensor cores (bf16, head_dim 128).
 //
-// Tiles, chunks, softmax and fold are those of the contiguous prefill kernel (attn_tc.cu): 128 query rows
-// (tq tokens x the heads of a KV group) against 128-key chunks in ascending order, S and O_c = P V by
-// tcgen05.mma with the operands in shared and tensor memory, softmax weights rounded to bf16, O folded
-// in fp32 registers.  A tile that one CTA walks from its first chunk to its last has the bits of the
-// contiguous prefill's rows.  What differs:
-//   - a chunk's rows lie in pages: a page (at most 128 rows) is one TMA copy issued by a lane of its own, and
-//     lands as row groups of 8 with their two 64-column halves side by side (see make_tmap_pages);
-//   - sequences have starts and counts of their own, read on the device (attn_chunk.cuh), and long caches under
-//     few rows are split over the CTAs;
-//   - rows do not see what lies behind them: P is 0 there, and so that 0 times an infinity or a NaN does not reach
-//     O, such values of a tile's newest positions are taken out of the chunk's V and added to the
-//     rows that do see them at the end (an infinity or NaN in O either way);
-//   - 32-row quarters of a tile without a row (short chunks) skip the softmax and the fold.
+// A tile is 256 query rows of a KV group (two halves of tqh tokens x the group's heads, 128 rows each), its keys come
+// in chunks of 128:
+//   S = Q K^T     tcgen05.mma M = N = K = 128, operands in shared memory
+//   softmax       thread = row: a running reference m of the row (log2 domain), p = 2^(s c - m) rounded to bf16, l += p.
+//                 m follows the row's maximum only when that has grown by more than 2^kSlack, so O is
+//                 seldom scaled (p <= 2^kSlack; nothing is lost, bf16 and fp32 keep their relative precision)
+//   O += P V      tcgen05.mma, P from tensor memory, O accumulated in tensor memory
+// Two streams run side by side so that one's MMAs cover the other's softmax: the halves of a tile, or, when a tile has
+// 128 rows at most (few new tokens), its even and its odd chunks, joined at the end.  A stream's S, P (over S) and O
+// take 128 columns each for S and O.  Roles:
+//   warp 0, 2     K (and Q), V: a page (at most 128 rows) is one TMA copy issued by a lane of its own, and lands as row
+//                 groups of 8 with their two 64-column halves side by side (make_tmap_pages)
+//   warp 1        tensor memory, MMAs: PV of a stream, then its next S, then the other stream's
+//   warp 3        the CTA's pieces (attn_chunk.cuh), a few ahead
+//   warps 4..11   softmax of stream 0, of stream 1
+//   warps 12..15  scaling of O, care of V, output
+// Rows do not see what lies behind them: P is 0 there, and so that 0 times an infinity or a NaN does not reach
+// O, such values of a tile's newest positions are taken out of the chunk's V and added to the rows that do see
+// them at the end (an infinity or NaN in O either way).
 #include <algorithm>
 
 #include "attn_chunk.cuh"
@@ -22,26 +28,72 @@ namespace llama {
 namespace {
 
 constexpr int kThreads = 512;
-// register split (launch: 128 per thread): as in the contiguous prefill, the fold threads hold a row of O each
-constexpr int kRegsCtrl = 56;
-constexpr int kRegsSoftmax = 112;
-constexpr int kRegsFold = 232;
-constexpr int kRegsNeeded = 128 * kRegsCtrl + 256 * kRegsSoftmax + 128 * kRegsFold;
+constexpr int kRegsCtrl = 56, kRegsSoftmax = 192, kRegsOut = 72;
+constexpr int kRegsNeeded = 128 * kRegsCtrl + 256 * kRegsSoftmax + 128 * kRegsOut;
 static_assert(kRegsNeeded <= 128 * kThreads, "register split exceeds the launch allocation");
-constexpr int OFF_Q = 0;                      // [buffer] Q: 2 sub-tiles
+constexpr float kSlack = 8.f;
+
+constexpr int OFF_Q = 0;                      // [half] Q: 2 sub-tiles
 constexpr int OFF_K = 4 * kSub;               // [stage] K, row groups of 8
 constexpr int OFF_V = OFF_K + 4 * kSub;       // [stage] V
 constexpr int OFF_BAR = OFF_V + 4 * kSub;
-constexpr int OFF_XCH = OFF_BAR + 256;        // softmax halves' exchange: 4 x 128 floats
-constexpr int OFF_SEQS = OFF_XCH + 2048;
+constexpr int OFF_PIECES = OFF_BAR + 512;     // the ring of pieces, and a word for each
+constexpr int OFF_SCALE = OFF_PIECES + 256;   // [stream][128] floats
+constexpr int OFF_ML = OFF_SCALE + 1024;      // [piece parity][stream][128] (m, l)
+constexpr int OFF_SEQS = OFF_ML + 4096;
 constexpr int SMEM_BYTES = OFF_SEQS + (int)sizeof(ChunkSeqs) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-static_assert(sizeof(ChunkSeqs) % 8 == 0 && OFF_SEQS % 8 == 0, "alignment of the prefix sums");
-constexpr int kSBufs = 3;                     // S[i % 3] at columns 0 / 128 / 256, O_c at 384
-constexpr int TM_S = 0, TM_OC = 384;
+constexpr int TM_S = 0, TM_O = 256;           // + 128 per stream
+
+// A CTA's pieces as its roles read them: warp 3 walks the CTA's share a few pieces ahead and leaves them in a ring
+// (a walk in every role took registers that the softmax does not have).
+constexpr int kRing = 4;
+static_assert(sizeof(ChunkPiece) == 40, "ring entries");
+
+// A barrier of n threads that tells whether `ok` holds for all of them.
+__device__ __forceinline__ bool named_bar_and(int id, int n, bool ok) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(n), "r"((uint32_t)ok)
+        : "memory");
+    return r != 0;
+}
 
 // The words of 2 bf16 whose exponent is all ones (infinity, NaN): bits 15 and 31.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return ((w & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+
+// Row `row` of a chunk's V, behind the tile's first position: cleared when it lies behind the last (it may hold
+// anything), else its infinities and NaN are; true when there were any.  Rolled loops: it runs for one or two
+// chunks of a tile.  (No call: a function of its own may use more registers than these warps keep.)
+__device__ __forceinline__ bool care_for_v(uint8_t* v, int row, bool clear) {
+    uint8_t* at = v + (row >> 3) * 2048 + (row & 7) * 128;
+    uint32_t bad = 0;
+#pragma unroll 2
+    for (int i = 0; i < 16; ++i) {   // 16-byte columns in an order that spreads the rows over the banks
+        uint4* u = reinterpret_cast<uint4*>(at + (i & 8) * 128 + ((i ^ row) & 7) * 16);
+        if (clear) *u = make_uint4(0, 0, 0, 0);
+        else bad |= not_finite2(u->x) | not_finite2(u->y) | not_finite2(u->z) | not_finite2(u->w);
+    }
+    if (!bad) return false;
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(at + (i >> 5) * 1024) + (i & 31);
+        const uint32_t f = not_finite2(*w);
+        *w &= ~((f & 0x8000u ? 0xffffu : 0u) | (f & 0x80000000u ? 0xffff0000u : 0u));
+    }
+    return true;
+}
+
+// A piece's steps: step i belongs to stream i % 2.  A pair (both halves have rows): both streams take every chunk.
+// Else the streams take turns.
+__device__ __forceinline__ bool is_pair(const ChunkPiece& p, int tqh) { return p.t1 - p.t0 > tqh; }
+__device__ __forceinline__ int steps_of(const ChunkPiece& p, int tqh) { return (p.c1 - p.c0) << is_pair(p, tqh); }
+__device__ __forceinline__ int steps_of_stream(const ChunkPiece& p, int tqh, int s) {
+    const int n = p.c1 - p.c0;
+    return is_pair(p, tqh) ? n : (n + 1 - s) >> 1;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_chunk(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
@@ -49,45 +101,54 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = (uint64_t*)(sm + OFF_BAR);
-    uint64_t* q_full = bars + 0;     // [2] TMA -> MMA (the Q tile of this CTA's piece j in buffer j % 2)
-    uint64_t* q_empty = bars + 2;    // [2] MMA (after the piece's last S) -> TMA
-    uint64_t* k_full = bars + 4;     // [2] TMA -> MMA
-    uint64_t* k_empty = bars + 6;    // [2] MMA (after S) -> TMA
-    uint64_t* v_full = bars + 8;     // [2] TMA -> MMA (and the softmax, before it clears rows)
-    uint64_t* v_empty = bars + 10;   // [2] MMA (after PV) -> TMA
-    uint64_t* s_full = bars + 12;    // [3] MMA (after S) -> softmax
-    uint64_t* p_full = bars + 15;    // [3] softmax (P, m, l written) -> MMA, fold
-    uint64_t* s_free = bars + 18;    // [3] fold (m, l read) -> MMA
-    uint64_t* oc_full = bars + 21;   // MMA (after PV) -> fold
-    uint64_t* oc_free = bars + 22;   // fold (O_c read) -> MMA
-    uint32_t* tmem_holder = (uint32_t*)(bars + 23);
-    int* poison = (int*)(bars + 24); // [4] j + 1: piece j has infinities or NaN among its newest values
+    uint64_t* q_full = bars + 0;     // TMA -> MMA
+    uint64_t* q_empty = bars + 1;    // MMA (after the piece's last S) -> TMA
+    uint64_t* k_full = bars + 2;     // [2] TMA -> MMA
+    uint64_t* k_empty = bars + 4;    // [2] MMA (after the chunk's last S) -> TMA
+    uint64_t* v_full = bars + 6;     // [2] TMA -> MMA, care of V
+    uint64_t* v_empty = bars + 8;    // [2] MMA (after the chunk's last PV) -> TMA
+    uint64_t* s_full = bars + 10;    // [stream] MMA -> softmax
+    uint64_t* p_full = bars + 12;    // [stream] softmax (P written) -> MMA
+    uint64_t* sc_full = bars + 14;   // [stream] softmax (scale of O written) -> warps 12..15
+    uint64_t* o_ready = bars + 16;   // [stream] warps 12..15 (O scaled, V cared for) -> MMA
+    uint64_t* pv_done = bars + 18;   // [stream] MMA -> warps 12..15
+    // [piece parity][stream] softmax (m and l of the piece written) -> warps 12..15: the softmax may be through with
+    // the next piece before they have looked at this one's
+    uint64_t* ml_full = bars + 20;
+    uint64_t* pc_full = bars + 24;   // [4] warp 3 -> all roles: piece j in entry j % 4
+    uint64_t* pc_free = bars + 28;   // [4] warps 12..15 (piece done, so every role is) -> warp 3
+    uint32_t* tmem_holder = (uint32_t*)(bars + 32);
+    ChunkPiece* pieces = (ChunkPiece*)(sm + OFF_PIECES);
+    int* poison = (int*)(sm + OFF_PIECES + kRing * sizeof(ChunkPiece));   // [4] j + 1: care was taken of piece j's V
     ChunkSeqs& seqs = *reinterpret_cast<ChunkSeqs*>(sm + OFF_SEQS);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     ptx::griddep_wait();   // lengths, tables, rows: whatever the stream holds in front
-    const int n_rep = a.n_heads / a.n_kv_heads;
-    const int n_ctas = gridDim.x;
+    const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq >> 1;
     int* err = a.err;
 
     if (threadIdx.x == 0) {
+        ptx::mbar_init(q_full, 1);
+        ptx::mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&q_full[i], 1);
-            ptx::mbar_init(&q_empty[i], 1);
             ptx::mbar_init(&k_full[i], 1);
             ptx::mbar_init(&k_empty[i], 1);
             ptx::mbar_init(&v_full[i], 1);
             ptx::mbar_init(&v_empty[i], 1);
-        }
-        for (int i = 0; i < kSBufs; ++i) {
             ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&p_full[i], 8);
-            ptx::mbar_init(&s_free[i], 4);
+            ptx::mbar_init(&p_full[i], 4);
+            ptx::mbar_init(&sc_full[i], 4);
+            ptx::mbar_init(&o_ready[i], 4);
+            ptx::mbar_init(&pv_done[i], 1);
+            ptx::mbar_init(&ml_full[i], 4);
+            ptx::mbar_init(&ml_full[2 + i], 4);
         }
-        ptx::mbar_init(oc_full, 1);
-        ptx::mbar_init(oc_free, 4);
+        for (int i = 0; i < kRing; ++i) {
+            ptx::mbar_init(&pc_full[i], 1);
+            ptx::mbar_init(&pc_free[i], 4);
+            poison[i] = 0;
+        }
         ptx::fence_mbar_init();
-        for (int i = 0; i < 4; ++i) poison[i] = 0;
     }
     if (warp == 1) {
         ptx::tmem_alloc(tmem_holder, 512);
@@ -101,9 +162,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     // dependents start only once this CTA holds its tensor memory
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
 
+    // piece j, once it is there; false behind the last (or when a wait gave up)
+    auto piece = [&](int j, ChunkPiece& p) -> bool {
+        if (!ptx::mbar_wait(&pc_full[j % kRing], (j / kRing) & 1, err)) return false;
+        p = pieces[j % kRing];
+        return p.c0 < p.c1;
+    };
     if (warp < 4) {
         ptx::setmaxnreg_dec<kRegsCtrl>();
-        if (warp == 0 || warp == 2) {
+        if (warp == 3) {
+            // ------------------------------------------------------------------ the pieces
+            if (lane == 0) {
+                ChunkWalk walk(a, seqs, blockIdx.x, gridDim.x);
+                a.cuts[blockIdx.x] = walk.begin();
+                ChunkPiece p;
+                for (int j = 0;; ++j) {
+                    const bool more = walk.next(p);
+                    if (j >= kRing && !ptx::mbar_wait(&pc_free[j % kRing], ((j / kRing) & 1) ^ 1, err)) break;
+                    if (!more) p.c0 = p.c1 = 0;
+                    pieces[j % kRing] = p;
+                    ptx::mbar_arrive(&pc_full[j % kRing]);
+                    if (!more) break;
+                }
+            }
+        } else if (warp == 0 || warp == 2) {
             // ------------------------------------------------------------------ TMA producers (K and Q, V), whole warps
             const bool is_k = (warp == 0);
             const CUtensorMap* map = is_k ? &mK : &mV;
@@ -111,13 +193,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t* empty = is_k ? k_empty : v_empty;
             uint8_t* ring = sm + (is_k ? OFF_K : OFF_V);
             const int shift = a.pages.shift, ps = 1 << shift, box = min(ps, kAttnChunk);
-            const uint64_t pol = ptx::policy_evict_last();   // the tiles of a KV head read the same rows
             if (lane == 0) ptx::prefetch_tmap(map);
             int gi = 0, n_q = 0;   // chunks and Q tiles issued
             bool ok = true;
-            ChunkWalk walk(a, seqs, blockIdx.x, n_ctas);
             ChunkPiece p;
-            for (int j = 0; ok && walk.next(p); ++j) {
+            for (int j = 0; ok && piece(j, p); ++j) {
                 // lane = page of a chunk: its id is read a chunk ahead of its copy
                 auto pages_in = [&](int c) { return (min(kAttnChunk, p.kv_last + 1 - c * kAttnChunk) + box - 1) / box; };
                 auto lookup = [&](int c) -> int {
@@ -127,20 +207,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 int next = lookup(p.c0);
                 if (is_k) {
-                    // Q of piece j into buffer j % 2 once piece j - 2's S MMAs are done with it
-                    const int qb = j & 1;
                     int go = 1;
-                    if (lane == 0 && j >= 2) go = ptx::mbar_wait(&q_empty[qb], ((j >> 1) - 1) & 1, err);
+                    if (lane == 0 && j >= 1) go = ptx::mbar_wait(q_empty, (j - 1) & 1, err);
                     if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
                     if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(&q_full[qb], 2 * n_rep * a.tq * 128);
-                        for (int half = 0; half < 2; ++half)
+                        const int halves = is_pair(p, tqh) ? 2 : 1;
+                        ptx::mbar_arrive_expect_tx(q_full, halves * 2 * n_rep * tqh * 128);
+                        for (int x = 0; x < 2 * halves; ++x)
                             asm volatile(
                                 "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                                " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
-                                    ptx::smem_u32(sm + OFF_Q + qb * 2 * kSub + half * kSub)),
-                                "l"(reinterpret_cast<uint64_t>(&mQ)), "r"(ptx::smem_u32(&q_full[qb])), "r"(half * 64),
-                                "r"(p.g * n_rep), "r"(p.b * a.tokens + p.t0)
+                                " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(sm + OFF_Q + x * kSub)),
+                                "l"(reinterpret_cast<uint64_t>(&mQ)), "r"(ptx::smem_u32(q_full)), "r"((x & 1) * 64),
+                                "r"(p.g * n_rep), "r"(p.b * a.tokens + p.t0 + (x >> 1) * tqh)
                                 : "memory");
                     }
                     ++n_q;
@@ -155,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane < n) {
                         const int row = ((id * a.n_kv_heads + p.g) << shift) + (c * kAttnChunk & (ps - 1));
-                        tma_load_page(ring + st * 2 * kSub + lane * box * 256, map, &full[st], row >> 3, pol);
+                        tma_load_page(ring + st * 2 * kSub + lane * box * 256, map, &full[st], row >> 3);
                     }
                     next = lookup(c + 1);
                 }
@@ -163,258 +241,329 @@ __global__ void __launch_bounds__(kThreads, 1)
             // no copy may still be landing when the CTA exits (it has landed already
             // unless a wait above gave up)
             if (lane == 0) {
-                for (int j = max(0, n_q - 2); j < n_q; ++j) ptx::mbar_wait_drain(&q_full[j & 1], (j >> 1) & 1);
+                if (n_q > 0) ptx::mbar_wait_drain(q_full, (n_q - 1) & 1);
                 for (int i = max(0, gi - 2); i < gi; ++i) ptx::mbar_wait_drain(&full[i & 1], (i >> 1) & 1);
             }
-        } else if (warp == 1) {
+        } else if (lane == 0) {
             // ------------------------------------------------------------------ MMA issuer
-            if (lane == 0) {
-                // S(gi) into S[gi % 3]: Q of its piece landed (at the piece's first chunk),
-                // K(gi) landed, and the fold has read chunk gi - 3's (m, l) from that buffer
-                // (PV(gi - 3), which read its P, was issued before and the MMAs run in issue
-                // order).  After a piece's last S its Q buffer is released.
-                ChunkWalk walk(a, seqs, blockIdx.x, n_ctas);
+            // Steps in order, S up to one step per stream ahead of PV.  S of a stream may be issued once
+            // its last PV is (the MMAs run in issue order, so P has been read when S overwrites it; the softmax
+            // has read S before it wrote P).
+            struct { int j, i, n; bool pair; } sp{0, 0, 0, false}, vp{0, 0, 0, false};   // step of the next S, PV
+            auto open = [&](auto& x) {
                 ChunkPiece p;
-                int s_j = 0, s_left = 0, issued = 0;   // piece of the next S, chunks left of it, S issued
-                bool first = true;
-                s_left = walk.next(p) ? p.c1 - p.c0 : 0;
-                auto issue_s = [&]() -> bool {
-                    if (s_left == 0) return true;
-                    const int gi = issued, k = gi & 1, sb = gi % kSBufs, qb = s_j & 1;
-                    if (first && !ptx::mbar_wait(&q_full[qb], (s_j >> 1) & 1, err)) return false;
-                    if (!ptx::mbar_wait(&k_full[k], (gi >> 1) & 1, err)) return false;
-                    if (gi >= kSBufs && !ptx::mbar_wait(&s_free[sb], ((gi / kSBufs) & 1) ^ 1, err)) return false;
-                    ptx::tc_fence_after();
-                    const uint64_t q_desc = ptx::sw128_kmajor_desc(ptx::smem_u32(sm + OFF_Q + qb * 2 * kSub));
-                    const uint32_t k_addr = ptx::smem_u32(sm + OFF_K + k * 2 * kSub);
-                    umma8_ss<kSub / 16, 1024 / 16, false>(tmem + TM_S + sb * 128, q_desc,
-                                                          desc_with_stride(ptx::sw128_kmajor_desc(k_addr), 2048), IDESC_S);
-                    ptx::umma_commit(&s_full[sb]);
+                x.i = 0;
+                x.n = 0;
+                if (!piece(x.j, p)) return;
+                x.n = steps_of(p, tqh);
+                x.pair = is_pair(p, tqh);
+            };
+            int kc = 0, vc = 0;               // chunks of K and V used up
+            int ns[2] = {0, 0}, nv[2] = {0, 0};   // S and PV issued per stream
+            bool ok = true;
+            // S of the next step, if its stream is free; `wait`: also when its operands are still on their way
+            auto issue_s = [&](bool wait) -> bool {
+                if (sp.n == 0) return true;
+                const int s = sp.i & 1, k = kc & 1;
+                if (ns[s] != nv[s]) return true;
+                if (!wait && sp.i == 0 && !ptx::mbar_try_wait(q_full, sp.j & 1)) return true;
+                if (sp.i == 0 && !ptx::mbar_wait(q_full, sp.j & 1, err)) return false;
+                if (!ptx::mbar_wait(&k_full[k], (kc >> 1) & 1, err)) return false;
+                ptx::tc_fence_after();
+                const uint32_t q_addr = ptx::smem_u32(sm + OFF_Q + (sp.pair ? s : 0) * 2 * kSub);
+                const uint32_t k_addr = ptx::smem_u32(sm + OFF_K + k * 2 * kSub);
+                umma8_ss<kSub / 16, 1024 / 16, false>(tmem + TM_S + s * 128, ptx::sw128_kmajor_desc(q_addr),
+                                                      desc_with_stride(ptx::sw128_kmajor_desc(k_addr), 2048), IDESC_S);
+                ptx::umma_commit(&s_full[s]);
+                if (!sp.pair || s == 1) {
                     ptx::umma_commit(&k_empty[k]);
-                    ++issued;
-                    first = false;
-                    if (--s_left == 0) {
-                        ptx::umma_commit(&q_empty[qb]);
-                        ++s_j;
-                        first = true;
-                        s_left = walk.next(p) ? p.c1 - p.c0 : 0;
-                    }
-                    return true;
-                };
-                bool ok = true;
-                for (int i = 0; i < kSBufs && ok; ++i) ok = issue_s();
-                for (int gi = 0; ok && gi < issued; ++gi) {
-                    const int k = gi & 1, sb = gi % kSBufs;
-                    if (!ptx::mbar_wait(&p_full[sb], (gi / kSBufs) & 1, err)) break;
-                    // O_c is overwritten once the fold has read chunk gi - 1's
-                    if (gi >= 1 && !ptx::mbar_wait(oc_free, (gi - 1) & 1, err)) break;
-                    if (!ptx::mbar_wait(&v_full[k], (gi >> 1) & 1, err)) break;
-                    ptx::tc_fence_after();
-                    const uint32_t v_addr = ptx::smem_u32(sm + OFF_V + k * 2 * kSub);
-                    // P of keys 16ks.. in TMEM columns 8ks.., V rows 16ks..
-                    umma8_ts<256>(tmem + TM_OC, tmem + TM_S + sb * 128,
-                                  desc_with_stride(ptx::sw128_mnmajor_desc(v_addr, 1024), 2048), IDESC_PV);
-                    ptx::umma_commit(oc_full);
-                    ptx::umma_commit(&v_empty[k]);
-                    ok = issue_s();
+                    ++kc;
                 }
+                ++ns[s];
+                if (++sp.i == sp.n) {
+                    ptx::umma_commit(q_empty);
+                    ++sp.j;
+                    open(sp);
+                }
+                return true;
+            };
+            open(sp);
+            open(vp);
+            while (ok && vp.n > 0) {
+                const int s = vp.i & 1, v = vc & 1;
+                if (ns[s] == nv[s]) ok = issue_s(true);
+                if (ok) ok = issue_s(false);   // the other stream's
+                if (!ok || ns[s] == nv[s]) {
+                    if (ok) continue;
+                    break;
+                }
+                if (!ptx::mbar_wait(&o_ready[s], nv[s] & 1, err)) break;
+                if (!ptx::mbar_wait(&v_full[v], (vc >> 1) & 1, err)) break;
+                if (!ptx::mbar_wait(&p_full[s], nv[s] & 1, err)) break;
+                ptx::tc_fence_after();
+                const uint32_t v_addr = ptx::smem_u32(sm + OFF_V + v * 2 * kSub);
+                // P of keys 16ks.. in columns 8ks.., V rows 16ks..
+                umma8_ts<256>(tmem + TM_O + s * 128, tmem + TM_S + s * 128,
+                              desc_with_stride(ptx::sw128_mnmajor_desc(v_addr, 1024), 2048), IDESC_PV, vp.i >= 2);
+                ptx::umma_commit(&pv_done[s]);
+                if (!vp.pair || s == 1) {
+                    ptx::umma_commit(&v_empty[v]);
+                    ++vc;
+                }
+                ++nv[s];
+                if (++vp.i == vp.n) {
+                    ++vp.j;
+                    open(vp);
+                }
+                ok = issue_s(false);
             }
         }
     } else if (warp < 12) {
-        // ------------------------------------------------------------------ softmax, two threads per row
-        ptx::setmaxnreg_dec<kRegsSoftmax>();
-        const int h = (warp - 4) >> 2;   // key half of this warpgroup
+        // ------------------------------------------------------------------ softmax of a stream, thread = row
+        ptx::setmaxnreg_inc<kRegsSoftmax>();
+        const int s = (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
-        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
         const int t_local = row / n_rep;
-        float* xch = reinterpret_cast<float*>(sm + OFF_XCH);
+        const uint32_t s_taddr = tmem + ((uint32_t)(quarter * 32) << 16) + TM_S + s * 128;
+        float* scale = reinterpret_cast<float*>(sm + OFF_SCALE) + s * 128 + row;
+        const float c = a.scale_log2;
+        int step = 0;   // of the stream
         bool ok = true;
-        int gi = 0;
-        ChunkWalk walk(a, seqs, blockIdx.x, n_ctas);
-        ChunkPiece p;
-        for (int j = 0; walk.next(p); ++j) {
-            const bool live = quarter * 32 < (p.t1 - p.t0) * n_rep;   // rows in this quarter
-            const bool valid = p.t0 + t_local < p.t1 && t_local < a.tq;
-            const int pos_r = p.pos0 + t_local;
-            for (int c = p.c0; c < p.c1; ++c, ++gi) {
-                const int k = gi & 1, sb = gi % kSBufs;
-                // s_full(gi) also means PV(gi - 3) -- issued before S(gi) -- is done with the P in S[sb]
-                if (ok) ok = ptx::mbar_wait(&s_full[sb], (gi / kSBufs) & 1, err);
-                ptx::tc_fence_after();
-                const int jmax = valid ? min(kAttnChunk - 1, pos_r - c * kAttnChunk) : -1;
-                float m;
-                // both halves reach the two barriers inside on every chunk, whatever `ok` says
-                if (live)
-                    softmax_half_tmem(tmem + lane_addr + TM_S + sb * 128, h, row, jmax, a.scale_log2, xch, 1 + quarter, m);
-                if (h == 0) {
-                    // values behind the first row: those past the tile's last position may hold anything and
-                    // are cleared, infinities and NaN among those that only some rows see are taken out
-                    // (P is 0 where they are hidden and 0 * NaN would poison O)
-                    if (c * kAttnChunk + kAttnChunk - 1 > p.pos0) {
-                        if (ok) ok = ptx::mbar_wait(&v_full[k], (gi >> 1) & 1, err);
-                        const int key = c * kAttnChunk + row;
-                        uint8_t* vrow = sm + OFF_V + k * 2 * kSub + (row >> 3) * 2048 + (row & 7) * 128;
-                        if (key > p.kv_last) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int c16 = (i ^ (row & 7)) * 16;   // spread over the banks
-                                *reinterpret_cast<uint4*>(vrow + c16) = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4*>(vrow + 1024 + c16) = make_uint4(0, 0, 0, 0);
-                            }
-                        } else if (key > p.pos0) {
-                            uint32_t bad = 0;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint4 u = *reinterpret_cast<const uint4*>(vrow + (i & 8) * 128 + ((i ^ row) & 7) * 16);
-                                bad |= not_finite2(u.x) | not_finite2(u.y) | not_finite2(u.z) | not_finite2(u.w);
-                            }
-                            if (bad) {
-                                poison[j & 3] = j + 1;
+        for (int j = 0;; ++j) {
+            int left, last_key, ahead;   // chunks of the stream; the row's last key from the chunk's first; keys a step
+            bool live;                   // rows in this quarter
+            {
+                ChunkPiece p;
+                if (!piece(j, p)) break;
+                const bool pair = is_pair(p, tqh);
+                left = steps_of_stream(p, tqh, s);
+                const int first = pair ? s * tqh : 0;   // token of the half
+                const int rows = min(p.t1 - p.t0 - first, tqh) * n_rep;
+                live = quarter * 32 < rows;
+                ahead = pair ? kAttnChunk : 2 * kAttnChunk;
+                last_key = row < rows ? p.pos0 + first + t_local - (p.c0 + (pair ? 0 : s)) * kAttnChunk : -1;
+            }
+            float m = -INFINITY, l = 0.f;
+            const bool any = left > 0;
 #pragma unroll 1
-                                for (int i = 0; i < 64; ++i) {
-                                    uint32_t* at = reinterpret_cast<uint32_t*>(vrow + (i >> 5) * 1024) + (i & 31);
-                                    const uint32_t f = not_finite2(*at);
-                                    *at &= ~((f & 0x8000u ? 0xffffu : 0u) | (f & 0x80000000u ? 0xffff0000u : 0u));
-                                }
-                            }
-                        }
+            for (; left > 0; --left, ++step, last_key -= ahead) {
+                if (ok) ok = ptx::mbar_wait(&s_full[s], step & 1, err);
+                ptx::tc_fence_after();
+                if (live) {
+                    float v[128];
+                    ptx::tmem_ld<32>(s_taddr, v);
+                    ptx::tmem_ld<32>(s_taddr + 32, v + 32);
+                    ptx::tmem_ld<32>(s_taddr + 64, v + 64);
+                    ptx::tmem_ld<32>(s_taddr + 96, v + 96);
+                    ptx::tmem_wait_ld();
+                    if (!__all_sync(0xffffffffu, last_key >= kAttnChunk - 1)) {
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            if (e > last_key) v[e] = -INFINITY;
                     }
-                    ptx::fence_proxy_async_smem();
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int e = 4; e < 124; e += 8) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], v[e + x], v[e + 4 + x]);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], v[124 + x]);
+                    const float mn = fmaxf(m, __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c));
+                    float sc = 1.f;
+                    if (mn != m && !(mn - m <= kSlack)) {
+                        sc = ex2(m - mn);
+                        m = mn;
+                    }
+                    *scale = sc;
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&sc_full[s]);
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const uint64_t c2 = pack2(c, c), nm2 = pack2(-ref, -ref);
+                    uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                    for (int e0 = 0; e0 < 128; e0 += 16) {
+                        uint32_t packed[8];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 4) {
+                            float x0, x1, x2, x3;
+                            unpack2(fma2(pack2(v[e0 + e], v[e0 + e + 1]), c2, nm2), x0, x1);
+                            unpack2(fma2(pack2(v[e0 + e + 2], v[e0 + e + 3]), c2, nm2), x2, x3);
+                            x0 = ex2(x0);
+                            x1 = ex2(x1);
+                            x2 = ex2(x2);
+                            x3 = ex2(x3);
+                            sum0 = add2(sum0, pack2(x0, x1));
+                            sum1 = add2(sum1, pack2(x2, x3));
+                            const __nv_bfloat162 p0 = __floats2bfloat162_rn(x0, x1), p1 = __floats2bfloat162_rn(x2, x3);
+                            packed[e / 2] = *reinterpret_cast<const uint32_t*>(&p0);
+                            packed[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
+                        }
+                        tmem_st8(s_taddr + e0 / 2, packed);
+                    }
+                    float a0, a1;
+                    unpack2(add2(sum0, sum1), a0, a1);
+                    l = __fmaf_rn(l, sc, a0 + a1);
+                    ptx::tmem_wait_st();
+                } else if (lane == 0) {
+                    ptx::mbar_arrive(&sc_full[s]);
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&p_full[sb]);
+                if (lane == 0) ptx::mbar_arrive(&p_full[s]);
+            }
+            if (any) {
+                reinterpret_cast<float2*>(sm + OFF_ML)[((j & 1) * 2 + s) * 128 + row] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&ml_full[(j & 1) * 2 + s]);
             }
         }
     } else {
-        // ------------------------------------------------------------------ fold + output
-        ptx::setmaxnreg_inc<kRegsFold>();
+        // ------------------------------------------------------------------ scaling of O, care of V, output
+        ptx::setmaxnreg_dec<kRegsOut>();
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
-        const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
         const int t_local = row / n_rep, h_local = row - t_local * n_rep;
-        float O[128];
+        const uint32_t o_taddr = tmem + ((uint32_t)(quarter * 32) << 16) + TM_O;
+        const float* scale = reinterpret_cast<const float*>(sm + OFF_SCALE) + row;
+        const float2* ml = reinterpret_cast<const float2*>(sm + OFF_ML) + row;
         bool ok = true;
-        int gi = 0;
-        ChunkWalk walk(a, seqs, blockIdx.x, n_ctas);
-        if (threadIdx.x == kThreads - 1) a.cuts[blockIdx.x] = walk.begin();
+        int vc = 0, done[2] = {0, 0};   // chunks, steps of a stream
+        uint32_t ml_phase = 0;          // parities of ml_full
         ChunkPiece p;
-        for (int j = 0; walk.next(p); ++j) {
-            const bool live = quarter * 32 < (p.t1 - p.t0) * n_rep;
-            const bool valid = p.t0 + t_local < p.t1 && t_local < a.tq;
-            float M = -INFINITY, L_sum = 0.f;
-            bool started = false;
+        for (int j = 0; named_bar_and(1, 128, piece(j, p)); ++j) {   // all four warps go on or none
+            const bool pair = is_pair(p, tqh);
+            const int steps = steps_of(p, tqh);
 #pragma unroll 1
-            for (int c = p.c0; c < p.c1; ++c, ++gi) {
-                const int sb = gi % kSBufs;
-                if (ok) ok = ptx::mbar_wait(&p_full[sb], (gi / kSBufs) & 1, err);
-                ptx::tc_fence_after();
-                float ml[2] = {-INFINITY, 0.f};
-                if (live) {
-                    ptx::tmem_ld<2>(tmem + lane_addr + TM_S + sb * 128 + PF_TM_ML, ml);
-                    ptx::tmem_wait_ld();
+            for (int i = 0; i < steps; ++i) {
+                const int s = i & 1;
+                if (!pair || s == 0) {
+                    const int key0 = (p.c0 + (pair ? i >> 1 : i)) * kAttnChunk, v = vc & 1;
+                    if (key0 + kAttnChunk - 1 > p.pos0) {
+                        if (ok) ok = ptx::mbar_wait(&v_full[v], (vc >> 1) & 1, err);
+                        if (key0 + row > p.pos0 && care_for_v(sm + OFF_V + v * 2 * kSub, row, key0 + row > p.kv_last))
+                            poison[j % kRing] = j + 1;
+                        ptx::fence_proxy_async_smem();
+                    }
+                    ++vc;
+                }
+                if (ok) ok = ptx::mbar_wait(&sc_full[s], done[s] & 1, err);
+                const int half = pair ? s : 0;
+                const bool live = quarter * 32 < min(p.t1 - p.t0 - half * tqh, tqh) * n_rep;
+                if (i >= 2 && live) {
+                    const float sc = scale[s * 128];
+                    if (__any_sync(0xffffffffu, sc != 1.f)) {
+                        if (ok) ok = ptx::mbar_wait(&pv_done[s], (done[s] - 1) & 1, err);
+                        ptx::tc_fence_after();
+#pragma unroll 1
+                        for (int cb = 0; cb < 128; cb += 32) {
+                            float o[32];
+                            ptx::tmem_ld<32>(o_taddr + s * 128 + cb, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= sc;
+                            ptx::tmem_st32(o_taddr + s * 128 + cb, o);
+                        }
+                        ptx::tmem_wait_st();
+                    }
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&s_free[sb]);
-                const float m = ml[0], l = ml[1];
-                if (ok) ok = ptx::mbar_wait(oc_full, gi & 1, err);
-                ptx::tc_fence_after();
-                if (!live) {
-                    if (lane == 0) ptx::mbar_arrive(oc_free);
-                    continue;
-                }
-                // Per row: skip a chunk with no visible key (or none above -inf), start from the first
-                // one, fold the rest.  The TMEM loads are issued by the whole
-                // warp whatever each row does (they are warp-collective).
-                const bool use = !(m == -INFINITY && l == 0.f);
-                const bool fold = use && started;
-                float alpha = 1.f, beta = 0.f;
-                if (fold) {
-                    const float Mn = fmaxf(M, m);
-                    alpha = exp2f(__fsub_rn(M, Mn));
-                    beta = exp2f(__fsub_rn(m, Mn));
-                    L_sum = __fmaf_rn(L_sum, alpha, __fmul_rn(l, beta));
-                    M = Mn;
-                } else if (use) {
-                    M = m;
-                    L_sum = l;
-                }
-                const uint32_t oc_addr = tmem + lane_addr + TM_OC;
-#pragma unroll
-                for (int cb = 0; cb < 4; ++cb) {
-                    float oc[32];
-                    ptx::tmem_ld<32>(oc_addr + cb * 32, oc);
-                    ptx::tmem_wait_ld();
-                    if (cb == 3) {   // O_c fully read: PV(gi + 1) may overwrite it
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(oc_free);
-                    }
-                    if (fold) {   // o = fma(o, alpha, oc * beta), two columns per instruction
-                        const uint64_t a2 = pack2(alpha, alpha), b2 = pack2(beta, beta);
-#pragma unroll
-                        for (int jj = 0; jj < 32; jj += 2) {
-                            float& o0 = O[cb * 32 + jj];
-                            float& o1 = O[cb * 32 + jj + 1];
-                            unpack2(fma2(pack2(o0, o1), a2, mul2(pack2(oc[jj], oc[jj + 1]), b2)), o0, o1);
-                        }
-                    } else if (use) {
-#pragma unroll
-                        for (int jj = 0; jj < 32; ++jj) O[cb * 32 + jj] = oc[jj];
-                    }
-                }
-                started = started || use;
+                if (lane == 0) ptx::mbar_arrive(&o_ready[s]);
+                ++done[s];
             }
-            if (!started) {   // no key above -inf: nothing of a split row, NaN (0 / 0) for a whole one
-                L_sum = 0.f;
-#pragma unroll
-                for (int jj = 0; jj < 128; ++jj) O[jj] = 0.f;
-            }
-            if (!valid || !ok) continue;
-            bf16* dst = static_cast<bf16*>(a.o) + ((size_t)p.b * a.tokens + p.t0 + t_local) * a.n_heads * 128 +
-                        (size_t)(p.g * n_rep + h_local) * 128;
+            // output: the halves one after another, or the two streams of one half joined
+            named_bar_and(1, 128, true);   // poison is written
+            const bool poisoned = poison[j % kRing] == j + 1;
             const bool split = p.c1 - p.c0 < p.n;
             const int slot = 2 * blockIdx.x + (p.c0 == 0);
-            float* part = a.partial + (size_t)slot * (128 * 128) + row * 4;   // [column / 4][row][4]
-            if (split) {
-                a.part_ml[slot * 128 + row] = make_float2(M, L_sum);
+#pragma unroll 1
+            for (int half = 0; half < (pair ? 2 : 1); ++half) {
+                // this half's streams: `half`, or 0 and (with two chunks or more) 1
+                const bool both = !pair && steps > 1;
+                for (int s = half; s <= (both ? 1 : half); ++s) {
+                    const int at = (j & 1) * 2 + s;
+                    if (ok) ok = ptx::mbar_wait(&ml_full[at], ml_phase >> at & 1, err);
+                    ml_phase ^= 1u << at;
+                    if (ok) ok = ptx::mbar_wait(&pv_done[s], (done[s] - 1) & 1, err);
+                }
+                ptx::tc_fence_after();
+                const int tokens = min(p.t1 - p.t0 - half * tqh, tqh);
+                if (quarter * 32 >= tokens * n_rep) continue;
+                const bool valid = t_local < tokens;
+                float2 x = ml[((j & 1) * 2 + half) * 128];
+                float w0 = 1.f, w1 = 0.f;   // weights of the streams
+                if (both) {
+                    const float2 y = ml[((j & 1) * 2 + 1) * 128];
+                    // a stream without a key above -inf has no weight
+                    const float M = fmaxf(x.x, y.x);
+                    w0 = x.x == -INFINITY && x.y == 0.f ? 0.f : ex2(x.x - M);
+                    w1 = y.x == -INFINITY && y.y == 0.f ? 0.f : ex2(y.x - M);
+                    x = make_float2(M, __fmaf_rn(x.y, w0, y.y * w1));
+                }
+                bf16* dst = static_cast<bf16*>(a.o) + ((size_t)p.b * a.tokens + p.t0 + half * tqh + t_local) * a.n_heads * 128 +
+                            (size_t)(p.g * n_rep + h_local) * 128;
+                float* part = a.partial + (size_t)(2 * slot + half) * (128 * 128) + row * 4;   // [column / 4][row][4]
+                if (split) {
+                    if (valid && ok) a.part_ml[(2 * slot + half) * 128 + row] = x;
+                } else {
+                    const float inv = 1.f / x.y;   // no key above -inf: 0 * infinity
+                    w0 *= inv;
+                    w1 *= inv;
+                }
+#pragma unroll 1
+                for (int cb = 0; cb < 128; cb += 16) {
+                    float o[16];
+                    ptx::tmem_ld<16>(o_taddr + half * 128 + cb, o);
+                    if (both) {
+                        float q[16];
+                        ptx::tmem_ld<16>(o_taddr + 128 + cb, q);
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                for (int d4 = 0; d4 < 32; ++d4)
-                    *reinterpret_cast<float4*>(part + d4 * 512) =
-                        make_float4(O[4 * d4], O[4 * d4 + 1], O[4 * d4 + 2], O[4 * d4 + 3]);
-            } else {
-                // o = O * (1 / L), rounded to bf16, while the next piece's chunks run
-                const float inv_l = __frcp_rn(L_sum);
+                        for (int e = 0; e < 16; ++e) o[e] = __fmaf_rn(o[e], w0, q[e] * w1);
+                    } else {
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                for (int c8 = 0; c8 < 16; ++c8) {
-                    uint32_t packed[4];
-#pragma unroll
-                    for (int jj = 0; jj < 8; jj += 2) {
-                        const __nv_bfloat162 v2 = __floats2bfloat162_rn(__fmul_rn(O[c8 * 8 + jj], inv_l),
-                                                                        __fmul_rn(O[c8 * 8 + jj + 1], inv_l));
-                        packed[jj >> 1] = *reinterpret_cast<const uint32_t*>(&v2);
+                        for (int e = 0; e < 16; ++e) o[e] *= w0;
                     }
-                    *reinterpret_cast<uint4*>(dst + c8 * 8) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+                    if (!valid || !ok) {
+                    } else if (split) {
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4)
+                            *reinterpret_cast<float4*>(part + (cb / 4 + q4) * 512) =
+                                make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
+                    } else {
+                        uint32_t packed[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+                            packed[e] = *reinterpret_cast<const uint32_t*>(&v2);
+                        }
+                        *reinterpret_cast<uint4*>(dst + cb) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+                        *reinterpret_cast<uint4*>(dst + cb + 8) = make_uint4(packed[4], packed[5], packed[6], packed[7]);
+                    }
+                }
+                if (poisoned && valid && ok) {
+                    // infinities and NaN that were taken out of V: onto the columns of the rows that see them
+                    const int first = max(p.pos0 + 1, p.c0 * kAttnChunk);
+                    const int last = min(p.pos0 + half * tqh + t_local, p.c1 * kAttnChunk - 1);
+                    for (int key = first; key <= last; ++key) {
+                        const int id = max(page_of(a.pages, p.b, key >> a.pages.shift, nullptr), 0);
+                        const size_t at = ((size_t)(id * a.n_kv_heads + p.g) << a.pages.shift) + (key & ((1 << a.pages.shift) - 1));
+                        const bf16* v = static_cast<const bf16*>(a.vc) + at * 128;
+                        for (int d = 0; d < 128; ++d) {
+                            const float bad = __bfloat162float(v[d]);
+                            if (bad - bad == 0.f) continue;
+                            if (split) part[(d >> 2) * 512 + (d & 3)] += bad;
+                            else dst[d] = __float2bfloat16_rn(__bfloat162float(dst[d]) + bad);
+                        }
+                    }
                 }
             }
-            if (poison[j & 3] == j + 1) {
-                // infinities and NaN that the softmax warps took out of V: onto the columns of the rows that see them
-                const int first = max(p.pos0 + 1, p.c0 * kAttnChunk);
-                const int last = min(min(p.pos0 + t_local, p.kv_last), p.c1 * kAttnChunk - 1);
-                for (int key = first; key <= last; ++key) {
-                    const int id = max(page_of(a.pages, p.b, key >> a.pages.shift, nullptr), 0);
-                    const size_t at = ((size_t)(id * a.n_kv_heads + p.g) << a.pages.shift) + (key & ((1 << a.pages.shift) - 1));
-                    const bf16* v = static_cast<const bf16*>(a.vc) + at * 128;
-                    for (int d = 0; d < 128; ++d) {
-                        const float x = __bfloat162float(v[d]);
-                        if (x - x == 0.f) continue;
-                        if (split) part[(d >> 2) * 512 + (d & 3)] += x;
-                        else dst[d] = __float2bfloat16_rn(__bfloat162float(dst[d]) + x);
-                    }
-                }
-            }
+            ptx::tc_fence_before();   // O read: the next piece's first PV may overwrite it
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&pc_free[j % kRing]);
         }
     }
 
@@ -425,19 +574,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the pieces of a split tile: CTA (i, part of the columns), i the first CTA that begins inside the tile.
+// Joins the pieces of a split tile: CTA (i, part of the columns, half), i the first CTA that begins inside the tile.
 // Pieces in ascending order: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M the largest m_p.
 constexpr int kJoinCols = 16;
 
 __global__ void __launch_bounds__(128) k_attn_chunk_join(const ChunkArgs a, int n_ctas) {
     ptx::griddep_wait();
-    const int i = blockIdx.x + 1, row = threadIdx.x;
+    const int i = blockIdx.x + 1, row = threadIdx.x, half = blockIdx.z;
     const int4 cut = __ldcg(a.cuts + i), before = __ldcg(a.cuts + i - 1);
     auto same = [&](const int4& x) { return x.w > 0 && x.x == cut.x && x.y == cut.y && x.z == cut.z; };
     if (cut.w == 0 || same(before)) return;
-    const int n_rep = a.n_heads / a.n_kv_heads;
-    const int t_local = row / n_rep, t = cut.z * a.tq + t_local;
-    const bool valid = t_local < a.tq && t < a.count[cut.x];
+    const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq >> 1;
+    const int t_local = row / n_rep, t = cut.z * a.tq + half * tqh + t_local;
+    if (t_local >= tqh || t >= a.count[cut.x]) return;
     // the pieces: CTA i - 1's last, then the first ones of CTAs i, i + 1, ... (empty where the next begins at the
     // same chunk)
     float M = -INFINITY, L = 0.f;
@@ -445,13 +594,13 @@ __global__ void __launch_bounds__(128) k_attn_chunk_join(const ChunkArgs a, int 
 #pragma unroll
     for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
     auto add = [&](int slot) {
-        const float2 ml = __ldcg(a.part_ml + slot * 128 + row);
-        if (!valid || (ml.x == -INFINITY && ml.y == 0.f)) return;
+        const float2 ml = __ldcg(a.part_ml + (2 * slot + half) * 128 + row);
+        if (ml.x == -INFINITY && ml.y == 0.f) return;
         const float Mn = fmaxf(M, ml.x);
         const float c = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml.x - Mn);
         M = Mn;
         L = fmaf(L, c, ml.y * w);
-        const float4* part = reinterpret_cast<const float4*>(a.partial + (size_t)slot * (128 * 128)) + row;
+        const float4* part = reinterpret_cast<const float4*>(a.partial + (size_t)(2 * slot + half) * (128 * 128)) + row;
 #pragma unroll
         for (int q = 0; q < kJoinCols / 4; ++q) {
             const float4 v = __ldcg(part + (blockIdx.y * (kJoinCols / 4) + q) * 128);
@@ -470,7 +619,6 @@ __global__ void __launch_bounds__(128) k_attn_chunk_join(const ChunkArgs a, int 
         if (!more) break;
         at = next;
     }
-    if (!valid) return;
     bf16* dst = static_cast<bf16*>(a.o) + ((size_t)cut.x * a.tokens + t) * a.n_heads * 128 +
                 (size_t)(cut.y * n_rep + row - t_local * n_rep) * 128 + blockIdx.y * kJoinCols;
     const float inv = 1.f / L;
@@ -514,13 +662,14 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
         k.start += b0;
         k.count += b0;
         k.pages.table += (size_t)b0 * a.pages.stride;
-        if (!make_tmap_q3d(&mq, k.q, a.n_heads, k.batch * a.tokens, n_rep, a.tq)) return cudaErrorInvalidValue;
-        // persistent: one CTA per SM at most (stretches of work assigned on the device)
-        const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kChunkMaxCtas / 2);
+        k.tq = 2 * (128 / n_rep);
+        if (!make_tmap_q3d(&mq, k.q, a.n_heads, k.batch * a.tokens, n_rep, k.tq / 2)) return cudaErrorInvalidValue;
+        // persistent: one CTA per SM at most (work assigned on the device)
+        const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kChunkMaxCtas);
         r = launch_pdl(k_attn_chunk, dim3(n_ctas), dim3(kThreads), SMEM_BYTES, s, mq, mk, mv, k);
         if (r != cudaSuccess) return r;
-        if (a.whole || n_ctas == 1) continue;
-        r = launch_pdl(k_attn_chunk_join, dim3(n_ctas - 1, 128 / kJoinCols), dim3(128), 0, s, k, (int)n_ctas);
+        if (n_ctas == 1) continue;
+        r = launch_pdl(k_attn_chunk_join, dim3(n_ctas - 1, 128 / kJoinCols, 2), dim3(128), 0, s, k, (int)n_ctas);
         if (r != cudaSuccess) return r;
     }
     return cudaSuccess;

@@ -64,6 +64,11 @@ __device__ __forceinline__ float add_bf16_hi(uint32_t p, float acc) {
         : "=f"(r) : "r"(p), "f"(acc));
     return r;
 }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // max(a, b, c), exact like every max
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -119,12 +124,14 @@ __device__ __forceinline__ void umma8_ss(uint32_t d, uint64_t a, uint64_t b, uin
 #undef LLAMA_BOFF
 }
 // A from tensor memory (step ks 8 columns on: 16 bf16 per row), B MN-major from
-// shared memory (step ks 16 rows = B_STEP16 x 16 bytes on).
+// shared memory (step ks 16 rows = B_STEP16 x 16 bytes on).  Step 0 accumulates when accumulate_first
+// is non-zero.
 template <int B_STEP16>
-__device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate_first = 0) {
     asm volatile(
         "{\n\t.reg .pred pf, pt;\n\t.reg .b32 t<8>;\n\t.reg .b64 b<8>;\n\t"
-        "setp.ne.b32 pf, %3, %3;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
+        "setp.ne.b32 pf, %11, 0;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
         "add.u32 t1, %1, 8;\n\tadd.s64 b1, %2, %4;\n\t"
         "add.u32 t2, %1, 16;\n\tadd.s64 b2, %2, %5;\n\t"
         "add.u32 t3, %1, 24;\n\tadd.s64 b3, %2, %6;\n\t"
@@ -142,7 +149,7 @@ __device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [t7], b7, %3, pt;\n\t"
         "}"
         ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "n"(B_STEP16), "n"(2 * B_STEP16), "n"(3 * B_STEP16), "n"(4 * B_STEP16),
-        "n"(5 * B_STEP16), "n"(6 * B_STEP16), "n"(7 * B_STEP16)
+        "n"(5 * B_STEP16), "n"(6 * B_STEP16), "n"(7 * B_STEP16), "r"(accumulate_first)
         : "memory");
 }
 
@@ -238,6 +245,15 @@ __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map,
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%3, %3, %3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(group), "l"(policy)
+        : "memory");
+}
+
+// The same through the default policy: rows that several tiles read.
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int group) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(group)
         : "memory");
 }
 
