@@ -10,10 +10,12 @@
 // Two streams run side by side so that one's MMAs cover the other's softmax: the halves of a tile, or, when a tile has
 // 128 rows at most (few new tokens), its even and its odd chunks, joined at the end.  A stream's S, P (over S) and O
 // take 128 columns each for S and O.  Roles:
-//   warp 0, 2     K (and Q), V: a page (at most 128 rows) is one TMA copy issued by a lane of its own, and lands as row
+//   warp 0        Q, K and V: a page (at most 128 rows) is one TMA copy issued by a lane of its own, and lands as row
 //                 groups of 8 with their two 64-column halves side by side (make_tmap_pages)
-//   warp 1        tensor memory, MMAs: PV of a stream, then its next S, then the other stream's
-//   warp 3        the CTA's pieces (attn_chunk.cuh), a few ahead
+//   warps 1, 3    tensor memory, MMAs of stream 0, of stream 1: S, then PV when P is there, the first 64 keys ahead of
+//                 the rest.  (One thread for both streams spent 3500 cycles on a step of each, most of
+//                 them on waits and commits: 8192 tokens of 32 / 8 heads took 730 us.)
+//   warp 2        the CTA's pieces (attn_chunk.cuh), a few ahead
 //   warps 4..11   softmax of stream 0, of stream 1
 //   warps 12..15  scaling of O, care of V, output
 // Rows do not see what lies behind them: P is 0 there, and so that 0 times an infinity or a NaN does not reach
@@ -39,13 +41,13 @@ constexpr int OFF_V = OFF_K + 4 * kSub;       // [stage] V
 constexpr int OFF_BAR = OFF_V + 4 * kSub;
 constexpr int OFF_PIECES = OFF_BAR + 512;     // the ring of pieces, and a word for each
 constexpr int OFF_SCALE = OFF_PIECES + 256;   // [stream][128] floats
-constexpr int OFF_ML = OFF_SCALE + 1024;      // [piece parity][stream][128] (m, l)
+constexpr int OFF_ML = OFF_SCALE + 1024;      // [parity][stream][128] (m, l): see ml_full
 constexpr int OFF_SEQS = OFF_ML + 4096;
 constexpr int SMEM_BYTES = OFF_SEQS + (int)sizeof(ChunkSeqs) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int TM_S = 0, TM_O = 256;           // + 128 per stream
 
-// A CTA's pieces as its roles read them: warp 3 walks the CTA's share a few pieces ahead and leaves them in a ring
+// A CTA's pieces as its roles read them: warp 2 walks the CTA's share a few pieces ahead and leaves them in a ring
 // (a walk in every role took registers that the softmax does not have).
 constexpr int kRing = 4;
 static_assert(sizeof(ChunkPiece) == 40, "ring entries");
@@ -102,22 +104,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sm = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     uint64_t* bars = (uint64_t*)(sm + OFF_BAR);
     uint64_t* q_full = bars + 0;     // TMA -> MMA
-    uint64_t* q_empty = bars + 1;    // MMA (after the piece's last S) -> TMA
+    uint64_t* q_empty = bars + 1;    // MMA (both streams, after their last S of the piece) -> TMA
     uint64_t* k_full = bars + 2;     // [2] TMA -> MMA
-    uint64_t* k_empty = bars + 4;    // [2] MMA (after the chunk's last S) -> TMA
+    uint64_t* k_empty = bars + 4;    // [2] MMA (two arrivals: of each stream, or of the one that takes the chunk) -> TMA
     uint64_t* v_full = bars + 6;     // [2] TMA -> MMA, care of V
-    uint64_t* v_empty = bars + 8;    // [2] MMA (after the chunk's last PV) -> TMA
+    uint64_t* v_empty = bars + 8;    // [2] MMA (as k_empty, after PV) -> TMA
     uint64_t* s_full = bars + 10;    // [stream] MMA -> softmax
-    uint64_t* p_full = bars + 12;    // [stream] softmax (P written) -> MMA
-    uint64_t* sc_full = bars + 14;   // [stream] softmax (scale of O written) -> warps 12..15
-    uint64_t* o_ready = bars + 16;   // [stream] warps 12..15 (O scaled, V cared for) -> MMA
-    uint64_t* pv_done = bars + 18;   // [stream] MMA -> warps 12..15
-    // [piece parity][stream] softmax (m and l of the piece written) -> warps 12..15: the softmax may be through with
-    // the next piece before they have looked at this one's
-    uint64_t* ml_full = bars + 20;
-    uint64_t* pc_full = bars + 24;   // [4] warp 3 -> all roles: piece j in entry j % 4
-    uint64_t* pc_free = bars + 28;   // [4] warps 12..15 (piece done, so every role is) -> warp 3
-    uint32_t* tmem_holder = (uint32_t*)(bars + 32);
+    uint64_t* p_half = bars + 12;    // [stream] softmax (P of keys 0..63 written) -> MMA
+    uint64_t* p_full = bars + 14;    // [stream] softmax (the rest written) -> MMA
+    uint64_t* sc_full = bars + 16;   // [stream] softmax (scale of O written) -> warps 12..15
+    uint64_t* o_ready = bars + 18;   // [stream] warps 12..15 (O scaled, V cared for) -> MMA
+    uint64_t* pv_done = bars + 20;   // [stream] MMA -> warps 12..15
+    // [parity][stream] softmax (m and l of the piece written) -> warps 12..15: the softmax may be through with
+    // the stream's next piece (pieces it has steps of are counted) before they have looked at this one's
+    uint64_t* ml_full = bars + 22;
+    uint64_t* pc_full = bars + 26;   // [4] warp 2 -> all roles: piece j in entry j % 4
+    // [4] -> warp 2: warps 12..15 (piece done), and MMA and softmax of stream 1 (entry read: they may have no step of
+    // the piece; the other roles have read it when it is done)
+    uint64_t* pc_free = bars + 30;
+    uint32_t* tmem_holder = (uint32_t*)(bars + 34);
     ChunkPiece* pieces = (ChunkPiece*)(sm + OFF_PIECES);
     int* poison = (int*)(sm + OFF_PIECES + kRing * sizeof(ChunkPiece));   // [4] j + 1: care was taken of piece j's V
     ChunkSeqs& seqs = *reinterpret_cast<ChunkSeqs*>(sm + OFF_SEQS);
@@ -129,13 +134,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(q_full, 1);
-        ptx::mbar_init(q_empty, 1);
+        ptx::mbar_init(q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&k_full[i], 1);
-            ptx::mbar_init(&k_empty[i], 1);
+            ptx::mbar_init(&k_empty[i], 2);
             ptx::mbar_init(&v_full[i], 1);
-            ptx::mbar_init(&v_empty[i], 1);
+            ptx::mbar_init(&v_empty[i], 2);
             ptx::mbar_init(&s_full[i], 1);
+            ptx::mbar_init(&p_half[i], 4);
             ptx::mbar_init(&p_full[i], 4);
             ptx::mbar_init(&sc_full[i], 4);
             ptx::mbar_init(&o_ready[i], 4);
@@ -145,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kRing; ++i) {
             ptx::mbar_init(&pc_full[i], 1);
-            ptx::mbar_init(&pc_free[i], 4);
+            ptx::mbar_init(&pc_free[i], 9);
             poison[i] = 0;
         }
         ptx::fence_mbar_init();
@@ -154,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(tmem_holder, 512);
         ptx::tmem_relinquish();
     }
-    if (warp == 2) chunk_seqs(a, seqs, blockIdx.x == 0);
+    if (warp == 0) chunk_seqs(a, seqs, blockIdx.x == 0);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -170,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp < 4) {
         ptx::setmaxnreg_dec<kRegsCtrl>();
-        if (warp == 3) {
+        if (warp == 2) {
             // ------------------------------------------------------------------ the pieces
             if (lane == 0) {
                 ChunkWalk walk(a, seqs, blockIdx.x, gridDim.x);
@@ -185,137 +191,117 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!more) break;
                 }
             }
-        } else if (warp == 0 || warp == 2) {
-            // ------------------------------------------------------------------ TMA producers (K and Q, V), whole warps
-            const bool is_k = (warp == 0);
-            const CUtensorMap* map = is_k ? &mK : &mV;
-            uint64_t* full = is_k ? k_full : v_full;
-            uint64_t* empty = is_k ? k_empty : v_empty;
-            uint8_t* ring = sm + (is_k ? OFF_K : OFF_V);
+        } else if (warp == 0) {
+            // ------------------------------------------------------------------ TMA producer, the whole warp
             const int shift = a.pages.shift, ps = 1 << shift, box = min(ps, kAttnChunk);
-            if (lane == 0) ptx::prefetch_tmap(map);
-            int gi = 0, n_q = 0;   // chunks and Q tiles issued
+            if (lane == 0) {
+                ptx::prefetch_tmap(&mQ);
+                ptx::prefetch_tmap(&mK);
+                ptx::prefetch_tmap(&mV);
+            }
+            int kc = 0, vc = 0, n_q = 0;   // chunks of K and V, Q tiles issued
             bool ok = true;
             ChunkPiece p;
+            // chunk c's copy into the next stage of a ring; lane = page of the chunk
+            auto copy = [&](const CUtensorMap* map, int c, int id, int off, uint64_t* full, uint64_t* empty, int& gi) {
+                const int st = gi & 1;
+                int go = 1;
+                if (lane == 0 && gi >= 2) go = ptx::mbar_wait(&empty[st], ((gi >> 1) & 1) ^ 1, err);
+                ok = __shfl_sync(0xffffffffu, go, 0);
+                if (!ok) return;
+                const int n = (min(kAttnChunk, p.kv_last + 1 - c * kAttnChunk) + box - 1) / box;
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], n * box * 256);
+                __syncwarp();
+                if (lane < n) {
+                    const int row = ((id * a.n_kv_heads + p.g) << shift) + (c * kAttnChunk & (ps - 1));
+                    tma_load_page(sm + off + st * 2 * kSub + lane * box * 256, map, &full[st], row >> 3);
+                }
+                ++gi;
+            };
             for (int j = 0; ok && piece(j, p); ++j) {
-                // lane = page of a chunk: its id is read a chunk ahead of its copy
-                auto pages_in = [&](int c) { return (min(kAttnChunk, p.kv_last + 1 - c * kAttnChunk) + box - 1) / box; };
+                // page ids are read a chunk ahead of their copies
                 auto lookup = [&](int c) -> int {
-                    if (c >= p.c1 || lane >= pages_in(c)) return 0;
-                    const int id = page_of(a.pages, p.b, (c * kAttnChunk >> shift) + lane, is_k ? err : nullptr);
+                    if (c >= p.c1 || lane * box >= min(kAttnChunk, p.kv_last + 1 - c * kAttnChunk)) return 0;
+                    const int id = page_of(a.pages, p.b, (c * kAttnChunk >> shift) + lane, err);
                     return max(id, 0);   // recorded; the rows are undefined, the copy stays inside the cache
                 };
-                int next = lookup(p.c0);
-                if (is_k) {
-                    int go = 1;
-                    if (lane == 0 && j >= 1) go = ptx::mbar_wait(q_empty, (j - 1) & 1, err);
-                    if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
-                    if (lane == 0) {
-                        const int halves = is_pair(p, tqh) ? 2 : 1;
-                        ptx::mbar_arrive_expect_tx(q_full, halves * 2 * n_rep * tqh * 128);
-                        for (int x = 0; x < 2 * halves; ++x)
-                            asm volatile(
-                                "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                                " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(sm + OFF_Q + x * kSub)),
-                                "l"(reinterpret_cast<uint64_t>(&mQ)), "r"(ptx::smem_u32(q_full)), "r"((x & 1) * 64),
-                                "r"(p.g * n_rep), "r"(p.b * a.tokens + p.t0 + (x >> 1) * tqh)
-                                : "memory");
-                    }
-                    ++n_q;
+                int id = lookup(p.c0), before = 0;
+                int go = 1;
+                if (lane == 0 && j >= 1) go = ptx::mbar_wait(q_empty, (j - 1) & 1, err);
+                if (!__shfl_sync(0xffffffffu, go, 0)) break;
+                if (lane == 0) {
+                    const int halves = is_pair(p, tqh) ? 2 : 1;
+                    ptx::mbar_arrive_expect_tx(q_full, halves * 2 * n_rep * tqh * 128);
+                    for (int x = 0; x < 2 * halves; ++x)
+                        asm volatile(
+                            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(ptx::smem_u32(sm + OFF_Q + x * kSub)),
+                            "l"(reinterpret_cast<uint64_t>(&mQ)), "r"(ptx::smem_u32(q_full)), "r"((x & 1) * 64),
+                            "r"(p.g * n_rep), "r"(p.b * a.tokens + p.t0 + (x >> 1) * tqh)
+                            : "memory");
                 }
-                for (int c = p.c0; c < p.c1; ++c, ++gi) {
-                    const int st = gi & 1;
-                    int go = 1;
-                    if (lane == 0 && gi >= 2) go = ptx::mbar_wait(&empty[st], ((gi >> 1) & 1) ^ 1, err);
-                    if (!__shfl_sync(0xffffffffu, go, 0)) { ok = false; break; }
-                    const int n = pages_in(c), id = next;
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], n * box * 256);
-                    __syncwarp();
-                    if (lane < n) {
-                        const int row = ((id * a.n_kv_heads + p.g) << shift) + (c * kAttnChunk & (ps - 1));
-                        tma_load_page(ring + st * 2 * kSub + lane * box * 256, map, &full[st], row >> 3);
-                    }
-                    next = lookup(c + 1);
+                ++n_q;
+                // K a chunk ahead of V: its stage is free earlier
+                for (int c = p.c0; ok && c <= p.c1; ++c) {
+                    const int next = lookup(c + 1);
+                    if (c < p.c1) copy(&mK, c, id, OFF_K, k_full, k_empty, kc);
+                    if (ok && c > p.c0) copy(&mV, c - 1, before, OFF_V, v_full, v_empty, vc);
+                    before = id;
+                    id = next;
                 }
             }
             // no copy may still be landing when the CTA exits (it has landed already
             // unless a wait above gave up)
             if (lane == 0) {
                 if (n_q > 0) ptx::mbar_wait_drain(q_full, (n_q - 1) & 1);
-                for (int i = max(0, gi - 2); i < gi; ++i) ptx::mbar_wait_drain(&full[i & 1], (i >> 1) & 1);
+                for (int i = max(0, kc - 2); i < kc; ++i) ptx::mbar_wait_drain(&k_full[i & 1], (i >> 1) & 1);
+                for (int i = max(0, vc - 2); i < vc; ++i) ptx::mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
             }
         } else if (lane == 0) {
-            // ------------------------------------------------------------------ MMA issuer
-            // Steps in order, S up to one step per stream ahead of PV.  S of a stream may be issued once
-            // its last PV is (the MMAs run in issue order, so P has been read when S overwrites it; the softmax
-            // has read S before it wrote P).
-            struct { int j, i, n; bool pair; } sp{0, 0, 0, false}, vp{0, 0, 0, false};   // step of the next S, PV
-            auto open = [&](auto& x) {
-                ChunkPiece p;
-                x.i = 0;
-                x.n = 0;
-                if (!piece(x.j, p)) return;
-                x.n = steps_of(p, tqh);
-                x.pair = is_pair(p, tqh);
-            };
-            int kc = 0, vc = 0;               // chunks of K and V used up
-            int ns[2] = {0, 0}, nv[2] = {0, 0};   // S and PV issued per stream
+            // ------------------------------------------------------------------ MMA issuer of stream s
+            // S(i + 1) follows PV(i) at once: MMAs run in issue order, so P(i) has been read when S(i + 1)
+            // overwrites it, and the softmax has read S(i) before it wrote P(i).
+            const int s = warp >> 1;
+            const uint32_t s_tmem = tmem + TM_S + s * 128, o_tmem = tmem + TM_O + s * 128;
+            const uint64_t k_desc = desc_with_stride(ptx::sw128_kmajor_desc(ptx::smem_u32(sm + OFF_K)), 2048);
+            const uint64_t v_desc = desc_with_stride(ptx::sw128_mnmajor_desc(ptx::smem_u32(sm + OFF_V), 1024), 2048);
+            int c0 = 0, step = 0;   // chunks of the pieces before, steps of the stream
             bool ok = true;
-            // S of the next step, if its stream is free; `wait`: also when its operands are still on their way
-            auto issue_s = [&](bool wait) -> bool {
-                if (sp.n == 0) return true;
-                const int s = sp.i & 1, k = kc & 1;
-                if (ns[s] != nv[s]) return true;
-                if (!wait && sp.i == 0 && !ptx::mbar_try_wait(q_full, sp.j & 1)) return true;
-                if (sp.i == 0 && !ptx::mbar_wait(q_full, sp.j & 1, err)) return false;
-                if (!ptx::mbar_wait(&k_full[k], (kc >> 1) & 1, err)) return false;
-                ptx::tc_fence_after();
-                const uint32_t q_addr = ptx::smem_u32(sm + OFF_Q + (sp.pair ? s : 0) * 2 * kSub);
-                const uint32_t k_addr = ptx::smem_u32(sm + OFF_K + k * 2 * kSub);
-                umma8_ss<kSub / 16, 1024 / 16, false>(tmem + TM_S + s * 128, ptx::sw128_kmajor_desc(q_addr),
-                                                      desc_with_stride(ptx::sw128_kmajor_desc(k_addr), 2048), IDESC_S);
-                ptx::umma_commit(&s_full[s]);
-                if (!sp.pair || s == 1) {
-                    ptx::umma_commit(&k_empty[k]);
-                    ++kc;
+            ChunkPiece p;
+            for (int j = 0; ok && piece(j, p); ++j) {
+                const bool pair = is_pair(p, tqh);
+                const int n = steps_of_stream(p, tqh, s);
+                const uint64_t q_desc = ptx::sw128_kmajor_desc(ptx::smem_u32(sm + OFF_Q + (pair ? s : 0) * 2 * kSub));
+                if (s == 1) ptx::mbar_arrive(&pc_free[j % kRing]);
+                if (!ptx::mbar_wait(q_full, j & 1, err)) break;
+                if (n == 0) ptx::mbar_arrive(q_empty);
+                int c = c0 + (pair ? 0 : s);
+                for (int i = 0; i < n; ++i, ++step, c += pair ? 1 : 2) {
+                    const int st = c & 1;
+                    const uint64_t stage = (uint64_t)(st * (2 * kSub / 16));
+                    if (!ptx::mbar_wait(&k_full[st], (c >> 1) & 1, err)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    umma8_ss<kSub / 16, 1024 / 16, false>(s_tmem, q_desc, k_desc + stage, IDESC_S);
+                    ptx::umma_commit(&s_full[s]);
+                    ptx::umma_commit(&k_empty[st]);
+                    if (!pair) ptx::umma_commit(&k_empty[st]);
+                    if (i == n - 1) ptx::umma_commit(q_empty);
+                    // o_ready first: with it the stage's last chunk has been used, so that the parity of v_full
+                    // tells this chunk's landing (the other stream may have used that one)
+                    if (!ptx::mbar_wait(&o_ready[s], step & 1, err)) { ok = false; break; }
+                    if (!ptx::mbar_wait(&v_full[st], (c >> 1) & 1, err)) { ok = false; break; }
+                    if (!ptx::mbar_wait(&p_half[s], step & 1, err)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    // P of keys 16ks.. in columns 8ks.., V rows 16ks..
+                    umma4_ts<256>(o_tmem, s_tmem, v_desc + stage, IDESC_PV, i > 0);
+                    if (!ptx::mbar_wait(&p_full[s], step & 1, err)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    umma4_ts<256>(o_tmem, s_tmem + 32, v_desc + stage + 4 * 256, IDESC_PV, 1);
+                    ptx::umma_commit(&pv_done[s]);
+                    ptx::umma_commit(&v_empty[st]);
+                    if (!pair) ptx::umma_commit(&v_empty[st]);
                 }
-                ++ns[s];
-                if (++sp.i == sp.n) {
-                    ptx::umma_commit(q_empty);
-                    ++sp.j;
-                    open(sp);
-                }
-                return true;
-            };
-            open(sp);
-            open(vp);
-            while (ok && vp.n > 0) {
-                const int s = vp.i & 1, v = vc & 1;
-                if (ns[s] == nv[s]) ok = issue_s(true);
-                if (ok) ok = issue_s(false);   // the other stream's
-                if (!ok || ns[s] == nv[s]) {
-                    if (ok) continue;
-                    break;
-                }
-                if (!ptx::mbar_wait(&o_ready[s], nv[s] & 1, err)) break;
-                if (!ptx::mbar_wait(&v_full[v], (vc >> 1) & 1, err)) break;
-                if (!ptx::mbar_wait(&p_full[s], nv[s] & 1, err)) break;
-                ptx::tc_fence_after();
-                const uint32_t v_addr = ptx::smem_u32(sm + OFF_V + v * 2 * kSub);
-                // P of keys 16ks.. in columns 8ks.., V rows 16ks..
-                umma8_ts<256>(tmem + TM_O + s * 128, tmem + TM_S + s * 128,
-                              desc_with_stride(ptx::sw128_mnmajor_desc(v_addr, 1024), 2048), IDESC_PV, vp.i >= 2);
-                ptx::umma_commit(&pv_done[s]);
-                if (!vp.pair || s == 1) {
-                    ptx::umma_commit(&v_empty[v]);
-                    ++vc;
-                }
-                ++nv[s];
-                if (++vp.i == vp.n) {
-                    ++vp.j;
-                    open(vp);
-                }
-                ok = issue_s(false);
+                c0 += p.c1 - p.c0;
             }
         }
     } else if (warp < 12) {
@@ -328,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_taddr = tmem + ((uint32_t)(quarter * 32) << 16) + TM_S + s * 128;
         float* scale = reinterpret_cast<float*>(sm + OFF_SCALE) + s * 128 + row;
         const float c = a.scale_log2;
-        int step = 0;   // of the stream
+        int step = 0, took = 0;   // of the stream: steps, parity of its pieces
         bool ok = true;
         for (int j = 0;; ++j) {
             int left, last_key, ahead;   // chunks of the stream; the row's last key from the chunk's first; keys a step
@@ -342,6 +328,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int rows = min(p.t1 - p.t0 - first, tqh) * n_rep;
                 live = quarter * 32 < rows;
                 ahead = pair ? kAttnChunk : 2 * kAttnChunk;
+                __syncwarp();
+                if (s == 1 && lane == 0) ptx::mbar_arrive(&pc_free[j % kRing]);
                 last_key = row < rows ? p.pos0 + first + t_local - (p.c0 + (pair ? 0 : s)) * kAttnChunk : -1;
             }
             float m = -INFINITY, l = 0.f;
@@ -401,6 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             packed[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
                         }
                         tmem_st8(s_taddr + e0 / 2, packed);
+                        if (e0 == 48) {   // keys 0..63
+                            ptx::tmem_wait_st();
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(&p_half[s]);
+                        }
                     }
                     float a0, a1;
                     unpack2(add2(sum0, sum1), a0, a1);
@@ -408,15 +402,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_wait_st();
                 } else if (lane == 0) {
                     ptx::mbar_arrive(&sc_full[s]);
+                    ptx::mbar_arrive(&p_half[s]);
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&p_full[s]);
             }
             if (any) {
-                reinterpret_cast<float2*>(sm + OFF_ML)[((j & 1) * 2 + s) * 128 + row] = make_float2(m, l);
+                reinterpret_cast<float2*>(sm + OFF_ML)[(took * 2 + s) * 128 + row] = make_float2(m, l);
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&ml_full[(j & 1) * 2 + s]);
+                if (lane == 0) ptx::mbar_arrive(&ml_full[took * 2 + s]);
+                took ^= 1;
             }
         }
     } else {
@@ -430,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2* ml = reinterpret_cast<const float2*>(sm + OFF_ML) + row;
         bool ok = true;
         int vc = 0, done[2] = {0, 0};   // chunks, steps of a stream
-        uint32_t ml_phase = 0;          // parities of ml_full
+        uint32_t took = 0, ml_phase = 0;   // parities of the streams' pieces, of ml_full
         ChunkPiece p;
         for (int j = 0; named_bar_and(1, 128, piece(j, p)); ++j) {   // all four warps go on or none
             const bool pair = is_pair(p, tqh);
@@ -438,6 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int i = 0; i < steps; ++i) {
                 const int s = i & 1;
+                // S of this step is done, so PV of the stream's last one is, and the V stage of this chunk
+                // holds no other
+                if (ok) ok = ptx::mbar_wait(&sc_full[s], done[s] & 1, err);
                 if (!pair || s == 0) {
                     const int key0 = (p.c0 + (pair ? i >> 1 : i)) * kAttnChunk, v = vc & 1;
                     if (key0 + kAttnChunk - 1 > p.pos0) {
@@ -448,7 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ++vc;
                 }
-                if (ok) ok = ptx::mbar_wait(&sc_full[s], done[s] & 1, err);
                 const int half = pair ? s : 0;
                 const bool live = quarter * 32 < min(p.t1 - p.t0 - half * tqh, tqh) * n_rep;
                 if (i >= 2 && live) {
@@ -483,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // this half's streams: `half`, or 0 and (with two chunks or more) 1
                 const bool both = !pair && steps > 1;
                 for (int s = half; s <= (both ? 1 : half); ++s) {
-                    const int at = (j & 1) * 2 + s;
+                    const int at = (took >> s & 1) * 2 + s;
                     if (ok) ok = ptx::mbar_wait(&ml_full[at], ml_phase >> at & 1, err);
                     ml_phase ^= 1u << at;
                     if (ok) ok = ptx::mbar_wait(&pv_done[s], (done[s] - 1) & 1, err);
@@ -492,10 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int tokens = min(p.t1 - p.t0 - half * tqh, tqh);
                 if (quarter * 32 >= tokens * n_rep) continue;
                 const bool valid = t_local < tokens;
-                float2 x = ml[((j & 1) * 2 + half) * 128];
+                float2 x = ml[((took >> half & 1) * 2 + half) * 128];
                 float w0 = 1.f, w1 = 0.f;   // weights of the streams
                 if (both) {
-                    const float2 y = ml[((j & 1) * 2 + 1) * 128];
+                    const float2 y = ml[((took >> 1) * 2 + 1) * 128];
                     // a stream without a key above -inf has no weight
                     const float M = fmaxf(x.x, y.x);
                     w0 = x.x == -INFINITY && x.y == 0.f ? 0.f : ex2(x.x - M);
@@ -561,6 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            took ^= steps > 1 ? 3 : 1;
             ptx::tc_fence_before();   // O read: the next piece's first PV may overwrite it
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&pc_free[j % kRing]);

@@ -124,14 +124,12 @@ __device__ __forceinline__ void umma8_ss(uint32_t d, uint64_t a, uint64_t b, uin
 #undef LLAMA_BOFF
 }
 // A from tensor memory (step ks 8 columns on: 16 bf16 per row), B MN-major from
-// shared memory (step ks 16 rows = B_STEP16 x 16 bytes on).  Step 0 accumulates when accumulate_first
-// is non-zero.
+// shared memory (step ks 16 rows = B_STEP16 x 16 bytes on).
 template <int B_STEP16>
-__device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate_first = 0) {
+__device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
     asm volatile(
         "{\n\t.reg .pred pf, pt;\n\t.reg .b32 t<8>;\n\t.reg .b64 b<8>;\n\t"
-        "setp.ne.b32 pf, %11, 0;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
+        "setp.ne.b32 pf, %3, %3;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
         "add.u32 t1, %1, 8;\n\tadd.s64 b1, %2, %4;\n\t"
         "add.u32 t2, %1, 16;\n\tadd.s64 b2, %2, %5;\n\t"
         "add.u32 t3, %1, 24;\n\tadd.s64 b3, %2, %6;\n\t"
@@ -149,7 +147,26 @@ __device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [t7], b7, %3, pt;\n\t"
         "}"
         ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "n"(B_STEP16), "n"(2 * B_STEP16), "n"(3 * B_STEP16), "n"(4 * B_STEP16),
-        "n"(5 * B_STEP16), "n"(6 * B_STEP16), "n"(7 * B_STEP16), "r"(accumulate_first)
+        "n"(5 * B_STEP16), "n"(6 * B_STEP16), "n"(7 * B_STEP16)
+        : "memory");
+}
+
+// Four steps of the same chain (64 keys of P): the second half accumulates from its step 0 on.
+template <int B_STEP16>
+__device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate_first) {
+    asm volatile(
+        "{\n\t.reg .pred pf, pt;\n\t.reg .b32 t<4>;\n\t.reg .b64 b<4>;\n\t"
+        "setp.ne.b32 pf, %7, 0;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
+        "add.u32 t1, %1, 8;\n\tadd.s64 b1, %2, %4;\n\t"
+        "add.u32 t2, %1, 16;\n\tadd.s64 b2, %2, %5;\n\t"
+        "add.u32 t3, %1, 24;\n\tadd.s64 b3, %2, %6;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pf;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t1], b1, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t2], b2, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t3], b3, %3, pt;\n\t"
+        "}"
+        ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "n"(B_STEP16), "n"(2 * B_STEP16), "n"(3 * B_STEP16),
+        "r"(accumulate_first)
         : "memory");
 }
 
