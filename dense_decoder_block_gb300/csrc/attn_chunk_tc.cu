@@ -13,11 +13,10 @@
 //   warp 0        Q, K and V: a page (at most 128 rows) is one TMA copy issued by a lane of its own, and lands as row
 //                 groups of 8 with their two 64-column halves side by side (make_tmap_pages)
 //   warps 1, 3    tensor memory, MMAs of stream 0, of stream 1: S, then PV when P is there, the first 64 keys ahead of
-//                 the rest.  (One thread for both streams spent 3500 cycles on a step of each, most of
-//                 them on waits and commits: 8192 tokens of 32 / 8 heads took 730 us.)
+//                 the rest; whole warps, see umma_ss_warp
 //   warp 2        the CTA's pieces (attn_chunk.cuh), a few ahead
-//   warps 4..11   softmax of stream 0, of stream 1
-//   warps 12..15  scaling of O, care of V, output
+//   warps 4..11   softmax of stream 0, of stream 1; scaling of O
+//   warps 12..15  care of V, output
 // Rows do not see what lies behind them: P is 0 there, and so that 0 times an infinity or a NaN does not reach
 // O, such values of a tile's newest positions are taken out of the chunk's V and added to the rows that do see
 // them at the end (an infinity or NaN in O either way).
@@ -30,7 +29,7 @@ namespace llama {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kRegsCtrl = 56, kRegsSoftmax = 192, kRegsOut = 72;
+constexpr int kRegsCtrl = 72, kRegsSoftmax = 168, kRegsOut = 104;
 constexpr int kRegsNeeded = 128 * kRegsCtrl + 256 * kRegsSoftmax + 128 * kRegsOut;
 static_assert(kRegsNeeded <= 128 * kThreads, "register split exceeds the launch allocation");
 constexpr float kSlack = 8.f;
@@ -40,8 +39,7 @@ constexpr int OFF_K = 4 * kSub;               // [stage] K, row groups of 8
 constexpr int OFF_V = OFF_K + 4 * kSub;       // [stage] V
 constexpr int OFF_BAR = OFF_V + 4 * kSub;
 constexpr int OFF_PIECES = OFF_BAR + 512;     // the ring of pieces, and a word for each
-constexpr int OFF_SCALE = OFF_PIECES + 256;   // [stream][128] floats
-constexpr int OFF_ML = OFF_SCALE + 1024;      // [parity][stream][128] (m, l): see ml_full
+constexpr int OFF_ML = OFF_PIECES + 256;      // [parity][stream][128] (m, l): see ml_full
 constexpr int OFF_SEQS = OFF_ML + 4096;
 constexpr int SMEM_BYTES = OFF_SEQS + (int)sizeof(ChunkSeqs) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -96,6 +94,8 @@ __device__ __forceinline__ int steps_of_stream(const ChunkPiece& p, int tqh, int
     const int n = p.c1 - p.c0;
     return is_pair(p, tqh) ? n : (n + 1 - s) >> 1;
 }
+// The first chunk with keys behind the tile's first position: from here on V wants care.
+__device__ __forceinline__ int care_from(const ChunkPiece& p) { return max(p.c0, (p.pos0 + 1) / kAttnChunk); }
 
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_chunk(const __grid_constant__ CUtensorMap mQ, const __grid_constant__ CUtensorMap mK,
@@ -107,14 +107,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* q_empty = bars + 1;    // MMA (both streams, after their last S of the piece) -> TMA
     uint64_t* k_full = bars + 2;     // [2] TMA -> MMA
     uint64_t* k_empty = bars + 4;    // [2] MMA (two arrivals: of each stream, or of the one that takes the chunk) -> TMA
-    uint64_t* v_full = bars + 6;     // [2] TMA -> MMA, care of V
+    uint64_t* v_full = bars + 6;     // [2] TMA -> MMA
     uint64_t* v_empty = bars + 8;    // [2] MMA (as k_empty, after PV) -> TMA
-    uint64_t* s_full = bars + 10;    // [stream] MMA -> softmax
-    uint64_t* p_half = bars + 12;    // [stream] softmax (P of keys 0..63 written) -> MMA
+    uint64_t* s_full = bars + 10;    // [stream] MMA -> softmax (S done, and PV of the step before)
+    uint64_t* p_half = bars + 12;    // [stream] softmax (P of keys 0..63 written, O scaled) -> MMA
     uint64_t* p_full = bars + 14;    // [stream] softmax (the rest written) -> MMA
-    uint64_t* sc_full = bars + 16;   // [stream] softmax (scale of O written) -> warps 12..15
-    uint64_t* o_ready = bars + 18;   // [stream] warps 12..15 (O scaled, V cared for) -> MMA
-    uint64_t* pv_done = bars + 20;   // [stream] MMA -> warps 12..15
+    uint64_t* care_req = bars + 16;  // [V stage] MMA (a chunk that wants care has landed) -> warps 12..15
+    uint64_t* care_done = bars + 18; // [V stage] warps 12..15 -> MMA
+    uint64_t* pv_done = bars + 20;   // [stream] MMA (after the last PV of a piece) -> warps 12..15
     // [parity][stream] softmax (m and l of the piece written) -> warps 12..15: the softmax may be through with
     // the stream's next piece (pieces it has steps of are counted) before they have looked at this one's
     uint64_t* ml_full = bars + 22;
@@ -122,12 +122,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // [4] -> warp 2: warps 12..15 (piece done), and MMA and softmax of stream 1 (entry read: they may have no step of
     // the piece; the other roles have read it when it is done)
     uint64_t* pc_free = bars + 30;
-    uint32_t* tmem_holder = (uint32_t*)(bars + 34);
+    uint64_t* o_free = bars + 34;    // [stream] warps 12..15 (O of a piece read) -> MMA
+    uint64_t* lag = bars + 36;       // MMA of stream 0 -> MMA of stream 1: it may begin the piece
+    uint32_t* tmem_holder = (uint32_t*)(bars + 37);
     ChunkPiece* pieces = (ChunkPiece*)(sm + OFF_PIECES);
     int* poison = (int*)(sm + OFF_PIECES + kRing * sizeof(ChunkPiece));   // [4] j + 1: care was taken of piece j's V
     ChunkSeqs& seqs = *reinterpret_cast<ChunkSeqs*>(sm + OFF_SEQS);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform
     ptx::griddep_wait();   // lengths, tables, rows: whatever the stream holds in front
     const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq >> 1;
     int* err = a.err;
@@ -135,6 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         ptx::mbar_init(q_full, 1);
         ptx::mbar_init(q_empty, 2);
+        ptx::mbar_init(lag, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&k_full[i], 1);
             ptx::mbar_init(&k_empty[i], 2);
@@ -143,8 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_half[i], 4);
             ptx::mbar_init(&p_full[i], 4);
-            ptx::mbar_init(&sc_full[i], 4);
-            ptx::mbar_init(&o_ready[i], 4);
+            ptx::mbar_init(&care_req[i], 1);
+            ptx::mbar_init(&care_done[i], 4);
+            ptx::mbar_init(&o_free[i], 4);
             ptx::mbar_init(&pv_done[i], 1);
             ptx::mbar_init(&ml_full[i], 4);
             ptx::mbar_init(&ml_full[2 + i], 4);
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
     // dependents start only once this CTA holds its tensor memory
     if (threadIdx.x == 0) ptx::griddep_launch_dependents();
 
@@ -257,51 +261,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = max(0, kc - 2); i < kc; ++i) ptx::mbar_wait_drain(&k_full[i & 1], (i >> 1) & 1);
                 for (int i = max(0, vc - 2); i < vc; ++i) ptx::mbar_wait_drain(&v_full[i & 1], (i >> 1) & 1);
             }
-        } else if (lane == 0) {
-            // ------------------------------------------------------------------ MMA issuer of stream s
+        } else {
+            // ------------------------------------------------------------------ MMA issuer of stream s, the whole warp
             // S(i + 1) follows PV(i) at once: MMAs run in issue order, so P(i) has been read when S(i + 1)
             // overwrites it, and the softmax has read S(i) before it wrote P(i).
             const int s = warp >> 1;
+            auto uniform = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
             const uint32_t s_tmem = tmem + TM_S + s * 128, o_tmem = tmem + TM_O + s * 128;
             const uint64_t k_desc = desc_with_stride(ptx::sw128_kmajor_desc(ptx::smem_u32(sm + OFF_K)), 2048);
             const uint64_t v_desc = desc_with_stride(ptx::sw128_mnmajor_desc(ptx::smem_u32(sm + OFF_V), 1024), 2048);
             int c0 = 0, step = 0;   // chunks of the pieces before, steps of the stream
+            uint32_t cared = 0;     // parities of care_done
             bool ok = true;
+            // every lane waits; the warp goes on or gives up as one
+            auto wait = [&](uint64_t* bar, int parity) { return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity, err)); };
             ChunkPiece p;
-            for (int j = 0; ok && piece(j, p); ++j) {
-                const bool pair = is_pair(p, tqh);
-                const int n = steps_of_stream(p, tqh, s);
+            for (int j = 0; ok && __all_sync(0xffffffffu, piece(j, p)); ++j) {
+                const bool pair = uniform(is_pair(p, tqh));
+                const int n = uniform(steps_of_stream(p, tqh, s)), chunks = uniform(p.c1 - p.c0);
+                const int care = c0 + uniform(care_from(p) - p.c0);   // first chunk (counted as c) that wants care
                 const uint64_t q_desc = ptx::sw128_kmajor_desc(ptx::smem_u32(sm + OFF_Q + (pair ? s : 0) * 2 * kSub));
-                if (s == 1) ptx::mbar_arrive(&pc_free[j % kRing]);
-                if (!ptx::mbar_wait(q_full, j & 1, err)) break;
-                if (n == 0) ptx::mbar_arrive(q_empty);
+                __syncwarp();
+                if (s == 1 && lane == 0) ptx::mbar_arrive(&pc_free[j % kRing]);
+                if (!wait(q_full, j & 1)) break;
+                if (n == 0) {
+                    if (lane == 0) ptx::mbar_arrive(q_empty);
+                    if (j > 0 && !wait(&o_free[s], (j - 1) & 1)) break;
+                }
                 int c = c0 + (pair ? 0 : s);
-                for (int i = 0; i < n; ++i, ++step, c += pair ? 1 : 2) {
+                const int by = pair ? 1 : 2;
+                // S of chunk c, the i-th of the piece
+                auto issue_s = [&](int c, int i) -> bool {
                     const int st = c & 1;
-                    const uint64_t stage = (uint64_t)(st * (2 * kSub / 16));
-                    if (!ptx::mbar_wait(&k_full[st], (c >> 1) & 1, err)) { ok = false; break; }
+                    if (!wait(&k_full[st], (c >> 1) & 1)) return false;
                     ptx::tc_fence_after();
-                    umma8_ss<kSub / 16, 1024 / 16, false>(s_tmem, q_desc, k_desc + stage, IDESC_S);
-                    ptx::umma_commit(&s_full[s]);
-                    ptx::umma_commit(&k_empty[st]);
-                    if (!pair) ptx::umma_commit(&k_empty[st]);
-                    if (i == n - 1) ptx::umma_commit(q_empty);
-                    // o_ready first: with it the stage's last chunk has been used, so that the parity of v_full
-                    // tells this chunk's landing (the other stream may have used that one)
-                    if (!ptx::mbar_wait(&o_ready[s], step & 1, err)) { ok = false; break; }
-                    if (!ptx::mbar_wait(&v_full[st], (c >> 1) & 1, err)) { ok = false; break; }
-                    if (!ptx::mbar_wait(&p_half[s], step & 1, err)) { ok = false; break; }
+                    const uint64_t k = k_desc + st * (2 * kSub / 16);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_ss_warp(s_tmem, q_desc + (ks / 4 * (kSub / 16) + ks % 4 * 2), k + (ks / 4 * 64 + ks % 4 * 2), IDESC_S,
+                                     ks > 0);
+                    umma_commit_warp(&s_full[s]);
+                    umma_commit_warp(&k_empty[st]);
+                    if (!pair) umma_commit_warp(&k_empty[st]);
+                    if (i == n - 1) umma_commit_warp(q_empty);
+                    return true;
+                };
+                // Streams that begin together stay together: their MMAs take turns, both then sit in their softmax and the
+                // tensor cores are idle for it.  Stream 1 of a pair begins when stream 0 has its first P: from then on
+                // the MMAs of one run under the softmax of the other (8192 tokens of 32 / 8 heads 450 -> 374 us, 4096
+                // of 64 behind 4096 648 -> 532).  Streams that share a tile's chunks wait for copies instead.
+                const bool together = !pair || n < 2;
+                if (s == 0 && together && lane == 0) ptx::mbar_arrive(lag);
+                if (s == 1 && !wait(lag, j & 1)) break;
+                if (n > 0) ok = issue_s(c, 0);
+                for (int i = 0; ok && i < n; ++i, ++step, c += by) {
+                    const int st = c & 1;
+                    const uint64_t v = v_desc + st * (2 * kSub / 16);
+                    // O of the last piece is read (and with that every chunk before is used, so that the
+                    // parity of v_full tells this chunk's landing)
+                    if (i == 0 && j > 0 && !wait(&o_free[s], (j - 1) & 1)) { ok = false; break; }
+                    if (!wait(&v_full[st], (c >> 1) & 1)) { ok = false; break; }
+                    if (c >= care) {
+                        if ((!pair || s == 0) && lane == 0) ptx::mbar_arrive(&care_req[st]);
+                        if (!wait(&care_done[st], cared >> st & 1)) { ok = false; break; }
+                        cared ^= 1u << st;
+                    }
+                    if (!wait(&p_half[s], step & 1)) { ok = false; break; }
+                    if (s == 0 && i == 0 && !together && lane == 0) ptx::mbar_arrive(lag);
                     ptx::tc_fence_after();
                     // P of keys 16ks.. in columns 8ks.., V rows 16ks..
-                    umma4_ts<256>(o_tmem, s_tmem, v_desc + stage, IDESC_PV, i > 0);
-                    if (!ptx::mbar_wait(&p_full[s], step & 1, err)) { ok = false; break; }
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) umma_ts_warp(o_tmem, s_tmem + ks * 8, v + ks * 256, IDESC_PV, i > 0 || ks > 0);
+                    if (!wait(&p_full[s], step & 1)) { ok = false; break; }
                     ptx::tc_fence_after();
-                    umma4_ts<256>(o_tmem, s_tmem + 32, v_desc + stage + 4 * 256, IDESC_PV, 1);
-                    ptx::umma_commit(&pv_done[s]);
-                    ptx::umma_commit(&v_empty[st]);
-                    if (!pair) ptx::umma_commit(&v_empty[st]);
+#pragma unroll
+                    for (int ks = 4; ks < 8; ++ks) umma_ts_warp(o_tmem, s_tmem + ks * 8, v + ks * 256, IDESC_PV, 1);
+                    umma_commit_warp(&v_empty[st]);
+                    if (!pair) umma_commit_warp(&v_empty[st]);
+                    if (i == n - 1) umma_commit_warp(&pv_done[s]);
+                    else ok = issue_s(c + by, i + 1);
                 }
-                c0 += p.c1 - p.c0;
+                // the other stream's chunks that want care, of which this one hears nothing
+                if (!pair)
+                    for (c = max(care, c0); c < c0 + chunks; ++c)
+                        if (((c - c0) & 1) != s) cared ^= 1u << (c & 1);
+                c0 += chunks;
             }
         }
     } else if (warp < 12) {
@@ -312,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = quarter * 32 + lane;
         const int t_local = row / n_rep;
         const uint32_t s_taddr = tmem + ((uint32_t)(quarter * 32) << 16) + TM_S + s * 128;
-        float* scale = reinterpret_cast<float*>(sm + OFF_SCALE) + s * 128 + row;
+        const uint32_t o_taddr = tmem + ((uint32_t)(quarter * 32) << 16) + TM_O + s * 128;
         const float c = a.scale_log2;
         int step = 0, took = 0;   // of the stream: steps, parity of its pieces
         bool ok = true;
@@ -333,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 last_key = row < rows ? p.pos0 + first + t_local - (p.c0 + (pair ? 0 : s)) * kAttnChunk : -1;
             }
             float m = -INFINITY, l = 0.f;
-            const bool any = left > 0;
+            const int steps = left;
 #pragma unroll 1
             for (; left > 0; --left, ++step, last_key -= ahead) {
                 if (ok) ok = ptx::mbar_wait(&s_full[s], step & 1, err);
@@ -364,9 +408,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sc = ex2(m - mn);
                         m = mn;
                     }
-                    *scale = sc;
-                    __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&sc_full[s]);
+                    if (left < steps && __any_sync(0xffffffffu, sc != 1.f)) {
+                        // O of the steps before (complete: see s_full); seldom after the first few
+#pragma unroll 1
+                        for (int cb = 0; cb < 128; cb += 16) {
+                            float o[16];
+                            ptx::tmem_ld<16>(o_taddr + cb, o);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= sc;
+                            ptx::tmem_st16(o_taddr + cb, o);
+                        }
+                    }
                     const float ref = m == -INFINITY ? 0.f : m;
                     const uint64_t c2 = pack2(c, c), nm2 = pack2(-ref, -ref);
                     uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
@@ -401,14 +454,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l = __fmaf_rn(l, sc, a0 + a1);
                     ptx::tmem_wait_st();
                 } else if (lane == 0) {
-                    ptx::mbar_arrive(&sc_full[s]);
                     ptx::mbar_arrive(&p_half[s]);
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&p_full[s]);
             }
-            if (any) {
+            if (steps > 0) {
                 reinterpret_cast<float2*>(sm + OFF_ML)[(took * 2 + s) * 128 + row] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&ml_full[took * 2 + s]);
@@ -416,61 +468,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        // ------------------------------------------------------------------ scaling of O, care of V, output
+        // ------------------------------------------------------------------ care of V, output
         ptx::setmaxnreg_dec<kRegsOut>();
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const int t_local = row / n_rep, h_local = row - t_local * n_rep;
         const uint32_t o_taddr = tmem + ((uint32_t)(quarter * 32) << 16) + TM_O;
-        const float* scale = reinterpret_cast<const float*>(sm + OFF_SCALE) + row;
         const float2* ml = reinterpret_cast<const float2*>(sm + OFF_ML) + row;
         bool ok = true;
-        int vc = 0, done[2] = {0, 0};   // chunks, steps of a stream
+        int c0 = 0;                        // chunks of the pieces before
         uint32_t took = 0, ml_phase = 0;   // parities of the streams' pieces, of ml_full
+        uint32_t cared = 0;                // parities of care_req
         ChunkPiece p;
         for (int j = 0; named_bar_and(1, 128, piece(j, p)); ++j) {   // all four warps go on or none
             const bool pair = is_pair(p, tqh);
             const int steps = steps_of(p, tqh);
 #pragma unroll 1
-            for (int i = 0; i < steps; ++i) {
-                const int s = i & 1;
-                // S of this step is done, so PV of the stream's last one is, and the V stage of this chunk
-                // holds no other
-                if (ok) ok = ptx::mbar_wait(&sc_full[s], done[s] & 1, err);
-                if (!pair || s == 0) {
-                    const int key0 = (p.c0 + (pair ? i >> 1 : i)) * kAttnChunk, v = vc & 1;
-                    if (key0 + kAttnChunk - 1 > p.pos0) {
-                        if (ok) ok = ptx::mbar_wait(&v_full[v], (vc >> 1) & 1, err);
-                        if (key0 + row > p.pos0 && care_for_v(sm + OFF_V + v * 2 * kSub, row, key0 + row > p.kv_last))
-                            poison[j % kRing] = j + 1;
-                        ptx::fence_proxy_async_smem();
-                    }
-                    ++vc;
-                }
-                const int half = pair ? s : 0;
-                const bool live = quarter * 32 < min(p.t1 - p.t0 - half * tqh, tqh) * n_rep;
-                if (i >= 2 && live) {
-                    const float sc = scale[s * 128];
-                    if (__any_sync(0xffffffffu, sc != 1.f)) {
-                        if (ok) ok = ptx::mbar_wait(&pv_done[s], (done[s] - 1) & 1, err);
-                        ptx::tc_fence_after();
-#pragma unroll 1
-                        for (int cb = 0; cb < 128; cb += 32) {
-                            float o[32];
-                            ptx::tmem_ld<32>(o_taddr + s * 128 + cb, o);
-                            ptx::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= sc;
-                            ptx::tmem_st32(o_taddr + s * 128 + cb, o);
-                        }
-                        ptx::tmem_wait_st();
-                    }
-                }
-                ptx::tc_fence_before();
+            for (int c = care_from(p); c < p.c1; ++c) {
+                const int at = c0 + c - p.c0, v = at & 1, key = c * kAttnChunk + row;
+                if (ok) ok = ptx::mbar_wait(&care_req[v], cared >> v & 1, err);
+                if (ok) ok = ptx::mbar_wait(&v_full[v], (at >> 1) & 1, err);
+                cared ^= 1u << v;
+                if (key > p.pos0 && care_for_v(sm + OFF_V + v * 2 * kSub, row, key > p.kv_last)) poison[j % kRing] = j + 1;
+                ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&o_ready[s]);
-                ++done[s];
+                if (lane == 0) ptx::mbar_arrive(&care_done[v]);
             }
+            c0 += p.c1 - p.c0;
             // output: the halves one after another, or the two streams of one half joined
             named_bar_and(1, 128, true);   // poison is written
             const bool poisoned = poison[j % kRing] == j + 1;
@@ -484,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int at = (took >> s & 1) * 2 + s;
                     if (ok) ok = ptx::mbar_wait(&ml_full[at], ml_phase >> at & 1, err);
                     ml_phase ^= 1u << at;
-                    if (ok) ok = ptx::mbar_wait(&pv_done[s], (done[s] - 1) & 1, err);
+                    if (ok) ok = ptx::mbar_wait(&pv_done[s], took >> s & 1, err);
                 }
                 ptx::tc_fence_after();
                 const int tokens = min(p.t1 - p.t0 - half * tqh, tqh);
@@ -562,7 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             took ^= steps > 1 ? 3 : 1;
             ptx::tc_fence_before();   // O read: the next piece's first PV may overwrite it
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&pc_free[j % kRing]);
+            if (lane == 0) {
+                ptx::mbar_arrive(&o_free[0]);
+                ptx::mbar_arrive(&o_free[1]);
+                ptx::mbar_arrive(&pc_free[j % kRing]);
+            }
         }
     }
 

@@ -151,22 +151,28 @@ __device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b
         : "memory");
 }
 
-// Four steps of the same chain (64 keys of P): the second half accumulates from its step 0 on.
-template <int B_STEP16>
-__device__ __forceinline__ void umma4_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate_first) {
+// The same chains issued by a whole converged warp, one elected lane executing them.  With values that are
+// uniform over the warp the compiler keeps descriptors in uniform registers, and an MMA costs the warp a few issue
+// slots; from a branch that one lane takes it costs dozens, and a busy scheduler then holds the tensor cores back (S and PV of
+// a 128-key chunk beside two warps of multiply-adds on the scheduler: 1025 cycles this way, 2080 the other).
+__device__ __forceinline__ void umma_ss_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred pf, pt;\n\t.reg .b32 t<4>;\n\t.reg .b64 b<4>;\n\t"
-        "setp.ne.b32 pf, %7, 0;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
-        "add.u32 t1, %1, 8;\n\tadd.s64 b1, %2, %4;\n\t"
-        "add.u32 t2, %1, 16;\n\tadd.s64 b2, %2, %5;\n\t"
-        "add.u32 t3, %1, 24;\n\tadd.s64 b3, %2, %6;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pf;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t1], b1, %3, pt;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t2], b2, %3, pt;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t3], b3, %3, pt;\n\t"
-        "}"
-        ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc), "n"(B_STEP16), "n"(2 * B_STEP16), "n"(3 * B_STEP16),
-        "r"(accumulate_first)
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts_warp(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_u32(bar))
         : "memory");
 }
 
