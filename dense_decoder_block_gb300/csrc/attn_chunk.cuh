@@ -4,11 +4,11 @@
 // its work is the keys that its last token attends and a constant for starting and storing a tile.  Lengths
 // and counts are read on the device, so both ways of dealing tiles out hold for any mixture of sequences
 // under any bound:
-//   - many tiles (kRounds per CTA or more): whole tiles in rounds, the longest of a sequence first and every other round
+//   - many tiles: whole tiles in rounds, the longest of a sequence first and every other round
 //     from the other end.  CTAs then walk the keys of a head at about the same time, and find them in L2
 //     (stretches of a line as below: 8192 tokens of 32 / 8 heads 920 us, in rounds 755, one tile a CTA at a time);
 //   - few: all tiles -- sequences in order, their KV heads, their tiles -- lie one after another on a line of length
-//     W, and CTA i of n takes the stretch [W i / n, W (i + 1) / n), cut at chunks of kAttnChunk keys (chunk_cut): a
+//     W, and CTA i of n takes the stretch from i W / n on, cut at chunks of kAttnChunk keys (chunk_cut): a
 //     tile that crosses the end of a stretch is shared by several CTAs, each of which leaves the softmax
 //     partial (m, l, o) of its chunks, and a second kernel joins them.
 #pragma once
@@ -43,10 +43,13 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s);
 constexpr int kTileKeys = 128;
 // The least chunks of a piece: what joining costs.
 constexpr int kMinPiece = 2;
-// The least work of a CTA (keys) for which another one is started.
+// The least work of a CTA (keys) for which tiles are split.
 constexpr int kMinStretch = 512;
-// Tiles per CTA from which on they are dealt out whole.
+// Tiles per CTA from which on they are dealt out whole ...
 constexpr int kRounds = 4;
+// ... and fewer are too where the last round's idle CTAs cost less than this work per CTA: what the partials and their
+// joining cost (2048 tokens of 32 / 8 heads, 256 tiles: split 65 us, whole 47).
+constexpr int kJoinKeys = 768;
 
 // The sequences of a launch (shared memory).
 struct ChunkSeqs {
@@ -121,6 +124,11 @@ struct ChunkPiece {
     int c0, c1, n;    // of n chunks
 };
 
+// a / b of numbers that are not negative, in 32 bits where they fit (a 64-bit division takes a microsecond of one lane)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
+
 // A CTA's pieces in order.
 struct ChunkWalk {
     const ChunkSeqs& s;
@@ -137,12 +145,16 @@ struct ChunkWalk {
         j = 0;
         w = w0 = w1 = 0;
         g = y = n_qt = start = count = 0;
-        rounds = (long long)s.tiles[batch] * n_kv >= (long long)kRounds * n_ctas;
+        const long long tiles = (long long)s.tiles[batch] * n_kv;
+        rounds = tiles >= (long long)kRounds * n_ctas;
+        if (!rounds && tiles > 0)
+            rounds = quotient(tiles + n_ctas - 1, n_ctas) * quotient(total, tiles) <= quotient(total, n_ctas) + kJoinKeys;
         if (rounds) return;
-        const int n = (int)min((long long)n_ctas, max(1ll, total / kMinStretch));
+        const int n = (int)min((long long)n_ctas, max(tiles, total / kMinStretch));
         if (cta >= n || total == 0) return;
-        w0 = total * cta / n;
-        w1 = total * (cta + 1) / n;
+        const long long each = quotient(total, n);
+        w0 = each * cta;
+        w1 = cta == n - 1 ? total : w0 + each;
         int lo = 0, hi = batch - 1;   // the last sequence that begins at or before w0: one with work
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -153,7 +165,7 @@ struct ChunkWalk {
         load();
         const long long one = s.pre[b + 1] - s.pre[b];
         long long r = w0 - s.pre[b] * n_kv;
-        g = (int)(r / one);
+        g = (int)quotient(r, one);
         r -= g * one;
         lo = 0;
         hi = n_qt - 1;

@@ -164,7 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_alloc(tmem_holder, 512);
         ptx::tmem_relinquish();
     }
-    if (warp == 0) chunk_seqs(a, seqs, blockIdx.x == 0);
+    if (warp == 2) {
+        chunk_seqs(a, seqs, blockIdx.x == 0);
+        __syncwarp();
+    }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -284,10 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (s == 1 && lane == 0) ptx::mbar_arrive(&pc_free[j % kRing]);
                 if (!wait(q_full, j & 1)) break;
-                if (n == 0) {
-                    if (lane == 0) ptx::mbar_arrive(q_empty);
-                    if (j > 0 && !wait(&o_free[s], (j - 1) & 1)) break;
-                }
                 int c = c0 + (pair ? 0 : s);
                 const int by = pair ? 1 : 2;
                 // S of chunk c, the i-th of the piece
@@ -313,7 +312,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool together = !pair || n < 2;
                 if (s == 0 && together && lane == 0) ptx::mbar_arrive(lag);
                 if (s == 1 && !wait(lag, j & 1)) break;
-                if (n > 0) ok = issue_s(c, 0);
+                if (n > 0) {
+                    ok = issue_s(c, 0);
+                } else {   // no step of this piece (stream 1)
+                    if (lane == 0) ptx::mbar_arrive(q_empty);
+                    if (j > 0 && !wait(&o_free[s], (j - 1) & 1)) break;
+                }
                 for (int i = 0; ok && i < n; ++i, ++step, c += by) {
                     const int st = c & 1;
                     const uint64_t v = v_desc + st * (2 * kSub / 16);
@@ -535,35 +539,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     w1 *= inv;
                 }
 #pragma unroll 1
-                for (int cb = 0; cb < 128; cb += 16) {
-                    float o[16];
-                    ptx::tmem_ld<16>(o_taddr + half * 128 + cb, o);
+                for (int cb = 0; cb < 128; cb += 32) {
+                    float o[32];
+                    ptx::tmem_ld<32>(o_taddr + half * 128 + cb, o);
                     if (both) {
-                        float q[16];
-                        ptx::tmem_ld<16>(o_taddr + 128 + cb, q);
+                        float q[32];
+                        ptx::tmem_ld<32>(o_taddr + 128 + cb, q);
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __fmaf_rn(o[e], w0, q[e] * w1);
+                        for (int e = 0; e < 32; ++e) o[e] = __fmaf_rn(o[e], w0, q[e] * w1);
                     } else {
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] *= w0;
+                        for (int e = 0; e < 32; ++e) o[e] *= w0;
                     }
                     if (!valid || !ok) {
                     } else if (split) {
 #pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4)
+                        for (int q4 = 0; q4 < 8; ++q4)
                             *reinterpret_cast<float4*>(part + (cb / 4 + q4) * 512) =
                                 make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
                     } else {
-                        uint32_t packed[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
-                            packed[e] = *reinterpret_cast<const uint32_t*>(&v2);
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            uint32_t packed[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[8 * q4 + 2 * e], o[8 * q4 + 2 * e + 1]);
+                                packed[e] = *reinterpret_cast<const uint32_t*>(&v2);
+                            }
+                            *reinterpret_cast<uint4*>(dst + cb + 8 * q4) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
                         }
-                        *reinterpret_cast<uint4*>(dst + cb) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-                        *reinterpret_cast<uint4*>(dst + cb + 8) = make_uint4(packed[4], packed[5], packed[6], packed[7]);
                     }
                 }
                 if (poisoned && valid && ok) {
@@ -601,63 +607,106 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the pieces of a split tile: CTA (i, part of the columns, half), i the first CTA that begins inside the tile.
-// Pieces in ascending order: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M the largest m_p.
-constexpr int kJoinCols = 16;
+// Joins the pieces of the split tiles, in ascending order: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M the
+// largest m_p.  Every CTA reads all cuts and lists the split tiles; an item is one half of a tile and kJoinCols columns,
+// thread = row.  The loads of several pieces go out together.
+constexpr int kJoinCols = 8, kJoinBatch = 6;
+constexpr int kJoinThreads = 128;
 
-__global__ void __launch_bounds__(128) k_attn_chunk_join(const ChunkArgs a, int n_ctas) {
+__global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArgs a, int n_ctas) {
+    __shared__ int4 s_cut[kChunkMaxCtas];
+    __shared__ int s_first[kChunkMaxCtas];
+    __shared__ unsigned s_word[8];   // bit i: a split tile's list begins with CTA i
+    static_assert(kChunkMaxCtas <= 2 * kJoinThreads && kJoinThreads == 128, "two CTAs a thread, words of 32");
     ptx::griddep_wait();
-    const int i = blockIdx.x + 1, row = threadIdx.x, half = blockIdx.z;
-    const int4 cut = __ldcg(a.cuts + i), before = __ldcg(a.cuts + i - 1);
-    auto same = [&](const int4& x) { return x.w > 0 && x.x == cut.x && x.y == cut.y && x.z == cut.z; };
-    if (cut.w == 0 || same(before)) return;
-    const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq >> 1;
-    const int t_local = row / n_rep, t = cut.z * a.tq + half * tqh + t_local;
-    if (t_local >= tqh || t >= a.count[cut.x]) return;
-    // the pieces: CTA i - 1's last, then the first ones of CTAs i, i + 1, ... (empty where the next begins at the
-    // same chunk)
-    float M = -INFINITY, L = 0.f;
-    float o[kJoinCols];
-#pragma unroll
-    for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
-    auto add = [&](int slot) {
-        const float2 ml = __ldcg(a.part_ml + (2 * slot + half) * 128 + row);
-        if (ml.x == -INFINITY && ml.y == 0.f) return;
-        const float Mn = fmaxf(M, ml.x);
-        const float c = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml.x - Mn);
-        M = Mn;
-        L = fmaf(L, c, ml.y * w);
-        const float4* part = reinterpret_cast<const float4*>(a.partial + (size_t)(2 * slot + half) * (128 * 128)) + row;
-#pragma unroll
-        for (int q = 0; q < kJoinCols / 4; ++q) {
-            const float4 v = __ldcg(part + (blockIdx.y * (kJoinCols / 4) + q) * 128);
-            o[4 * q] = fmaf(o[4 * q], c, v.x * w);
-            o[4 * q + 1] = fmaf(o[4 * q + 1], c, v.y * w);
-            o[4 * q + 2] = fmaf(o[4 * q + 2], c, v.z * w);
-            o[4 * q + 3] = fmaf(o[4 * q + 3], c, v.w * w);
-        }
+    for (int i = threadIdx.x; i < n_ctas; i += kJoinThreads) s_cut[i] = __ldcg(a.cuts + i);
+    __syncthreads();
+    // CTA j begins inside the tile that CTA i begins inside of
+    auto same = [&](int i, int j) {
+        return s_cut[j].w > 0 && s_cut[j].x == s_cut[i].x && s_cut[j].y == s_cut[i].y && s_cut[j].z == s_cut[i].z;
     };
-    add(2 * (i - 1) + 1);
-    int4 at = cut;
-    for (int j = i; j < n_ctas; ++j) {
-        const int4 next = j + 1 < n_ctas ? __ldcg(a.cuts + j + 1) : make_int4(0, 0, 0, 0);
-        const bool more = same(next);
-        if (!more || next.w > at.w) add(2 * j);
-        if (!more) break;
-        at = next;
-    }
-    bf16* dst = static_cast<bf16*>(a.o) + ((size_t)cut.x * a.tokens + t) * a.n_heads * 128 +
-                (size_t)(cut.y * n_rep + row - t_local * n_rep) * 128 + blockIdx.y * kJoinCols;
-    const float inv = 1.f / L;
+    bool first[2];
 #pragma unroll
-    for (int e = 0; e < kJoinCols; e += 8) {
+    for (int x = 0; x < 2; ++x) {
+        const int i = x * kJoinThreads + threadIdx.x;
+        first[x] = i > 0 && i < n_ctas && s_cut[i].w > 0 && !same(i, i - 1);
+        const unsigned word = __ballot_sync(0xffffffffu, first[x]);
+        if ((threadIdx.x & 31) == 0) s_word[i >> 5] = word;
+    }
+    __syncthreads();
+    int n_split = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int i = x * kJoinThreads + threadIdx.x;
+        int at = __popc(s_word[i >> 5] & ((1u << (i & 31)) - 1));
+        for (int w = 0; w < i >> 5; ++w) at += __popc(s_word[w]);
+        if (first[x]) s_first[at] = i;
+    }
+#pragma unroll
+    for (int w = 0; w < 8; ++w) n_split += __popc(s_word[w]);
+    __syncthreads();
+    const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq >> 1, row = threadIdx.x, t_local = row / n_rep;
+    const int items = n_split * 2 * (128 / kJoinCols);
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int cols = item % (128 / kJoinCols), half = item / (128 / kJoinCols) % 2, i = s_first[item / (2 * (128 / kJoinCols))];
+        const int4 cut = s_cut[i];
+        const int t = cut.z * a.tq + half * tqh + t_local;
+        if (t_local >= tqh || t >= a.count[cut.x]) continue;
+        int end = i + 1;   // CTAs that begin in the tile: i .. end - 1
+        while (end < n_ctas && same(i, end)) ++end;
+        // piece k of end - i + 1: CTA i - 1's last, then the first ones of CTAs i, i + 1, ...; a piece is empty where the
+        // next begins at the same chunk
+        auto slot_of = [&](int k) { return k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1); };
+        auto ml_of = [&](int k) {
+            const int j = i + k - 1;
+            if (k > 0 && j + 1 < end && s_cut[j + 1].w == s_cut[j].w) return make_float2(-INFINITY, 0.f);
+            return __ldcg(a.part_ml + (2 * slot_of(k) + half) * 128 + row);
+        };
+        const int n = end - i + 1;
+        float M = -INFINITY, L = 0.f;
+        float o[kJoinCols];
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+        for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
+            float2 ml[kJoinBatch];
+            float4 v[kJoinBatch][kJoinCols / 4];
+#pragma unroll
+            for (int x = 0; x < kJoinBatch; ++x) {
+                if (k0 + x >= n) break;
+                ml[x] = ml_of(k0 + x);
+                const float4* part =
+                    reinterpret_cast<const float4*>(a.partial + (size_t)(2 * slot_of(k0 + x) + half) * (128 * 128)) + row;
+#pragma unroll
+                for (int q = 0; q < kJoinCols / 4; ++q) v[x][q] = __ldcg(part + (cols * (kJoinCols / 4) + q) * 128);
+            }
+#pragma unroll
+            for (int x = 0; x < kJoinBatch; ++x) {
+                if (k0 + x >= n) break;
+                if (ml[x].x == -INFINITY && ml[x].y == 0.f) continue;   // nothing (or an empty piece: its part is not written)
+                const float Mn = fmaxf(M, ml[x].x);
+                const float c = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml[x].x - Mn);
+                M = Mn;
+                L = fmaf(L, c, ml[x].y * w);
+#pragma unroll
+                for (int q = 0; q < kJoinCols / 4; ++q) {
+                    o[4 * q] = fmaf(o[4 * q], c, v[x][q].x * w);
+                    o[4 * q + 1] = fmaf(o[4 * q + 1], c, v[x][q].y * w);
+                    o[4 * q + 2] = fmaf(o[4 * q + 2], c, v[x][q].z * w);
+                    o[4 * q + 3] = fmaf(o[4 * q + 3], c, v[x][q].w * w);
+                }
+            }
+        }
+        bf16* dst = static_cast<bf16*>(a.o) + ((size_t)cut.x * a.tokens + t) * a.n_heads * 128 +
+                    (size_t)(cut.y * n_rep + row - t_local * n_rep) * 128 + cols * kJoinCols;
+        const float inv = 1.f / L;
         uint32_t packed[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[e + 2 * q] * inv, o[e + 2 * q + 1] * inv);
+            const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[2 * q] * inv, o[2 * q + 1] * inv);
             packed[q] = *reinterpret_cast<const uint32_t*>(&v2);
         }
-        *reinterpret_cast<uint4*>(dst + e) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        static_assert(kJoinCols == 8, "one vector of bf16");
+        *reinterpret_cast<uint4*>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
     }
 }
 
@@ -695,8 +744,9 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
         const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kChunkMaxCtas);
         r = launch_pdl(k_attn_chunk, dim3(n_ctas), dim3(kThreads), SMEM_BYTES, s, mq, mk, mv, k);
         if (r != cudaSuccess) return r;
-        if (n_ctas == 1) continue;
-        r = launch_pdl(k_attn_chunk_join, dim3(n_ctas - 1, 128 / kJoinCols, 2), dim3(128), 0, s, k, (int)n_ctas);
+        // tiles of fewer chunks than two pieces have are never split (the join costs 3 us without any)
+        if (n_ctas == 1 || a.max_pos < 2 * kMinPiece * kAttnChunk - (kAttnChunk - 1)) continue;
+        r = launch_pdl(k_attn_chunk_join, dim3(8 * n_ctas), dim3(kJoinThreads), 0, s, k, (int)n_ctas);
         if (r != cudaSuccess) return r;
     }
     return cudaSuccess;
