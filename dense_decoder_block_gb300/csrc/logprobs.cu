@@ -7,12 +7,15 @@
 //
 // One pass over the logits.  A row is cut into segments of kSeg logits; a warp takes a segment at a time, all its
 // loads issued ahead, and keeps per lane the running maximum, d and t relative to it (the maximum's own term left out),
-// and per segment the maximum.  The lanes' triples are joined in fp64.  The n largest logits lie in the n segments with
+// and per segment the maximum.  The lanes' triples are joined in a tree, in fp32 (in fp64 the joins took 40 us a row).
+// The n largest logits lie in the n segments with
 // the largest maxima (equal maxima: the first segments): a segment outside has n segments whose best is better than all
 // it has.  So the alternatives come from n segments read a second time, from L2.
 //
-// Few rows are split over a cluster of CTAs (their triples and segment maxima in distributed shared memory, the first
-// CTA finishes the row), many rows take a CTA each.
+// Few rows are split over a cluster of CTAs of 16 warps (their triples and segment maxima in distributed shared memory,
+// the first CTA finishes the row).  Many rows (kManyRows per SM or more) take a CTA of 4 warps each, 8 to an SM: one
+// finishes its row while the others read, and no round of large CTAs ends half empty (924 rows of 128256 logits: 137 us
+// with 16 warps a row).
 #include <algorithm>
 #include <cmath>
 
@@ -23,7 +26,8 @@ namespace llama {
 namespace {
 
 constexpr int kMaxTop = 32;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kFewThreads = 512, kManyThreads = 128;
+constexpr int kManyRows = 4;
 constexpr int kVec = 4;                        // 16-byte vectors of a lane in a segment
 constexpr int kSeg = 32 * 4 * kVec;            // 512 logits
 constexpr int kMaxSegs = (1 << 20) / kSeg + 1; // of a row (one more where it starts off 16 bytes)
@@ -53,27 +57,49 @@ __device__ __forceinline__ unsigned long long order_key(unsigned bits, int place
 }
 __device__ __forceinline__ int place_of(unsigned long long key) { return (int)(0xffffffffu - (unsigned)key); }
 // Sums relative to the maximum m, without the maximum's own term: d = sum e^(z - m) - 1, t = sum e^(z - m) (z - m);
-// m = -inf: none.
+// m = -inf: none.  A NaN in d stays: a row with a NaN or +inf.
 struct Sums {
-    float m;
-    double d, t;
+    float m, d, t;
 };
+// e^x, x <= 0: 2^-22 relative beside the rounding of x log2 e; 0 below 2^-126.
+__device__ __forceinline__ float exp_neg(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+// The larger, NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+constexpr float kFar = -200.f;   // e^kFar is 0: nothing below it (or -inf) is told apart, and 0 * -inf does not arise
 // The two taken together: the larger maximum stays, the other's terms and its 1 move to it.
 __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
-    const Sums &hi = a.m >= b.m ? a : b, &lo = a.m >= b.m ? b : a;
-    if (lo.m == -INFINITY) return hi;
-    const double x = (double)lo.m - (double)hi.m, w = exp(x);
-    Sums r;
-    r.m = hi.m;
-    r.d = hi.d + w * (1.0 + lo.d);
-    r.t = hi.t + w * (lo.t + x * (1.0 + lo.d));
-    return r;
+    const bool first = a.m >= b.m;
+    const float hm = first ? a.m : b.m, hd = first ? a.d : b.d, ht = first ? a.t : b.t;
+    const float lm = first ? b.m : a.m, ld = first ? b.d : a.d, lt = first ? b.t : a.t;
+    const float x = fmaxf(lm - hm, kFar), w = lm == -INFINITY ? 0.f : exp_neg(x), one = 1.f + ld;
+    return Sums{hm, __fmaf_rn(w, one, hd), __fmaf_rn(w, __fmaf_rn(x, one, lt), ht)};
+}
+__device__ __forceinline__ Sums join_warp(Sums s) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Sums x;
+        x.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+        x.d = __shfl_xor_sync(0xffffffffu, s.d, o);
+        x.t = __shfl_xor_sync(0xffffffffu, s.t, o);
+        // both lanes of a pair join in one order, so that all end with the same bits
+        s = lane & o ? join(x, s) : join(s, x);
+    }
+    return s;
 }
 
 // Shared memory of a CTA; the first CTA's is written by all of its cluster.
 struct Shared {
-    Sums part[kMaxCluster * kWarps];
-    Sums total;
+    Sums part[kMaxCluster * kFewThreads / 32];
+    Sums total;                           // m, log(1 + d), -
     int n_cand;
     unsigned long long cand[kSeg];        // candidates
     int segs[kMaxTop];
@@ -89,10 +115,6 @@ __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
 __device__ __forceinline__ void st_remote(uint32_t a, unsigned v) {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
-__device__ __forceinline__ void st_remote(uint32_t a, double v) {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(a), "d"(v) : "memory");
-}
-
 // A lane's vectors of segment `seg`: virtual places seg * kSeg + (i * 32 + lane) * 4 + 0..3 of the row seen from the
 // 16-byte boundary `head` logits in front of it; what lies outside the row is -inf.
 __device__ __forceinline__ void load_segment(const float* row, int head, int vocab, int seg, float (&z)[4 * kVec]) {
@@ -116,8 +138,9 @@ __device__ __forceinline__ void load_segment(const float* row, int head, int voc
     }
 }
 
-template <bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a) {
+template <int kThreads, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logprobs(const LogprobArgs a) {
+    constexpr int kWarps = kThreads / 32;
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.vocab;
     const int ctas = CLUSTER ? (int)(gridDim.x / a.rows) : 1, rank = CLUSTER ? (int)ptx::cluster_rank() : 0;
@@ -137,73 +160,70 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a) {
     const int n_segs = (head + V + kSeg - 1) / kSeg;
     // ---------------------------------------------------------------- the pass: warp x of the row takes segments x, x + n, ...
     const int me = rank * kWarps + warp, all = ctas * kWarps;
-    float m = -INFINITY, d = 0.f, t = 0.f;
-    int bad = 0;
-    float z[4 * kVec], next[4 * kVec];
-    if (me < n_segs) load_segment(row, head, V, me, next);
-    for (int seg = me; seg < n_segs; seg += all) {
-#pragma unroll
-        for (int i = 0; i < 4 * kVec; ++i) z[i] = next[i];
-        if (seg + all < n_segs) load_segment(row, head, V, seg + all, next);
+    Sums s{-INFINITY, 0.f, 0.f};
+    auto take = [&](int seg, float (&z)[4 * kVec]) {
         float mx = z[0];
-        bool odd = false;
+#pragma unroll
+        for (int i = 1; i < 4 * kVec; ++i) mx = fmaxf(mx, z[i]);
+        if (a.n_top > 0) {
+            const unsigned best = __reduce_max_sync(0xffffffffu, order_bits(mx));
+            if (lane == 0) {
+                if (CLUSTER) st_remote(remote(&sh.seg_max[seg], 0), best);
+                else sh.seg_max[seg] = best;
+            }
+        }
+        if (!(mx <= s.m)) {   // a new maximum: the sums move to it, its first place is left out of them
+            const float x = fmaxf(s.m - mx, kFar), w = s.m == -INFINITY ? 0.f : exp_neg(x), one = 1.f + s.d;
+            s.t = w * __fmaf_rn(x, one, s.t);
+            s.d = w * one;
+            s.m = mx;
+            bool own = false;
+#pragma unroll
+            for (int i = 0; i < 4 * kVec; ++i)
+                if (!own && z[i] == mx) {
+                    own = true;
+                    z[i] = -INFINITY;
+                }
+            if (mx == INFINITY) s.d = NAN;
+        }
+        if (s.m == -INFINITY) {   // nothing above -inf so far; a NaN among it stays
+#pragma unroll
+            for (int i = 0; i < 4 * kVec; ++i)
+                if (z[i] != z[i]) s.d = NAN;
+            return;
+        }
+        float d4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4 * kVec; ++i) {
-            mx = fmaxf(mx, z[i]);
-            odd |= !(z[i] < INFINITY);
+            const float x = max_nan(z[i] - s.m, kFar), e = exp_neg(x);
+            d4[i & 3] += e;
+            t4[i & 3] = __fmaf_rn(e, x, t4[i & 3]);
         }
-        bad |= odd;
-        // the lane's running sums: d and t move to the new maximum
-        const float mn = fmaxf(m, mx);
-        if (mn != -INFINITY && !(mn == INFINITY)) {
-            bool own = mn == m;   // the maximum's own term is outside already
-            if (!own && m != -INFINITY) {
-                const float x = m - mn, w = expf(x);   // x may be -inf: maxima of the type's ends
-                t = w > 0.f ? w * fmaf(x, 1.f + d, t) : 0.f;
-                d = w * (1.f + d);
-            }
-            float d4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 4 * kVec; ++i) {
-                const float x = z[i] - mn;
-                float e = expf(x);
-                if (!own && x == 0.f) {   // the first of the maximum's places
-                    own = true;
-                    e = 0.f;
-                }
-                d4[i & 3] += e;
-                if (e > 0.f) t4[i & 3] = fmaf(e, x, t4[i & 3]);
-            }
-            d += (d4[0] + d4[1]) + (d4[2] + d4[3]);
-            t += (t4[0] + t4[1]) + (t4[2] + t4[3]);
-            m = mn;
-        }
-        const unsigned best = __reduce_max_sync(0xffffffffu, order_bits(mx));
-        if (a.n_top > 0 && lane == 0) {
-            if (CLUSTER) st_remote(remote(&sh.seg_max[seg], 0), best);
-            else sh.seg_max[seg] = best;
-        }
+        s.d += (d4[0] + d4[1]) + (d4[2] + d4[3]);
+        s.t += (t4[0] + t4[1]) + (t4[2] + t4[3]);
+    };
+    // a segment's loads go out before the one in front of it is taken
+    float z0[4 * kVec], z1[4 * kVec];
+    int seg = me;
+    if (seg < n_segs) load_segment(row, head, V, seg, z0);
+    while (seg < n_segs) {
+        if (seg + all < n_segs) load_segment(row, head, V, seg + all, z1);
+        take(seg, z0);
+        seg += all;
+        if (seg >= n_segs) break;
+        if (seg + all < n_segs) load_segment(row, head, V, seg + all, z0);
+        take(seg, z1);
+        seg += all;
     }
-    Sums s{m, (double)d, (double)t};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        Sums x;
-        x.m = __shfl_xor_sync(0xffffffffu, s.m, o);
-        x.d = __shfl_xor_sync(0xffffffffu, s.d, o);
-        x.t = __shfl_xor_sync(0xffffffffu, s.t, o);
-        // both lanes of a pair join in one order, so that all end with the same bits
-        s = lane & o ? join(x, s) : join(s, x);
-    }
-    bad = __any_sync(0xffffffffu, bad);
+    s = join_warp(s);
     if (lane == 0) {
         Sums* to = &sh.part[me];
         if (CLUSTER) {
             st_remote(remote(&to->m, 0), __float_as_uint(s.m));
-            st_remote(remote(&to->d, 0), s.d);
-            st_remote(remote(&to->t, 0), bad ? (double)NAN : s.t);
+            st_remote(remote(&to->d, 0), __float_as_uint(s.d));
+            st_remote(remote(&to->t, 0), __float_as_uint(s.t));
         } else {
             *to = s;
-            if (bad) to->t = NAN;
         }
     }
     if (CLUSTER) {
@@ -214,30 +234,15 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a) {
     }
     // ---------------------------------------------------------------- the row's sums (warp 0), the segments of the alternatives (the rest)
     if (warp == 0) {
-        Sums x{-INFINITY, 0.0, 0.0};
-        bool nan = false;
-        for (int w = lane; w < all; w += 32) {
-            const Sums y = sh.part[w];
-            if (y.t != y.t) nan = true;
-            else x = join(x, y);
-        }
-        nan = __any_sync(0xffffffffu, nan);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            Sums y;
-            y.m = __shfl_xor_sync(0xffffffffu, x.m, o);
-            y.d = __shfl_xor_sync(0xffffffffu, x.d, o);
-            y.t = __shfl_xor_sync(0xffffffffu, x.t, o);
-            x = lane & o ? join(y, x) : join(x, y);
-        }
+        Sums x{-INFINITY, 0.f, 0.f};
+        for (int w = lane; w < all; w += 32) x = join(x, sh.part[w]);
+        x = join_warp(x);
         if (lane == 0) {
-            // total: m, log(1 + d); NaN: a NaN or +inf in the row
-            const double lse = nan ? (double)NAN : log1p(x.d);
-            sh.total.m = x.m;
-            sh.total.d = lse;
-            const bool empty = x.m == -INFINITY && !nan;
-            if (a.entropy) a.entropy[r] = empty ? 0.f : (float)(lse - x.t / (1.0 + x.d));
-            if (a.logprobs) a.logprobs[r] = empty ? -INFINITY : (float)((double)(row[token] - x.m) - lse);
+            const bool empty = x.m == -INFINITY && x.d == x.d;
+            const float lse = x.d == x.d ? log1pf(x.d) : NAN;
+            sh.total = Sums{x.m, lse, 0.f};
+            if (a.entropy) a.entropy[r] = empty ? 0.f : lse - x.t / (1.f + x.d);
+            if (a.logprobs) a.logprobs[r] = empty ? -INFINITY : (row[token] - x.m) - lse;
         }
     }
     if (a.n_top == 0) return;
@@ -275,10 +280,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a) {
     const int found = sh.n_cand;
     auto put = [&](int k, unsigned long long key) {
         const float best = from_bits((unsigned)(key >> 32));
-        const double lse = sh.total.d;
+        const float lse = sh.total.d;
         a.top_ids[(size_t)r * n + k] = place_of(key);
         a.top_logprobs[(size_t)r * n + k] =
-            sh.total.m == -INFINITY && lse == lse ? -INFINITY : (float)((double)(best - sh.total.m) - lse);
+            sh.total.m == -INFINITY && lse == lse ? -INFINITY : (best - sh.total.m) - lse;
     };
     if (found <= kSeg) {
         for (int i = tid; i < found; i += kThreads) {
@@ -294,9 +299,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_logprobs(const LogprobArgs a) {
     unsigned long long mine = 0;
     for (int k = 0; k < want; ++k) {
         __syncthreads();
-        const int v = sh.segs[k] * kSeg - head + tid;
-        static_assert(kThreads == kSeg, "a logit a thread");
-        sh.cand[tid] = v >= 0 && v < V ? order_key(order_bits(__ldcg(row + v)), v) : 0ull;
+        for (int i = tid; i < kSeg; i += kThreads) {
+            const int v = sh.segs[k] * kSeg - head + i;
+            sh.cand[i] = v >= 0 && v < V ? order_key(order_bits(__ldcg(row + v)), v) : 0ull;
+        }
         __syncthreads();
         if (warp == 0)
             for (int i = 0; i < kSeg; ++i) {   // insertion: later ones move a lane on
@@ -323,13 +329,18 @@ extern "C" int llama_token_logprobs(const float* logits, int rows, int vocab, co
     if (!logits || (n_top > 0 && (!top_ids || !top_logprobs))) return LLAMA_ERR_INVALID_ARG;
     LogprobArgs a{logits, rows, vocab, n_top, tokens, logprobs, entropy, top_ids, top_logprobs, err_dev};
     cudaStream_t s = (cudaStream_t)stream;
-    // CTAs per row: as many as the device has room for at once (two an SM), each with a segment per warp at least
-    const int room = 2 * device_sm_count() / std::min(rows, 2 * device_sm_count());
-    const int useful = ((vocab + kSeg - 1) / kSeg + kWarps - 1) / kWarps;
-    int ctas = 1;
-    while (2 * ctas <= std::min({room, useful, kMaxCluster})) ctas *= 2;
-    const cudaError_t e = ctas == 1
-                              ? launch_pdl(k_logprobs<false>, dim3(rows), dim3(kThreads), 0, s, a)
-                              : launch_pdl_cluster(k_logprobs<true>, dim3(rows * ctas), dim3(kThreads), 0, ctas, s, a);
+    const int n_sm = device_sm_count();
+    cudaError_t e;
+    if (rows >= kManyRows * n_sm) {
+        e = launch_pdl(k_logprobs<kManyThreads, false>, dim3(rows), dim3(kManyThreads), 0, s, a);
+    } else {
+        // CTAs per row: as many as the device has room for at once (two an SM), each with a segment per warp at least
+        const int room = 2 * n_sm / std::min(rows, 2 * n_sm);
+        const int useful = ((vocab + kSeg - 1) / kSeg + kFewThreads / 32 - 1) / (kFewThreads / 32);
+        int ctas = 1;
+        while (2 * ctas <= std::min({room, useful, kMaxCluster})) ctas *= 2;
+        e = ctas == 1 ? launch_pdl(k_logprobs<kFewThreads, false>, dim3(rows), dim3(kFewThreads), 0, s, a)
+                      : launch_pdl_cluster(k_logprobs<kFewThreads, true>, dim3(rows * ctas), dim3(kFewThreads), 0, ctas, s, a);
+    }
     return e == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
 }

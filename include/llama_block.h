@@ -346,9 +346,9 @@ int llama_sample(const float* logits, int batch, int vocab, float temperature, i
  * NULL, n_top 0 (top_ids and top_logprobs are then not used).  Logits of -inf have
  * probability 0; a row of them alone has log probabilities of -inf, entropy 0 and the lowest
  * tokens on top.  A row with a NaN or +inf gets NaN log probabilities and entropy, and tokens
- * of its own vocabulary as alternatives.  Sums are held in fp32 per thread and in fp64 across
- * threads; exponentials and logarithms are fp32 ones except the last.  0 <= n_top <= 32, n_top
- * <= vocab <= 2^20. */
+ * of its own vocabulary as alternatives.  Everything is held in fp32, the sums in a
+ * tree over threads and without the largest term, so that small probabilities beside a large one keep
+ * their digits.  0 <= n_top <= 32, n_top <= vocab <= 2^20. */
 int llama_token_logprobs(const float* logits, int rows, int vocab, const int32_t* tokens, int n_top, float* logprobs,
                          float* entropy, int32_t* top_ids, float* top_logprobs, int32_t* err_dev, void* stream);
 
