@@ -6,8 +6,10 @@
 // all without cancellation: the terms of t are <= 0, and leaving the 1 out of the sums keeps small d.
 //
 // One pass over the logits.  A row is cut into segments of kSeg logits; a warp takes a segment at a time, all its
-// loads issued ahead, and keeps per lane the running maximum, d and t relative to it (the maximum's own term left out),
-// and per segment the maximum.  The lanes' triples are joined in a tree, in fp32 (in fp64 the joins took 40 us a row).
+// loads issued ahead, and keeps its running maximum, the lanes' parts of d and t relative to it (the maximum's own term
+// left out), and the maximum of each segment.  (A maximum per lane moves in most segments for some lane of the warp, the warp's
+// a few times a row: 23 instructions a logit against 9.)  The warps' triples are joined in a tree, in fp32 (in fp64 that
+// took 40 us a row).
 // The n largest logits lie in the n segments with
 // the largest maxima (equal maxima: the first segments): a segment outside has n segments whose best is better than all
 // it has.  So the alternatives come from n segments read a second time, from L2.
@@ -17,6 +19,7 @@
 // finishes its row while the others read, and no round of large CTAs ends half empty (924 rows of 128256 logits: 137 us
 // with 16 warps a row).
 #include <algorithm>
+#include <climits>
 #include <cmath>
 
 #include "internal.h"
@@ -95,6 +98,11 @@ __device__ __forceinline__ Sums join_warp(Sums s) {
     }
     return s;
 }
+__device__ __forceinline__ float add_warp(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
 
 // Shared memory of a CTA; the first CTA's is written by all of its cluster.
 struct Shared {
@@ -139,7 +147,7 @@ __device__ __forceinline__ void load_segment(const float* row, int head, int voc
 }
 
 template <int kThreads, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logprobs(const LogprobArgs a) {
+__global__ void __launch_bounds__(kThreads, kThreads == kManyThreads ? 7 : 2) k_logprobs(const LogprobArgs a) {
     constexpr int kWarps = kThreads / 32;
     __shared__ Shared sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.vocab;
@@ -160,47 +168,51 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logprobs(const Lo
     const int n_segs = (head + V + kSeg - 1) / kSeg;
     // ---------------------------------------------------------------- the pass: warp x of the row takes segments x, x + n, ...
     const int me = rank * kWarps + warp, all = ctas * kWarps;
-    Sums s{-INFINITY, 0.f, 0.f};
+    const unsigned none = order_bits(-INFINITY);
+    unsigned top = none;             // the warp's maximum so far
+    float m = -INFINITY, d = 0.f, t = 0.f;   // d, t: this lane's part
     auto take = [&](int seg, float (&z)[4 * kVec]) {
         float mx = z[0];
 #pragma unroll
         for (int i = 1; i < 4 * kVec; ++i) mx = fmaxf(mx, z[i]);
-        if (a.n_top > 0) {
-            const unsigned best = __reduce_max_sync(0xffffffffu, order_bits(mx));
-            if (lane == 0) {
-                if (CLUSTER) st_remote(remote(&sh.seg_max[seg], 0), best);
-                else sh.seg_max[seg] = best;
+        const unsigned bits = order_bits(mx), best = __reduce_max_sync(0xffffffffu, bits);
+        if (a.n_top > 0 && lane == 0) {
+            if (CLUSTER) st_remote(remote(&sh.seg_max[seg], 0), best);
+            else sh.seg_max[seg] = best;
+        }
+        if (best > top) {   // the sums move to the new maximum, whose first place is left out of them
+            const float mn = from_bits(best), x = fmaxf(m - mn, kFar), w = top == none ? 0.f : exp_neg(x);
+            const float own = lane == 0 ? 1.f + d : d;   // lane 0 takes the old maximum's term in
+            t = w * __fmaf_rn(x, own, t);
+            d = w * own;
+            m = mn;
+            top = best;
+            if (lane == __ffs(__ballot_sync(0xffffffffu, bits == best)) - 1) {
+                bool out = false;
+#pragma unroll
+                for (int i = 0; i < 4 * kVec; ++i)
+                    if (!out && z[i] == mn) {
+                        out = true;
+                        z[i] = -INFINITY;
+                    }
             }
+            if (mn == INFINITY) d = NAN;
         }
-        if (!(mx <= s.m)) {   // a new maximum: the sums move to it, its first place is left out of them
-            const float x = fmaxf(s.m - mx, kFar), w = s.m == -INFINITY ? 0.f : exp_neg(x), one = 1.f + s.d;
-            s.t = w * __fmaf_rn(x, one, s.t);
-            s.d = w * one;
-            s.m = mx;
-            bool own = false;
+        if (top == none) {   // nothing above -inf so far; a NaN among it stays
 #pragma unroll
             for (int i = 0; i < 4 * kVec; ++i)
-                if (!own && z[i] == mx) {
-                    own = true;
-                    z[i] = -INFINITY;
-                }
-            if (mx == INFINITY) s.d = NAN;
-        }
-        if (s.m == -INFINITY) {   // nothing above -inf so far; a NaN among it stays
-#pragma unroll
-            for (int i = 0; i < 4 * kVec; ++i)
-                if (z[i] != z[i]) s.d = NAN;
+                if (z[i] != z[i]) d = NAN;
             return;
         }
         float d4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 4 * kVec; ++i) {
-            const float x = max_nan(z[i] - s.m, kFar), e = exp_neg(x);
+            const float x = max_nan(z[i] - m, kFar), e = exp_neg(x);
             d4[i & 3] += e;
             t4[i & 3] = __fmaf_rn(e, x, t4[i & 3]);
         }
-        s.d += (d4[0] + d4[1]) + (d4[2] + d4[3]);
-        s.t += (t4[0] + t4[1]) + (t4[2] + t4[3]);
+        d += (d4[0] + d4[1]) + (d4[2] + d4[3]);
+        t += (t4[0] + t4[1]) + (t4[2] + t4[3]);
     };
     // a segment's loads go out before the one in front of it is taken
     float z0[4 * kVec], z1[4 * kVec];
@@ -215,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logprobs(const Lo
         take(seg, z1);
         seg += all;
     }
-    s = join_warp(s);
+    const Sums s{m, add_warp(d), add_warp(t)};
     if (lane == 0) {
         Sums* to = &sh.part[me];
         if (CLUSTER) {
@@ -248,16 +260,50 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_logprobs(const Lo
     if (a.n_top == 0) return;
     const int n = a.n_top, want = min(n, n_segs);
     if (tid == 0) sh.n_cand = 0;
-    // the best `want` segments: a segment's rank is the number of better ones
-    for (int g = tid; g < n_segs; g += kThreads) {
-        const unsigned b = sh.seg_max[g];
-        int better = 0;
-        for (int x = 0; x < n_segs; ++x) {
-            const unsigned o = sh.seg_max[x];
-            better += o > b || (o == b && x < g);
+    // the best `want` segments
+    if constexpr (kThreads == kManyThreads) {
+        // one warp, a segment a round (the other CTAs of the SM have the schedulers): lane x holds the best of segments x,
+        // x + 32, ... that are left, equal ones by increasing segment
+        if (warp == 1) {
+            unsigned b = 0;
+            int at = INT_MAX;
+            auto look = [&] {
+                b = 0;
+                for (int g = lane; g < n_segs; g += 32) {
+                    const unsigned o = sh.seg_max[g];
+                    if (o > b) {
+                        b = o;
+                        at = g;
+                    }
+                }
+            };
+            look();
+            for (int k = 0; k < want; ++k) {
+                const unsigned best = __reduce_max_sync(0xffffffffu, b);
+                const int seg = __reduce_min_sync(0xffffffffu, b == best ? at : INT_MAX);
+                if (lane == 0) {
+                    sh.segs[k] = seg;
+                    sh.least = best;
+                }
+                if (k + 1 < want && (seg & 31) == lane) {
+                    sh.seg_max[seg] = 0;   // below every logit's bits
+                    look();
+                }
+                __syncwarp();
+            }
         }
-        if (better < want) sh.segs[better] = g;
-        if (better == want - 1) sh.least = b;
+    } else {
+        // all threads: a segment's rank is the number of better ones
+        for (int g = tid; g < n_segs; g += kThreads) {
+            const unsigned b = sh.seg_max[g];
+            int better = 0;
+            for (int x = 0; x < n_segs; ++x) {
+                const unsigned o = sh.seg_max[x];
+                better += o > b || (o == b && x < g);
+            }
+            if (better < want) sh.segs[better] = g;
+            if (better == want - 1) sh.least = b;
+        }
     }
     __syncthreads();
     // their logits that may be among the n best: none below the least of the n segments' maxima (all, with fewer segments)
