@@ -1,7 +1,8 @@
 // llama_paged_chunk_attention: a chunk of new tokens per sequence over a paged KV cache.
 //
 // "Llama 3.1 70B", Grouped-Query Attention, with the rows found through a block table: token t of
-// sequence b attends positions 0 .. start[b] + t.
+// sequence b attends positions 0 .. start[b] + t.  bf16 runs on the tensor cores (attn_chunk_tc.cu), fp32 on the CUDA
+// cores (attn_chunk_f32.cu); both deal out the same tiles and chunks (attn_chunk.cuh).
 #include <algorithm>
 #include <cmath>
 
@@ -10,64 +11,6 @@
 
 namespace llama {
 namespace {
-
-__device__ __forceinline__ float to_f(bf16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ void from_f(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void from_f(float* p, float v) { *p = v; }
-
-// New tokens of sequence b: 0 (recorded) where its words are out of range.
-__device__ __forceinline__ int chunk_count(const ChunkArgs& a, int b, int& start) {
-    start = a.start[b];
-    const int count = a.count[b];
-    if (start >= 0 && count >= 0 && count <= a.tokens && (long long)start + count <= a.max_pos) return count;
-    record_error(a.err, LLAMA_ERR_POS_RANGE);
-    return 0;
-}
-
-// A warp per query row, its lanes sharing the row's columns, one key after another.
-template <typename T, int DH>
-__global__ void __launch_bounds__(256) k_attn_chunk_rows(const ChunkArgs a) {
-    constexpr int DPL = DH / 32;
-    ptx::griddep_wait();
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
-    int start;
-    const int count = chunk_count(a, b, start);
-    if (t >= count) return;
-    const int g = h / (a.n_heads / a.n_kv_heads);
-    const size_t row = ((size_t)b * a.tokens + t) * a.n_heads + h;
-    float q[DPL], o[DPL], m = -INFINITY, l = 0.f;
-    for (int e = 0; e < DPL; ++e) {
-        q[e] = to_f(static_cast<const T*>(a.q)[row * DH + lane * DPL + e]);
-        o[e] = 0.f;
-    }
-    const int shift = a.pages.shift;
-    size_t base = 0;
-    for (int j = 0; j <= start + t; ++j) {
-        if ((j & ((1 << shift) - 1)) == 0)
-            base = (((size_t)max(page_of(a.pages, b, j >> shift, a.err), 0) * a.n_kv_heads + g) << shift) * DH;
-        const size_t at = base + (size_t)(j & ((1 << shift) - 1)) * DH + lane * DPL;
-        float s = 0.f;
-        for (int e = 0; e < DPL; ++e) s = fmaf(q[e], to_f(static_cast<const T*>(a.kc)[at + e]), s);
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale_log2;
-        const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-        const float c = exp2f(m - ref), p = exp2f(s - ref);
-        l = fmaf(l, c, p);
-        for (int e = 0; e < DPL; ++e) o[e] = fmaf(o[e], c, p * to_f(static_cast<const T*>(a.vc)[at + e]));
-        m = mn;
-    }
-    for (int e = 0; e < DPL; ++e) from_f(static_cast<T*>(a.o) + row * DH + lane * DPL + e, o[e] / l);
-}
-
-template <typename T, int DH>
-cudaError_t launch_rows(const ChunkArgs& a, cudaStream_t s) {
-    const long long ctas = ((long long)a.tokens * a.n_heads + 7) / 8;
-    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    return launch_pdl(k_attn_chunk_rows<T, DH>, dim3((unsigned)ctas, a.batch), dim3(256), 0, s, a);
-}
 
 size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }
 
@@ -125,10 +68,6 @@ extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens,
     a.part_ml = (float2*)(a.partial + (size_t)kChunkMaxCtas * 512 * head_dim);
     a.cuts = (int4*)((uint8_t*)ws + align16((size_t)kChunkMaxCtas * 512 * (head_dim + 2) * sizeof(float)));
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
-    if (dtype == LLAMA_BF16) e = launch_chunk_tc(a, head_dim, s);
-    else if (head_dim == 32) e = launch_rows<float, 32>(a, s);
-    else if (head_dim == 64) e = launch_rows<float, 64>(a, s);
-    else e = launch_rows<float, 128>(a, s);
+    const cudaError_t e = dtype == LLAMA_BF16 ? launch_chunk_tc(a, head_dim, s) : launch_chunk_f32(a, head_dim, s);
     return e == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
 }

@@ -32,24 +32,26 @@ struct ChunkArgs {
     PageTable pages;
     float scale_log2;
     int tq;              // tokens per tile
-    float* partial;      // [2 CTAs][256 / rows of a part][head_dim / 4][rows of a part] float4
-    float2* part_ml;     // [2 CTAs][256]
+    int join_keys;       // work (keys) per CTA that the partials and their joining cost
+    int min_stretch;     // the least work of a CTA (keys) for which tiles are split
+    float* partial;      // [2 CTAs][halves of a tile][head_dim / 4][rows of a half] float4
+    float2* part_ml;     // [2 CTAs][halves][rows]
     int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it
     int* err;
 };
-cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s);
+cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s);    // bf16
+cudaError_t launch_chunk_f32(const ChunkArgs& a, int head_dim, cudaStream_t s);
 
 // Work of a tile in keys, beside the keys themselves: filling and draining the pipeline, q and o.
 constexpr int kTileKeys = 128;
 // The least chunks of a piece: what joining costs.
 constexpr int kMinPiece = 2;
-// The least work of a CTA (keys) for which tiles are split.
-constexpr int kMinStretch = 512;
+// Tiles of fewer positions have fewer chunks than two pieces and are never split (the join costs 3 us without any).
+constexpr int kNeverSplit = (2 * kMinPiece - 1) * kAttnChunk + 1;
 // Tiles per CTA from which on they are dealt out whole ...
 constexpr int kRounds = 4;
-// ... and fewer are too where the last round's idle CTAs cost less than this work per CTA: what the partials and their
-// joining cost (2048 tokens of 32 / 8 heads, 256 tiles: split 65 us, whole 47).
-constexpr int kJoinKeys = 768;
+// ... and fewer are too where the last round's idle CTAs cost less than join_keys per CTA (2048 tokens of 32 / 8 heads,
+// 256 tiles: split 65 us, whole 40).
 
 // The sequences of a launch (shared memory).
 struct ChunkSeqs {
@@ -148,9 +150,9 @@ struct ChunkWalk {
         const long long tiles = (long long)s.tiles[batch] * n_kv;
         rounds = tiles >= (long long)kRounds * n_ctas;
         if (!rounds && tiles > 0)
-            rounds = quotient(tiles + n_ctas - 1, n_ctas) * quotient(total, tiles) <= quotient(total, n_ctas) + kJoinKeys;
+            rounds = quotient(tiles + n_ctas - 1, n_ctas) * quotient(total, tiles) <= quotient(total, n_ctas) + a.join_keys;
         if (rounds) return;
-        const int n = (int)min((long long)n_ctas, max(tiles, total / kMinStretch));
+        const int n = (int)min((long long)n_ctas, max(tiles, quotient(total, a.min_stretch)));
         if (cta >= n || total == 0) return;
         const long long each = quotient(total, n);
         w0 = each * cta;
@@ -241,5 +243,124 @@ struct ChunkWalk {
         return make_int4(b, g, y, c < n ? c : 0);
     }
 };
+
+namespace {
+
+// Joins the pieces of the split tiles, in ascending order: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M the
+// largest m_p.  Every CTA reads all cuts and lists the split tiles; an item is one half of a tile and kJoinCols columns,
+// thread = row
+// (rows of 64: two column groups).  The loads of several pieces go out together.
+constexpr int kJoinCols = 8, kJoinBatch = 6;
+constexpr int kJoinThreads = 128;
+
+__device__ __forceinline__ void store_joined(bf16* dst, const float (&o)[kJoinCols], float inv) {
+    uint32_t packed[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[2 * q] * inv, o[2 * q + 1] * inv);
+        packed[q] = *reinterpret_cast<const uint32_t*>(&v2);
+    }
+    *reinterpret_cast<uint4*>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+}
+__device__ __forceinline__ void store_joined(float* dst, const float (&o)[kJoinCols], float inv) {
+#pragma unroll
+    for (int q = 0; q < kJoinCols; q += 4)
+        *reinterpret_cast<float4*>(dst + q) = make_float4(o[q] * inv, o[q + 1] * inv, o[q + 2] * inv, o[q + 3] * inv);
+}
+
+// HALVES of ROWS rows each.
+template <typename T, int DH, int HALVES, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArgs a, int n_ctas) {
+    __shared__ int4 s_cut[kChunkMaxCtas];
+    __shared__ int s_first[kChunkMaxCtas];
+    __shared__ unsigned s_word[8];   // bit i: a split tile's list begins with CTA i
+    static_assert(kChunkMaxCtas <= 2 * kJoinThreads && kJoinThreads == 128, "two CTAs a thread, words of 32");
+    ptx::griddep_wait();
+    for (int i = threadIdx.x; i < n_ctas; i += kJoinThreads) s_cut[i] = __ldcg(a.cuts + i);
+    __syncthreads();
+    // CTA j begins inside the tile that CTA i begins inside of
+    auto same = [&](int i, int j) {
+        return s_cut[j].w > 0 && s_cut[j].x == s_cut[i].x && s_cut[j].y == s_cut[i].y && s_cut[j].z == s_cut[i].z;
+    };
+    bool first[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int i = x * kJoinThreads + threadIdx.x;
+        first[x] = i > 0 && i < n_ctas && s_cut[i].w > 0 && !same(i, i - 1);
+        const unsigned word = __ballot_sync(0xffffffffu, first[x]);
+        if ((threadIdx.x & 31) == 0) s_word[i >> 5] = word;
+    }
+    __syncthreads();
+    int n_split = 0;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const int i = x * kJoinThreads + threadIdx.x;
+        int at = __popc(s_word[i >> 5] & ((1u << (i & 31)) - 1));
+        for (int w = 0; w < i >> 5; ++w) at += __popc(s_word[w]);
+        if (first[x]) s_first[at] = i;
+    }
+#pragma unroll
+    for (int w = 0; w < 8; ++w) n_split += __popc(s_word[w]);
+    __syncthreads();
+    constexpr int kCols = DH / kJoinCols, kSets = kJoinThreads / ROWS;   // column groups; of an item
+    const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq / HALVES, row = threadIdx.x % ROWS, t_local = row / n_rep;
+    const int items = n_split * HALVES * (kCols / kSets);
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int cols = item % (kCols / kSets) * kSets + threadIdx.x / ROWS, x = item / (kCols / kSets), half = x % HALVES;
+        const int i = s_first[x / HALVES];
+        const int4 cut = s_cut[i];
+        const int t = cut.z * a.tq + half * tqh + t_local;
+        if (t_local >= tqh || t >= a.count[cut.x]) continue;
+        int end = i + 1;   // CTAs that begin in the tile: i .. end - 1
+        while (end < n_ctas && same(i, end)) ++end;
+        // piece k of end - i + 1: CTA i - 1's last, then the first ones of CTAs i, i + 1, ...; a piece is empty where the
+        // next begins at the same chunk
+        auto slot_of = [&](int k) { return k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1); };
+        auto ml_of = [&](int k) {
+            const int j = i + k - 1;
+            if (k > 0 && j + 1 < end && s_cut[j + 1].w == s_cut[j].w) return make_float2(-INFINITY, 0.f);
+            return __ldcg(a.part_ml + (HALVES * slot_of(k) + half) * ROWS + row);
+        };
+        const int n = end - i + 1;
+        float M = -INFINITY, L = 0.f;
+        float o[kJoinCols];
+#pragma unroll
+        for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
+        for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
+            float2 ml[kJoinBatch];
+            float4 v[kJoinBatch][kJoinCols / 4];
+#pragma unroll
+            for (int x = 0; x < kJoinBatch; ++x) {
+                if (k0 + x >= n) break;
+                ml[x] = ml_of(k0 + x);
+                const float4* part =
+                    reinterpret_cast<const float4*>(a.partial + (size_t)(HALVES * slot_of(k0 + x) + half) * (ROWS * DH)) + row;
+#pragma unroll
+                for (int q = 0; q < kJoinCols / 4; ++q) v[x][q] = __ldcg(part + (cols * (kJoinCols / 4) + q) * ROWS);
+            }
+#pragma unroll
+            for (int x = 0; x < kJoinBatch; ++x) {
+                if (k0 + x >= n) break;
+                if (ml[x].x == -INFINITY && ml[x].y == 0.f) continue;   // nothing (or an empty piece: its part is not written)
+                const float Mn = fmaxf(M, ml[x].x);
+                const float c = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml[x].x - Mn);
+                M = Mn;
+                L = fmaf(L, c, ml[x].y * w);
+#pragma unroll
+                for (int q = 0; q < kJoinCols / 4; ++q) {
+                    o[4 * q] = fmaf(o[4 * q], c, v[x][q].x * w);
+                    o[4 * q + 1] = fmaf(o[4 * q + 1], c, v[x][q].y * w);
+                    o[4 * q + 2] = fmaf(o[4 * q + 2], c, v[x][q].z * w);
+                    o[4 * q + 3] = fmaf(o[4 * q + 3], c, v[x][q].w * w);
+                }
+            }
+        }
+        T* dst = static_cast<T*>(a.o) + ((size_t)cut.x * a.tokens + t) * a.n_heads * DH +
+                 (size_t)(cut.y * n_rep + row - t_local * n_rep) * DH + cols * kJoinCols;
+        store_joined(dst, o, 1.f / L);
+    }
+}
+
+}  // namespace
 
 }  // namespace llama

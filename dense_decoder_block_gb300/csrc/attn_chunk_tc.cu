@@ -607,109 +607,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the pieces of the split tiles, in ascending order: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M the
-// largest m_p.  Every CTA reads all cuts and lists the split tiles; an item is one half of a tile and kJoinCols columns,
-// thread = row.  The loads of several pieces go out together.
-constexpr int kJoinCols = 8, kJoinBatch = 6;
-constexpr int kJoinThreads = 128;
-
-__global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArgs a, int n_ctas) {
-    __shared__ int4 s_cut[kChunkMaxCtas];
-    __shared__ int s_first[kChunkMaxCtas];
-    __shared__ unsigned s_word[8];   // bit i: a split tile's list begins with CTA i
-    static_assert(kChunkMaxCtas <= 2 * kJoinThreads && kJoinThreads == 128, "two CTAs a thread, words of 32");
-    ptx::griddep_wait();
-    for (int i = threadIdx.x; i < n_ctas; i += kJoinThreads) s_cut[i] = __ldcg(a.cuts + i);
-    __syncthreads();
-    // CTA j begins inside the tile that CTA i begins inside of
-    auto same = [&](int i, int j) {
-        return s_cut[j].w > 0 && s_cut[j].x == s_cut[i].x && s_cut[j].y == s_cut[i].y && s_cut[j].z == s_cut[i].z;
-    };
-    bool first[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int i = x * kJoinThreads + threadIdx.x;
-        first[x] = i > 0 && i < n_ctas && s_cut[i].w > 0 && !same(i, i - 1);
-        const unsigned word = __ballot_sync(0xffffffffu, first[x]);
-        if ((threadIdx.x & 31) == 0) s_word[i >> 5] = word;
-    }
-    __syncthreads();
-    int n_split = 0;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int i = x * kJoinThreads + threadIdx.x;
-        int at = __popc(s_word[i >> 5] & ((1u << (i & 31)) - 1));
-        for (int w = 0; w < i >> 5; ++w) at += __popc(s_word[w]);
-        if (first[x]) s_first[at] = i;
-    }
-#pragma unroll
-    for (int w = 0; w < 8; ++w) n_split += __popc(s_word[w]);
-    __syncthreads();
-    const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq >> 1, row = threadIdx.x, t_local = row / n_rep;
-    const int items = n_split * 2 * (128 / kJoinCols);
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int cols = item % (128 / kJoinCols), half = item / (128 / kJoinCols) % 2, i = s_first[item / (2 * (128 / kJoinCols))];
-        const int4 cut = s_cut[i];
-        const int t = cut.z * a.tq + half * tqh + t_local;
-        if (t_local >= tqh || t >= a.count[cut.x]) continue;
-        int end = i + 1;   // CTAs that begin in the tile: i .. end - 1
-        while (end < n_ctas && same(i, end)) ++end;
-        // piece k of end - i + 1: CTA i - 1's last, then the first ones of CTAs i, i + 1, ...; a piece is empty where the
-        // next begins at the same chunk
-        auto slot_of = [&](int k) { return k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1); };
-        auto ml_of = [&](int k) {
-            const int j = i + k - 1;
-            if (k > 0 && j + 1 < end && s_cut[j + 1].w == s_cut[j].w) return make_float2(-INFINITY, 0.f);
-            return __ldcg(a.part_ml + (2 * slot_of(k) + half) * 128 + row);
-        };
-        const int n = end - i + 1;
-        float M = -INFINITY, L = 0.f;
-        float o[kJoinCols];
-#pragma unroll
-        for (int e = 0; e < kJoinCols; ++e) o[e] = 0.f;
-        for (int k0 = 0; k0 < n; k0 += kJoinBatch) {
-            float2 ml[kJoinBatch];
-            float4 v[kJoinBatch][kJoinCols / 4];
-#pragma unroll
-            for (int x = 0; x < kJoinBatch; ++x) {
-                if (k0 + x >= n) break;
-                ml[x] = ml_of(k0 + x);
-                const float4* part =
-                    reinterpret_cast<const float4*>(a.partial + (size_t)(2 * slot_of(k0 + x) + half) * (128 * 128)) + row;
-#pragma unroll
-                for (int q = 0; q < kJoinCols / 4; ++q) v[x][q] = __ldcg(part + (cols * (kJoinCols / 4) + q) * 128);
-            }
-#pragma unroll
-            for (int x = 0; x < kJoinBatch; ++x) {
-                if (k0 + x >= n) break;
-                if (ml[x].x == -INFINITY && ml[x].y == 0.f) continue;   // nothing (or an empty piece: its part is not written)
-                const float Mn = fmaxf(M, ml[x].x);
-                const float c = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml[x].x - Mn);
-                M = Mn;
-                L = fmaf(L, c, ml[x].y * w);
-#pragma unroll
-                for (int q = 0; q < kJoinCols / 4; ++q) {
-                    o[4 * q] = fmaf(o[4 * q], c, v[x][q].x * w);
-                    o[4 * q + 1] = fmaf(o[4 * q + 1], c, v[x][q].y * w);
-                    o[4 * q + 2] = fmaf(o[4 * q + 2], c, v[x][q].z * w);
-                    o[4 * q + 3] = fmaf(o[4 * q + 3], c, v[x][q].w * w);
-                }
-            }
-        }
-        bf16* dst = static_cast<bf16*>(a.o) + ((size_t)cut.x * a.tokens + t) * a.n_heads * 128 +
-                    (size_t)(cut.y * n_rep + row - t_local * n_rep) * 128 + cols * kJoinCols;
-        const float inv = 1.f / L;
-        uint32_t packed[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[2 * q] * inv, o[2 * q + 1] * inv);
-            packed[q] = *reinterpret_cast<const uint32_t*>(&v2);
-        }
-        static_assert(kJoinCols == 8, "one vector of bf16");
-        *reinterpret_cast<uint4*>(dst) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
@@ -739,14 +636,15 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
         k.count += b0;
         k.pages.table += (size_t)b0 * a.pages.stride;
         k.tq = 2 * (128 / n_rep);
+        k.join_keys = 768;
+        k.min_stretch = 512;
         if (!make_tmap_q3d(&mq, k.q, a.n_heads, k.batch * a.tokens, n_rep, k.tq / 2)) return cudaErrorInvalidValue;
         // persistent: one CTA per SM at most (work assigned on the device)
         const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kChunkMaxCtas);
         r = launch_pdl(k_attn_chunk, dim3(n_ctas), dim3(kThreads), SMEM_BYTES, s, mq, mk, mv, k);
         if (r != cudaSuccess) return r;
-        // tiles of fewer chunks than two pieces have are never split (the join costs 3 us without any)
-        if (n_ctas == 1 || a.max_pos < 2 * kMinPiece * kAttnChunk - (kAttnChunk - 1)) continue;
-        r = launch_pdl(k_attn_chunk_join, dim3(8 * n_ctas), dim3(kJoinThreads), 0, s, k, (int)n_ctas);
+        if (n_ctas == 1 || a.max_pos < kNeverSplit) continue;
+        r = launch_pdl(k_attn_chunk_join<bf16, 128, 2, 128>, dim3(8 * n_ctas), dim3(kJoinThreads), 0, s, k, (int)n_ctas);
         if (r != cudaSuccess) return r;
     }
     return cudaSuccess;
