@@ -7,6 +7,7 @@
 // As in paged.cu, kernels are launched with programmatic stream serialization, wait for the kernels
 // before them before they read anything, and let their dependents start only when they end.
 #include <algorithm>
+#include <climits>
 
 #include "internal.h"
 #include "paged.cuh"
@@ -77,18 +78,23 @@ __global__ void __launch_bounds__(kShareThreads) k_fork_jobs(const ForkArgs a) {
     const int tid = threadIdx.x;
     ptx::griddep_wait();
     const int n_free = __ldcg(a.pool);
-    for (int i = tid; i < kRowWords; i += kShareThreads) s_once[i] = s_twice[i] = s_source[i] = 0;
+    // the first forks, one a thread, are read once (each read is a round trip of the call)
+    int3 mine = make_int3(-1, -1, -1);
+    if (tid < a.n) mine = make_int3(__ldcg(a.src + tid), __ldcg(a.dst + tid), __ldcg(a.lens + tid));
+    auto words = [&](int i) { return i == tid ? mine : make_int3(__ldcg(a.src + i), __ldcg(a.dst + i), __ldcg(a.lens + i)); };
+    for (int i = tid; i < (a.rows + 31) >> 5; i += kShareThreads) s_once[i] = s_twice[i] = s_source[i] = 0;
     __syncthreads();
     for (int i = tid; i < a.n; i += kShareThreads) {
-        const int d = a.dst[i], s = a.src[i];
-        if (d >= 0 && d < a.rows && mark(s_once, d)) mark(s_twice, d);
-        if (s >= 0 && s < a.rows) mark(s_source, s);
+        const int3 w = words(i);
+        if (w.y >= 0 && w.y < a.rows && mark(s_once, w.y)) mark(s_twice, w.y);
+        if (w.x >= 0 && w.x < a.rows) mark(s_source, w.x);
     }
     __syncthreads();
     // a fork's full pages and unfilled rows; none of either when it is left out
     auto fork = [&](int i, bool record) -> int4 {
-        int4 j = make_int4(a.src[i], a.dst[i], 0, 0);
-        const int len = a.lens[i];
+        const int3 w = words(i);
+        int4 j = make_int4(w.x, w.y, 0, 0);
+        const int len = w.z;
         if (j.x < 0 || j.x >= a.rows || j.y < 0 || j.y >= a.rows || marked(s_twice, j.y) || marked(s_source, j.y)) {
             if (record) record_error(a.err, LLAMA_ERR_INVALID_ARG);
         } else if (len < 0 || len > (long long)a.stride << a.shift) {
@@ -128,16 +134,21 @@ __global__ void __launch_bounds__(kShareThreads) k_fork_jobs(const ForkArgs a) {
     }
 }
 
+// The copies of a fork -- K and V of every layer, heads, rows, vectors -- are one list, cut over gridDim.y - 1 CTAs; a
+// thread has kCopyVec loads under way.  (A CTA per layer and K or V read jobs and tables again and was mostly waiting:
+// 112 forks of 32 layers 37 us.)  The last CTA of a fork moves its table entries.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyVec = 4;
+constexpr int kCopyCtas = 16;   // per SM: from here on a CTA takes more
 
 __global__ void __launch_bounds__(kCopyThreads) k_fork_copy(const ForkArgs a, const __grid_constant__ ForkCaches c) {
     ptx::griddep_wait();
-    const int4 j = __ldcg(a.jobs + blockIdx.z);
+    const int4 j = __ldcg(a.jobs + blockIdx.x);
     const int* from = a.table + (size_t)j.x * a.stride;
     int* to = a.table + (size_t)j.y * a.stride;
-    if ((int)blockIdx.y == 2 * a.n_layers) {   // table entries and counts
-        for (int e = blockIdx.x * kCopyThreads + threadIdx.x; e < j.z; e += gridDim.x * kCopyThreads) {
+    const int parts = gridDim.y - 1;
+    if ((int)blockIdx.y == parts) {   // table entries and counts
+        for (int e = threadIdx.x; e < j.z; e += kCopyThreads) {
             const int id = __ldcg(from + e);
             to[e] = id;
             if (id >= 0 && id < a.n_pages) atomicAdd(a.refs + id, 1);
@@ -149,28 +160,29 @@ __global__ void __launch_bounds__(kCopyThreads) k_fork_copy(const ForkArgs a, co
     const int sp = __ldcg(from + j.z), dp = __ldcg(to + j.z);
     if (dp < 0 || dp >= a.n_pages) return;   // recorded when it was taken
     if (sp < 0 || sp >= a.n_pages) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) record_error(a.err, LLAMA_ERR_INVALID_ARG);
+        if (blockIdx.y == 0 && threadIdx.x == 0) record_error(a.err, LLAMA_ERR_INVALID_ARG);
         return;
     }
     const size_t page = (size_t)a.n_kv_heads << (a.shift + a.log_vec);
-    const uint4* src = c.kv[blockIdx.y] + sp * page;
-    uint4* dst = c.kv[blockIdx.y] + dp * page;
-    const int per_head = j.w << a.log_vec, n = a.n_kv_heads * per_head;
-    for (int x0 = blockIdx.x * kCopyThreads * kCopyVec + threadIdx.x; x0 < n; x0 += gridDim.x * kCopyThreads * kCopyVec) {
+    const unsigned per_head = j.w << a.log_vec, per_buffer = a.n_kv_heads * per_head;   // vectors: below 2^31
+    const long long n = (long long)per_buffer * 2 * a.n_layers, step = (long long)parts * kCopyThreads;
+    for (long long x0 = (long long)blockIdx.y * kCopyThreads + threadIdx.x; x0 < n; x0 += step * kCopyVec) {
         uint4 v[kCopyVec];
-        size_t at[kCopyVec];
+        uint4* dst[kCopyVec];
 #pragma unroll
         for (int i = 0; i < kCopyVec; ++i) {
-            const int x = x0 + i * kCopyThreads;
+            const long long x = x0 + i * step;
             if (x < n) {
-                const int h = x / per_head;
-                at[i] = ((size_t)h << (a.shift + a.log_vec)) + (x - h * per_head);
-                v[i] = __ldcg(src + at[i]);
+                const unsigned b = n >> 31 ? (unsigned)(x / per_buffer) : (unsigned)x / per_buffer;
+                const unsigned r = (unsigned)(x - (long long)b * per_buffer), h = r / per_head;
+                const size_t at = ((size_t)h << (a.shift + a.log_vec)) + (r - h * per_head);
+                v[i] = __ldcg(c.kv[b] + sp * page + at);
+                dst[i] = c.kv[b] + dp * page + at;
             }
         }
 #pragma unroll
         for (int i = 0; i < kCopyVec; ++i)
-            if (x0 + i * kCopyThreads < n) dst[at[i]] = v[i];
+            if (x0 + i * step < n) *dst[i] = v[i];
     }
 }
 
@@ -182,9 +194,9 @@ __global__ void __launch_bounds__(kCopyThreads) k_fork_copy(const ForkArgs a, co
 //
 // One cluster (one CTA where there are few entries), its warps with runs of entries of one length,
 // and barriers of the cluster between the steps: clear the pages' words, count and take the maximum
-// (atomics whose order does not matter), count what goes back per warp, write.  The
-// pages' words lie in the workspace and are cleared for the pages of the call alone, so the
-// cost does not grow with the cache.
+// (atomics whose order does not matter), count what goes back per warp, write.  A thread keeps its first
+// entries' pages and outcomes in registers.  The pages' words lie in the workspace and are cleared for the
+// pages of the call alone, so the cost does not grow with the cache.
 struct FreeArgs {
     const int* list;
     const int* lens;
@@ -196,14 +208,17 @@ struct FreeArgs {
     const int* table;
     int* drops;     // [n_pages]
     int* last;      // [n_pages]
-    int* prefix;    // [n + 1]
+    int* prefix;    // [n + 1]; calls of few rows keep it in shared memory
     int* counts;    // [kFreeCtas * 32]: pages that go back, per warp
     int* err;
 };
 constexpr int kFreeCtas = 8;
+constexpr int kFewRows = 2048;
+constexpr int kKept = 4;        // entries of a thread in registers
 
 __global__ void __launch_bounds__(kShareThreads) k_paged_free(const FreeArgs a) {
     __shared__ unsigned s_once[kRowWords], s_twice[kRowWords];
+    __shared__ int s_prefix[kFewRows + 1], s_row[kFewRows];
     __shared__ int s_scan[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ctas = gridDim.x;   // one cluster
@@ -218,11 +233,18 @@ __global__ void __launch_bounds__(kShareThreads) k_paged_free(const FreeArgs a) 
         }
         return;
     }
-    if (blockIdx.x == 0) {
-        for (int i = tid; i < kRowWords; i += kShareThreads) s_once[i] = s_twice[i] = 0;
+    auto sync = [&] {
+        if (ctas > 1) ptx::cluster_sync();
+        else __syncthreads();
+    };
+    // Where each row's entries begin: of few rows every CTA finds out by itself, of many the first does.
+    const bool few = a.n <= kFewRows;
+    if (few || blockIdx.x == 0) {
+        const int2 mine = tid < a.n ? make_int2(__ldcg(a.list + tid), __ldcg(a.lens + tid)) : make_int2(-1, -1);
+        for (int i = tid; i < (a.rows + 31) >> 5; i += kShareThreads) s_once[i] = s_twice[i] = 0;
         __syncthreads();
         for (int i = tid; i < a.n; i += kShareThreads) {
-            const int r = a.list[i];
+            const int r = i == tid ? mine.x : __ldcg(a.list + i);
             if (r >= 0 && r < a.rows && mark(s_once, r)) mark(s_twice, r);
         }
         __syncthreads();
@@ -231,46 +253,48 @@ __global__ void __launch_bounds__(kShareThreads) k_paged_free(const FreeArgs a) 
             const int i = i0 + tid;
             int pages = 0;
             if (i < a.n) {
-                const int r = a.list[i], len = a.lens[i];
-                if (r < 0 || r >= a.rows || marked(s_twice, r)) record_error(a.err, LLAMA_ERR_INVALID_ARG);
-                else if (len < 0 || len > (long long)a.stride << a.shift) record_error(a.err, LLAMA_ERR_POS_RANGE);
+                const int r = i0 == 0 ? mine.x : __ldcg(a.list + i), len = i0 == 0 ? mine.y : __ldcg(a.lens + i);
+                int bad = 0;
+                if (r < 0 || r >= a.rows || marked(s_twice, r)) bad = LLAMA_ERR_INVALID_ARG;
+                else if (len < 0 || len > (long long)a.stride << a.shift) bad = LLAMA_ERR_POS_RANGE;
                 else pages = (int)(((long long)len + (1 << a.shift) - 1) >> a.shift);
+                if (bad && blockIdx.x == 0) record_error(a.err, bad);
+                if (few) s_row[i] = r;
             }
             int here;
             const int before = block_prefix(pages, s_scan, here);
-            if (i < a.n) a.prefix[i] = run + before;
+            if (i < a.n) (few ? s_prefix : a.prefix)[i] = run + before;
             run += here;
         }
-        if (tid == 0) a.prefix[a.n] = run;
+        if (tid == 0) (few ? s_prefix : a.prefix)[a.n] = run;
     }
-    auto sync = [&] {
-        if (ctas > 1) ptx::cluster_sync();
-        else __syncthreads();
-    };
-    sync();
-    const int total = __ldcg(a.prefix + a.n);
+    if (few) __syncthreads();
+    else sync();
+    auto prefix = [&](int i) { return few ? s_prefix[i] : __ldcg(a.prefix + i); };
+    const int total = prefix(a.n);
     const int wid = blockIdx.x * 32 + warp, warps = ctas * 32;
     const int e0 = (int)((long long)total * wid / warps), e1 = (int)((long long)total * (wid + 1) / warps);
-    int row0 = 0;   // the last row whose entries start at or before e0
-    for (int hi = a.n - 1; row0 < hi;) {
-        const int mid = (row0 + hi + 1) >> 1;
-        if (__ldcg(a.prefix + mid) <= e0) row0 = mid;
-        else hi = mid - 1;
-    }
-    // f(entry, page) for this warp's entries, 32 at a time; page -1 where there is none
-    auto entries = [&](auto&& f) {
-        int row = row0, next = e0 < e1 ? __ldcg(a.prefix + row + 1) : 0;
-        for (int e = e0 + lane; e - lane < e1; e += 32) {
-            int id = -1;
-            if (e < e1) {
-                while (next <= e) next = __ldcg(a.prefix + ++row + 1);
-                id = __ldcg(a.table + (size_t)a.list[row] * a.stride + (e - __ldcg(a.prefix + row)));
-                if (id < 0 || id >= a.n_pages) id = -2;
-            }
-            f(e, id);
+    auto page_at = [&](int e) -> int {   // of entry e, -2 when it is no page
+        int lo = 0;   // the last row whose entries start at or before e
+        for (int hi = a.n - 1; lo < hi;) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix(mid) <= e) lo = mid;
+            else hi = mid - 1;
         }
+        const int id = __ldcg(a.table + (size_t)(few ? s_row[lo] : __ldcg(a.list + lo)) * a.stride + (e - prefix(lo)));
+        return id < 0 || id >= a.n_pages ? -2 : id;
     };
-    entries([&](int, int id) {
+    int page[kKept];   // -1: no entry
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) page[k] = e0 + 32 * k + lane < e1 ? page_at(e0 + 32 * k + lane) : -1;
+    // f(place among this thread's entries, entry, page) for this warp's entries, 32 at a time
+    auto entries = [&](auto&& f) {
+#pragma unroll
+        for (int k = 0; k < kKept; ++k)
+            if (e0 + 32 * k < e1) f(k, e0 + 32 * k + lane, page[k]);
+        for (int e = e0 + 32 * kKept + lane; e - lane < e1; e += 32) f(kKept, e, e < e1 ? page_at(e) : -1);
+    };
+    entries([&](int, int, int id) {
         if (id == -2) record_error(a.err, LLAMA_ERR_INVALID_ARG);
         if (id >= 0) {
             a.drops[id] = 0;
@@ -278,24 +302,26 @@ __global__ void __launch_bounds__(kShareThreads) k_paged_free(const FreeArgs a) 
         }
     });
     sync();
-    entries([&](int e, int id) {
+    entries([&](int, int e, int id) {
         if (id >= 0) {
             atomicAdd(a.drops + id, 1);
             atomicMax(a.last + id, e);
         }
     });
     sync();
-    // the entry that settles its page: how many holds are given up, how many there are
-    auto settles = [&](int e, int id, int& drops, int& holders) {
-        if (id < 0 || __ldcg(a.last + id) != e) return false;
-        drops = __ldcg(a.drops + id);
-        holders = max(__ldcg(a.refs + id), 0) + 1;
-        return true;
+    // Of the entry that settles its page: the holds left (below 0: given up more often than held); kOther: another does.
+    constexpr int kOther = INT_MAX;
+    auto settle = [&](int e, int id) -> int {
+        if (id < 0) return kOther;
+        const int last = __ldcg(a.last + id), drops = __ldcg(a.drops + id), refs = __ldcg(a.refs + id);
+        return last == e ? max(refs, 0) + 1 - drops : kOther;
     };
+    int left[kKept];
     int mine = 0;
-    entries([&](int e, int id) {
-        int d, h;
-        mine += __popc(__ballot_sync(0xffffffffu, settles(e, id, d, h) && d >= h));
+    entries([&](int k, int e, int id) {
+        const int x = settle(e, id);
+        if (k < kKept) left[k] = x;
+        mine += __popc(__ballot_sync(0xffffffffu, x <= 0));
     });
     if (lane == 0) a.counts[wid] = mine;
     sync();
@@ -314,14 +340,13 @@ __global__ void __launch_bounds__(kShareThreads) k_paged_free(const FreeArgs a) 
         a.pool_out[1] = 0;
     }
     if (!room) return;
-    entries([&](int e, int id) {
-        int d = 0, h = 0;
-        const bool s = settles(e, id, d, h);
-        const unsigned ones = __ballot_sync(0xffffffffu, s && d >= h);
-        if (s) {
-            if (d > h) record_error(a.err, LLAMA_ERR_INVALID_ARG);
-            a.refs[id] = d >= h ? 0 : h - 1 - d;
-            if (d >= h) a.free_pages[n_free + back - 1 - (before + __popc(ones & ((1u << lane) - 1)))] = id;
+    entries([&](int k, int e, int id) {
+        const int x = k < kKept ? left[k] : settle(e, id);
+        const unsigned ones = __ballot_sync(0xffffffffu, x <= 0);
+        if (x != kOther) {
+            if (x < 0) record_error(a.err, LLAMA_ERR_INVALID_ARG);
+            a.refs[id] = max(x - 1, 0);
+            if (x <= 0) a.free_pages[n_free + back - 1 - (before + __popc(ones & ((1u << lane) - 1)))] = id;
         }
         before += __popc(ones);
     });
@@ -378,9 +403,10 @@ extern "C" int llama_paged_fork(const int32_t* src, const int32_t* dst, const in
     cudaStream_t s = (cudaStream_t)stream;
     if (launch_pdl(k_fork_jobs, dim3(1), dim3(kShareThreads), 0, s, a) != cudaSuccess) return LLAMA_ERR_CUDA;
     if (n == 0) return LLAMA_OK;
-    const long long most = ((long long)n_kv_heads * (caches[0].page_size - 1)) << a.log_vec;   // vectors of one page
+    const long long most = (((long long)n_kv_heads * (caches[0].page_size - 1)) << a.log_vec) * 2 * n_layers;   // vectors of a fork
     const long long want = (most + kCopyThreads * kCopyVec - 1) / (kCopyThreads * kCopyVec);
-    const dim3 grid((unsigned)std::min<long long>(want, 64), 2 * n_layers + 1, n);
+    const long long room = std::max(1, kCopyCtas * device_sm_count() / n);
+    const dim3 grid(n, (unsigned)std::min(want, room) + 1);
     return launch_pdl(k_fork_copy, grid, dim3(kCopyThreads), 0, s, a, c) == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
 }
 
@@ -419,7 +445,7 @@ extern "C" int llama_paged_free(const int32_t* list, const int32_t* lens, int n,
     a.counts = a.prefix + n + 1;
     a.err = err_dev;
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = (long long)n * table_stride <= 8 * kShareThreads
+    const cudaError_t e = (long long)n * table_stride <= kShareThreads
                               ? launch_pdl(k_paged_free, dim3(1), dim3(kShareThreads), 0, s, a)
                               : launch_pdl_cluster(k_paged_free, dim3(kFreeCtas), dim3(kShareThreads), 0, kFreeCtas, s, a);
     return e == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
