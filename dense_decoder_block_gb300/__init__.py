@@ -37,6 +37,7 @@ __all__ = [
     "llama_paged_attention", "llama_paged_attention_workspace_bytes", "llama_block_decode_paged",
     "llama_beam_select", "llama_beam_select_workspace_bytes", "llama_beam_reorder",
     "llama_paged_chunk_attention", "llama_paged_chunk_attention_workspace_bytes",
+    "llama_block_prefill_paged", "llama_block_prefill_paged_workspace_bytes",
     "llama_paged_fork", "llama_paged_fork_workspace_bytes", "llama_paged_free", "llama_paged_free_workspace_bytes",
     "llama_token_logprobs",
 ]
@@ -174,6 +175,17 @@ def llama_block_decode_seqpos(h, x, batch, kv: llama_kv_cache, pos_seq, y, ws, w
 def llama_block_decode_paged(h, x, batch, kv: llama_paged_cache, table, pos_seq, y, ws, ws_bytes, stream=None) -> None:
     _check(h, lib().llama_block_decode_paged(h, _ptr(x), batch, C.byref(kv), _ptr(table), table.shape[1], _ptr(pos_seq),
                                              _ptr(y), _ptr(ws), ws_bytes, _stream(stream)), "llama_block_decode_paged")
+
+
+def llama_block_prefill_paged_workspace_bytes(h, batch: int, tokens: int) -> int:
+    return int(lib().llama_block_prefill_paged_workspace_bytes(h, batch, tokens))
+
+
+def llama_block_prefill_paged(h, x, batch, tokens, kv: llama_paged_cache, table, start, count, y, ws, ws_bytes,
+                              stream=None) -> None:
+    _check(h, lib().llama_block_prefill_paged(h, _ptr(x), batch, tokens, C.byref(kv), _ptr(table), table.shape[1], _ptr(start),
+                                              _ptr(count), _ptr(y), _ptr(ws), ws_bytes, _stream(stream)),
+           "llama_block_prefill_paged")
 
 
 def llama_block_set_stage_events(h, events) -> None:
@@ -644,6 +656,23 @@ class LlamaBlock:
         _table_arg(table, "table", x.shape[0], None)
         _arg(pos_seq, "pos_seq", torch.int32, x.shape[0])
         llama_block_decode_paged(self.h, x, x.shape[0], kv.c, table, pos_seq, y, ws, ws.numel(), stream)
+
+    def workspace_paged(self, batch: int, tokens: int, device=None) -> torch.Tensor:
+        n = llama_block_prefill_paged_workspace_bytes(self.h, batch, tokens)
+        return torch.empty(n, dtype=torch.uint8, device=device or self._keep["wq"].device)
+
+    def prefill_paged(self, x, kv: "PagedCache", table, start, count, y, ws, stream=None):
+        """count[b] new tokens of sequence b at positions start[b] on (int32 CUDA tensors), x, y [B, tokens, d]; their pages are
+        in row b of table (llama_paged_plan)."""
+        if kv.n_kv_heads != self.dims.n_kv_heads or kv.head_dim != self.dims.head_dim or \
+                kv.dtype != self._keep["wq"].dtype:
+            raise ValueError("the paged cache's heads or type are not the block's")
+        B, T = x.shape[0], x.shape[1]
+        _current(kv.device)
+        _table_arg(table, "table", B, None)
+        _arg(start, "start", torch.int32, B)
+        _arg(count, "count", torch.int32, B)
+        llama_block_prefill_paged(self.h, x, B, T, kv.c, table, start, count, y, ws, ws.numel(), stream)
 
     def poll_error(self, stream=None) -> int:
         return llama_block_poll_error(self.h, stream)

@@ -106,6 +106,10 @@ SIGNATURES = {
     "llama_paged_chunk_attention": (C.c_int, [C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int, C.c_int,
                                               C.POINTER(llama_paged_cache), C.c_void_p, C.c_int, C.c_void_p, C.c_void_p,
                                               C.c_int, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+    "llama_block_prefill_paged_workspace_bytes": (C.c_size_t, [C.c_void_p, C.c_int, C.c_int]),
+    "llama_block_prefill_paged": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.POINTER(llama_paged_cache),
+                                            C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t,
+                                            C.c_void_p]),
     "llama_paged_fork_workspace_bytes": (C.c_size_t, [C.c_int]),
     "llama_paged_fork": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p,
                                    C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.POINTER(llama_paged_cache), C.c_int,

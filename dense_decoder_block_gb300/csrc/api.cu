@@ -57,6 +57,7 @@ struct Ws {
     void* q_raw = nullptr;
     float* gemm_partial = nullptr;
     float* attn_partial = nullptr;
+    void* chunk = nullptr;   // paged prefill only (and k_raw, v_raw)
     size_t total = 0;
 };
 
@@ -109,7 +110,7 @@ GemmProblem problem_down(const llama_block_s* b, int M, const void* x) {
     return p;
 }
 
-Ws layout(const llama_block_s* b, int B, int T, uint8_t* base, bool decode) {
+Ws layout(const llama_block_s* b, int B, int T, uint8_t* base, bool decode, bool chunk = false) {
     const auto& d = b->dims;
     const size_t M = (size_t)B * T;
     const size_t es = d.dtype == LLAMA_BF16 ? 2 : 4;
@@ -143,6 +144,11 @@ Ws layout(const llama_block_s* b, int B, int T, uint8_t* base, bool decode) {
         w.attn_partial = (float*)take(attn_decode_partial_bytes(B, d.n_kv_heads, attn_chunk_slots(d), n_rep,
                                                                 d.head_dim));
     }
+    if (chunk) {   // k and v before they go to their pages, and the attention's partials
+        w.k_raw = take(M * kvd * es);
+        w.v_raw = take(M * kvd * es);
+        w.chunk = take(attn_chunk_workspace_bytes(d.head_dim));
+    }
     w.total = off;
     return w;
 }
@@ -158,22 +164,24 @@ int check_kv(llama_block b, const llama_kv_cache* kv, int batch, int last_pos) {
 }
 
 // The block's schedule, shared by prefill (T tokens at 0..T-1) and decode
-// (T = 1 at `pos`, or at *pos_dev).
+// (T = 1 at `pos`, or at *pos_dev); on pages: T = 1 at pos_seq[b], or count[b] tokens from start[b] on.
 int run_block(llama_block b, const void* x, int B, int T, const llama_kv_cache* kv, int start_pos,
               const int32_t* pos_dev, void* y, void* ws, size_t ws_bytes, void* stream_v, bool decode,
-              const int32_t* pos_seq = nullptr, const PageTable* pages = nullptr) {
+              const int32_t* pos_seq = nullptr, const PageTable* pages = nullptr, const int32_t* start = nullptr,
+              const int32_t* count = nullptr) {
     const auto& d = b->dims;
     cudaStream_t s = (cudaStream_t)stream_v;
     const int M = B * T;
     if (M == 0) return LLAMA_OK;
-    Ws w = layout(b, B, T, nullptr, decode);
+    const bool chunk = start != nullptr;   // paged prefill
+    Ws w = layout(b, B, T, nullptr, decode, chunk);
     if (!ws || ws_bytes < w.total)
         return fail(b, LLAMA_ERR_WORKSPACE, "workspace too small: need " + std::to_string(w.total) + " bytes");
     if (!aligned16(ws)) return fail(b, LLAMA_ERR_INVALID_ARG, "workspace not 16-byte aligned");
     int cur = -1;
     if (cudaGetDevice(&cur) != cudaSuccess) return fail(b, LLAMA_ERR_CUDA, "cudaGetDevice failed");
     if (cur != b->device) return fail(b, LLAMA_ERR_INVALID_ARG, "the handle's device is not the current device");
-    w = layout(b, B, T, (uint8_t*)ws, decode);
+    w = layout(b, B, T, (uint8_t*)ws, decode, chunk);
     // on pages (kv: n_pages "sequences" of page_size rows) a table row bounds the positions
     const int max_pos =
         pages ? (int)std::min<long long>(d.max_seq, (long long)pages->stride << pages->shift) : std::min(d.max_seq, kv->max_seq);
@@ -259,15 +267,31 @@ int run_block(llama_block b, const void* x, int B, int T, const llama_kv_cache* 
         // kernel rotates them in place: the per-column table loads of a fused RoPE
         // kept that projection's epilogue warps behind its MMAs.
         eq.rope_later = pick_gemm_path(pq, PATH_AUTO) == PATH_TOKEN_TILED && !gemm_tt_split(pq, PATH_AUTO);
+        if (chunk) {
+            // Positions and pages differ from sequence to sequence: k and v are left, unrotated, as the rows
+            // 0 .. T-1 of a cache in the workspace, whatever the schedule, and launch_rope_paged takes them on.
+            eq.kc = (bf16*)w.k_raw;
+            eq.vc = (bf16*)w.v_raw;
+            eq.kv_seq = eq.max_pos = T;
+            eq.pages = PageTable();
+            eq.rope_later = true;
+        }
         LLAMA_TRY(launch_gemm(pq, eq, PATH_AUTO, w.gemm_partial, s), "qkv");
-        if (eq.rope_later)
+        if (eq.rope_later && !chunk)
             LLAMA_TRY(launch_rope_inplace(w.q, kv->k, M, T, d.n_heads, d.n_kv_heads, kv->max_seq, start_pos, pos_dev,
                                           max_pos, b->cos_tab, b->sin_tab, b->err_dev, s),
                       "qkv_rope");
         if (gemm_needs_reduce(pq, PATH_AUTO)) LLAMA_TRY(reduce(pq, eq, EPI_QKV), "qkv_reduce");
+        if (chunk)
+            LLAMA_TRY(launch_rope_paged(w.q, w.k_raw, w.v_raw, B, T, d.n_heads, d.n_kv_heads, kv->k, kv->v, *pages, start,
+                                        count, max_pos, b->cos_tab, b->sin_tab, b->err_dev, s),
+                      "qkv_rope_paged");
         // 3. attention (tensor cores when the group size divides 128; one choice per handle)
         mark();
-        if (pages) {
+        if (chunk) {
+            LLAMA_TRY(launch_attention_chunk(at, start, count, w.chunk, s), "attention_chunk");
+            n_launch += attn_chunk_launches(at) - 1;
+        } else if (pages) {
             LLAMA_TRY(launch_attention_paged(at, s), "attention_paged");
             ++n_launch;   // and its combine
         } else if (attention_tc_supported(d.n_heads, d.n_kv_heads, d.head_dim)) {
@@ -614,6 +638,33 @@ extern "C" int llama_block_decode_paged(llama_block b, const void* x, int batch,
     pages.n_pages = kv->n_pages;
     pages.shift = page_shift(kv->page_size);
     return run_block(b, x, batch, 1, &flat, 0, nullptr, y, ws, ws_bytes, stream, true, pos_seq, &pages);
+}
+
+extern "C" size_t llama_block_prefill_paged_workspace_bytes(llama_block b, int batch, int tokens) {
+    if (!b || batch <= 0 || tokens <= 0 || b->dims.dtype != LLAMA_BF16) return 0;
+    return layout(b, batch, tokens, nullptr, false, true).total;
+}
+
+extern "C" int llama_block_prefill_paged(llama_block b, const void* x, int batch, int tokens, const llama_paged_cache* kv,
+                                         const int32_t* table, int table_stride, const int32_t* start,
+                                         const int32_t* count, void* y, void* ws, size_t ws_bytes, void* stream) {
+    if (!b) return LLAMA_ERR_INVALID_ARG;
+    if (batch < 0 || batch > 65535 || tokens < 0) return fail(b, LLAMA_ERR_INVALID_ARG, "batch or tokens out of range");
+    const auto& d = b->dims;
+    if (d.dtype != LLAMA_BF16 || (long long)batch * tokens > INT32_MAX / 2)
+        return fail(b, LLAMA_ERR_UNSUPPORTED_DIMS, "paged prefill takes bf16 blocks and fewer than 2^30 rows");
+    const int rc = paged_cache_check(kv, d.n_kv_heads, d.head_dim, d.dtype);
+    if (rc != LLAMA_OK) return fail(b, rc, "paged cache: null, misaligned or of an unsupported geometry");
+    if (batch == 0 || tokens == 0) return LLAMA_OK;
+    if (!x || !y || !table || !start || !count || table_stride <= 0 || !aligned16(x) || !aligned16(y))
+        return fail(b, LLAMA_ERR_INVALID_ARG, "x / y / table / start / count null or x / y not 16-byte aligned");
+    const llama_kv_cache flat{kv->k, kv->v, kv->n_pages, kv->page_size};
+    PageTable pages;
+    pages.table = table;
+    pages.stride = table_stride;
+    pages.n_pages = kv->n_pages;
+    pages.shift = page_shift(kv->page_size);
+    return run_block(b, x, batch, tokens, &flat, 0, nullptr, y, ws, ws_bytes, stream, false, nullptr, &pages, start, count);
 }
 
 extern "C" int llama_block_poll_error(llama_block b, void* stream) {

@@ -12,14 +12,44 @@
 namespace llama {
 namespace {
 
-size_t align16(size_t v) { return (v + 15) & ~(size_t)15; }
-
 bool heads_ok(int n_heads, int n_kv_heads, int head_dim) {
     return n_heads > 0 && n_kv_heads > 0 && n_heads <= 65535 && n_heads % n_kv_heads == 0 &&
            n_heads / n_kv_heads <= 64 && (head_dim == 32 || head_dim == 64 || head_dim == 128);
 }
 
+size_t partial_bytes(int head_dim) { return (size_t)kChunkMaxCtas * 512 * (head_dim + 2) * sizeof(float); }
+
 }  // namespace
+
+// two partials (m, l, o) of up to 256 rows for each CTA, and where the CTAs begin
+size_t attn_chunk_workspace_bytes(int head_dim) { return partial_bytes(head_dim) + kChunkMaxCtas * sizeof(int4); }
+
+int attn_chunk_launches(const AttnArgs& a) {
+    return (a.batch + kChunkSeqs - 1) / kChunkSeqs * (device_sm_count() == 1 || a.max_pos < kNeverSplit ? 1 : 2);
+}
+
+cudaError_t launch_attention_chunk(const AttnArgs& a, const int* start, const int* count, void* ws, cudaStream_t s) {
+    ChunkArgs k{};
+    k.q = a.q;
+    k.o = a.o;
+    k.kc = a.kc;
+    k.vc = a.vc;
+    k.batch = a.batch;
+    k.tokens = a.tokens;
+    k.n_heads = a.n_heads;
+    k.n_kv_heads = a.n_kv_heads;
+    k.max_pos = a.max_pos;
+    k.start = start;
+    k.count = count;
+    k.pages = a.pages;
+    k.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
+    k.partial = (float*)ws;
+    k.part_ml = (float2*)(k.partial + (size_t)kChunkMaxCtas * 512 * a.head_dim);
+    k.cuts = (int4*)((uint8_t*)ws + partial_bytes(a.head_dim));
+    k.err = a.err;
+    return a.dtype == LLAMA_BF16 ? launch_chunk_tc(k, a.head_dim, s) : launch_chunk_f32(k, a.head_dim, s);
+}
+
 }  // namespace llama
 
 using namespace llama;
@@ -27,8 +57,7 @@ using namespace llama;
 extern "C" size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads,
                                                               int head_dim, int max_len) {
     if (batch <= 0 || tokens <= 0 || max_len <= 0 || !heads_ok(n_heads, n_kv_heads, head_dim)) return 0;
-    // two partials (m, l, o) of up to 256 rows for each CTA, and where the CTAs begin
-    return align16((size_t)kChunkMaxCtas * 512 * (head_dim + 2) * sizeof(float)) + kChunkMaxCtas * sizeof(int4);
+    return attn_chunk_workspace_bytes(head_dim);
 }
 
 extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_heads, int n_kv_heads,
@@ -45,7 +74,7 @@ extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens,
     if (!ws || ws_bytes < llama_paged_chunk_attention_workspace_bytes(batch, tokens, n_heads, n_kv_heads, head_dim, max_len))
         return LLAMA_ERR_WORKSPACE;
     if ((uintptr_t)ws & 15) return LLAMA_ERR_INVALID_ARG;
-    ChunkArgs a{};
+    AttnArgs a;
     a.q = q;
     a.o = o;
     a.kc = kv->k;
@@ -54,20 +83,16 @@ extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens,
     a.tokens = tokens;
     a.n_heads = n_heads;
     a.n_kv_heads = n_kv_heads;
-    a.start = start;
-    a.count = count;
+    a.head_dim = head_dim;
     a.pages.table = table;
     a.pages.stride = table_stride;
     a.pages.n_pages = kv->n_pages;
     a.pages.shift = page_shift(kv->page_size);
+    // positions must fit max_len and the table row
     const long long room = (long long)table_stride * kv->page_size;
     a.max_pos = room < max_len ? (int)room : max_len;
-    a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)head_dim));
+    a.dtype = dtype;
     a.err = err_dev;
-    a.partial = (float*)ws;
-    a.part_ml = (float2*)(a.partial + (size_t)kChunkMaxCtas * 512 * head_dim);
-    a.cuts = (int4*)((uint8_t*)ws + align16((size_t)kChunkMaxCtas * 512 * (head_dim + 2) * sizeof(float)));
-    cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = dtype == LLAMA_BF16 ? launch_chunk_tc(a, head_dim, s) : launch_chunk_f32(a, head_dim, s);
+    const cudaError_t e = launch_attention_chunk(a, start, count, ws, (cudaStream_t)stream);
     return e == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
 }

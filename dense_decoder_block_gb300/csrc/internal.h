@@ -148,6 +148,11 @@ cudaError_t launch_attention_paged(const AttnArgs& a, cudaStream_t s);
 // Tensor cores (bf16, attention_tc_supported, at most 64 query heads per KV head), + combine.
 cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s);
+// Attention of chunks of new tokens over a paged cache (a.pages; a.tokens columns, sequence b's new tokens are
+// count[b] at positions start[b] on, below a.max_pos); ws: attn_chunk_workspace_bytes.
+size_t attn_chunk_workspace_bytes(int head_dim);
+int attn_chunk_launches(const AttnArgs& a);   // kernels of a call
+cudaError_t launch_attention_chunk(const AttnArgs& a, const int* start, const int* count, void* ws, cudaStream_t s);
 // LLAMA_OK, or why the pages of kv cannot be used with these heads.
 int paged_cache_check(const llama_paged_cache* kv, int n_kv_heads, int head_dim, int dtype);
 // LLAMA_OK, or why a cache cannot have such pages.
@@ -168,6 +173,13 @@ cudaError_t launch_attention_tc_decode(const AttnArgs& a, int chunks_per_cta, cu
 cudaError_t launch_rope_inplace(void* q, void* kc, int M, int T, int n_heads, int n_kv_heads, int kv_seq,
                                 int start_pos, const int* pos_dev, int max_pos, const float* cos_tab,
                                 const float* sin_tab, int* err, cudaStream_t s);
+
+// The same for chunks of new tokens on a paged cache: q in place, and k and v [batch, n_kv_heads, T, 128] as the QKV
+// projection leaves them to the pages, k rotated.  Token t of sequence b lies at position start[b] + t, t < count[b];
+// the others are left alone.
+cudaError_t launch_rope_paged(void* q, const void* k, const void* v, int batch, int T, int n_heads, int n_kv_heads,
+                              void* pk, void* pv, const PageTable& pages, const int* start, const int* count,
+                              int max_pos, const float* cos_tab, const float* sin_tab, int* err, cudaStream_t s);
 
 // fp32 SIMT block pieces
 cudaError_t launch_linear_f32(const float* x, const float* w, const float* w2, const float* resid, float* y, int M,

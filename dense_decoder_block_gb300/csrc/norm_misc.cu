@@ -222,6 +222,75 @@ __global__ void __launch_bounds__(256) k_rope_inplace(bf16* __restrict__ q, bf16
     TRACE(trace_cta(TR_ROPE, tr0, tr1);)
 }
 
+// RoPE of chunks of new tokens, their rows to pages (launch_rope_paged): as above, one thread per 8 elements of
+// kRopeRows rows of a token -- q rows in place, then k rows (rotated) and v rows (copied) into the pages.
+__global__ void __launch_bounds__(256) k_rope_paged(bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
+                                                    int M, int T, int n_heads, int n_kv_heads, bf16* __restrict__ pk,
+                                                    bf16* __restrict__ pv, const PageTable pages, const int* start,
+                                                    const int* count, int max_pos, const float* __restrict__ cos_tab,
+                                                    const float* __restrict__ sin_tab, int* err) {
+    // the attention behind it reads nothing before its own wait
+    if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n_rows = n_heads + 2 * n_kv_heads;                 // 128-wide rows per token
+    const int n_grp = (n_rows + kRopeRows - 1) / kRopeRows;      // row groups per token
+    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (idx >= (long long)M * n_grp * 16) return;
+    const int g8 = (int)(idx & 15);                              // 8-element group of the row
+    const long long rest = idx >> 4;
+    const int n = (int)(rest / n_grp), grp = (int)(rest - (long long)n * n_grp);
+    const int b = n / T, t = n - b * T;
+    const int first = __ldcg(start + b), c = __ldcg(count + b);
+    if (first < 0 || c < 0 || c > T || (long long)first + c > max_pos) {
+        record_error(err, LLAMA_ERR_POS_RANGE);
+        return;
+    }
+    if (t >= c) return;
+    const int pos = first + t;
+    const float4 cs = *reinterpret_cast<const float4*>(cos_tab + (size_t)pos * kRopeMaxPairs + g8 * 4);
+    const float4 sn = *reinterpret_cast<const float4*>(sin_tab + (size_t)pos * kRopeMaxPairs + g8 * 4);
+    const float cv[4] = {cs.x, cs.y, cs.z, cs.w}, sv[4] = {sn.x, sn.y, sn.z, sn.w};
+    const int row0 = grp * kRopeRows;
+    int page = 0;
+    if (row0 + kRopeRows > n_heads) {
+        page = page_of(pages, b, pos >> pages.shift, err);
+        if (page < 0 && row0 >= n_heads) return;   // recorded: rows of the cache are not written
+    }
+    uint4* dst[kRopeRows];
+    uint4 u[kRopeRows];
+#pragma unroll
+    for (int r = 0; r < kRopeRows; ++r) {
+        const int head = row0 + r;
+        dst[r] = nullptr;
+        if (head < n_heads) {
+            dst[r] = reinterpret_cast<uint4*>(q + (size_t)n * n_heads * 128 + (size_t)head * 128 + g8 * 8);
+            u[r] = *dst[r];
+        } else if (head < n_rows && page >= 0) {
+            const bool is_k = head < n_heads + n_kv_heads;
+            const int h = head - n_heads - (is_k ? 0 : n_kv_heads);
+            const size_t to = (((size_t)page * n_kv_heads + h) << pages.shift) + (pos & ((1 << pages.shift) - 1));
+            dst[r] = reinterpret_cast<uint4*>((is_k ? pk : pv) + to * 128 + g8 * 8);
+            u[r] = __ldcg(reinterpret_cast<const uint4*>((is_k ? k : v) + (((size_t)b * n_kv_heads + h) * T + t) * 128 + g8 * 8));
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kRopeRows; ++r) {
+        if (dst[r] == nullptr) continue;
+        if (row0 + r < n_heads + n_kv_heads) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(&u[r]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 pr = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+                const float a0 = __low2float(pr), a1 = __high2float(pr);
+                const __nv_bfloat162 o = __floats2bfloat162_rn(rope_rotate_elem(a0, a1, cv[e], sv[e], false),
+                                                               rope_rotate_elem(a1, a0, cv[e], sv[e], true));
+                w[e] = *reinterpret_cast<const uint32_t*>(&o);
+            }
+        }
+        *dst[r] = u[r];
+    }
+}
+
 template <typename T>
 __global__ void k_embed(const int32_t* __restrict__ ids, const T* __restrict__ w, T* __restrict__ x, int vocab,
                         int d, int32_t* err) {
@@ -373,6 +442,16 @@ cudaError_t launch_rope_inplace(void* q, void* kc, int M, int T, int n_heads, in
     const dim3 grid((unsigned)((threads + 255) / 256));
     return launch_small(k_rope_inplace, grid, dim3(256), s, (bf16*)q, (bf16*)kc, M, T, n_heads, n_kv_heads,
                       kv_seq, start_pos, pos_dev, max_pos, cos_tab, sin_tab, err);
+}
+
+cudaError_t launch_rope_paged(void* q, const void* k, const void* v, int batch, int T, int n_heads, int n_kv_heads,
+                              void* pk, void* pv, const PageTable& pages, const int* start, const int* count,
+                              int max_pos, const float* cos_tab, const float* sin_tab, int* err, cudaStream_t s) {
+    const int M = batch * T;
+    const long long threads = (long long)M * ((n_heads + 2 * n_kv_heads + kRopeRows - 1) / kRopeRows) * 16;
+    const dim3 grid((unsigned)((threads + 255) / 256));
+    return launch_small(k_rope_paged, grid, dim3(256), s, (bf16*)q, (const bf16*)k, (const bf16*)v, M, T, n_heads, n_kv_heads,
+                        (bf16*)pk, (bf16*)pv, pages, start, count, max_pos, cos_tab, sin_tab, err);
 }
 
 cudaError_t launch_embed(const int32_t* ids, int n, const void* w, int vocab, int d, void* x, int32_t* err,

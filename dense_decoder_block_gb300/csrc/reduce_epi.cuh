@@ -87,7 +87,7 @@ __device__ __forceinline__ Qkv4 epi4_qkv_prepare(const GemmEpi& e, int n, int f0
         p.dst = nullptr;
         return p;
     }
-    p.rope = kind < 2;
+    p.rope = kind < 2 && !e.rope_later;
     if (p.rope) {
         const int i0 = row0 >> 1;
         p.c0 = __ldg(e.cos_tab + (size_t)pos * kRopeMaxPairs + i0);

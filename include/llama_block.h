@@ -474,6 +474,21 @@ int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_head
                                 const int32_t* start, const int32_t* count, int max_len, void* o, void* workspace,
                                 size_t workspace_bytes, int32_t* err_dev, void* stream);
 
+/* The block on a chunk of new tokens per sequence, on a paged cache: prompts in chunks, further turns of a
+ * conversation, drafted tokens.  x, y [batch, tokens, d_model] (y may alias x); sequence b has count[b] new tokens
+ * (0 .. tokens) at positions start[b] on, the start and count of its llama_paged_plan; positions 0 .. start[b] - 1 are in
+ * the pages, those of the new tokens are written.  Cache rows have the bits that llama_block_prefill_at writes for the
+ * same x; the attention is llama_paged_chunk_attention's, so y agrees with that call's to the attention's last
+ * rounding, not bit for bit.  Rows of y at t >= count[b] are undefined.  bf16 handles; batch * tokens < 2^30.  A sequence
+ * with start or count out of range, or positions beyond max_seq or its table row, is recorded in the handle's error word
+ * (LLAMA_ERR_POS_RANGE), and so is a page id outside [0, n_pages) (LLAMA_ERR_INVALID_ARG): its rows of the cache are not
+ * written (those of the bad page) and its rows of y are undefined.  workspace:
+ * llama_block_prefill_paged_workspace_bytes (0 for invalid arguments). */
+size_t llama_block_prefill_paged_workspace_bytes(llama_block blk, int batch, int tokens);
+int llama_block_prefill_paged(llama_block blk, const void* x, int batch, int tokens, const llama_paged_cache* kv,
+                              const int32_t* table, int table_stride, const int32_t* start, const int32_t* count,
+                              void* y, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Samples of one prompt share its pages.  refs [n_pages] counts, for each page, the rows
  * that hold it beside the first: all zeros at first, and of no concern to the calls above.
  *

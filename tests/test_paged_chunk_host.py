@@ -83,6 +83,11 @@ def test_free_refusals(lib):
     assert lib.llama_paged_free_workspace_bytes(0, 8) == 0
 
 
+def test_prefill_paged_refusals(lib):
+    assert lib.llama_block_prefill_paged(None, P, 1, 4, _cache(), P, 4, P, P, P, P, 1 << 20, None) == INVALID
+    assert lib.llama_block_prefill_paged_workspace_bytes(None, 1, 4) == 0
+
+
 def test_python_wrappers_check_their_tensors(lib):
     import dense_decoder_block_gb300 as ddb
     z = torch.zeros(2, 10)
