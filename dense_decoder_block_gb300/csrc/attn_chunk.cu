@@ -88,8 +88,8 @@ extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens,
     a.pages.stride = table_stride;
     a.pages.n_pages = kv->n_pages;
     a.pages.shift = page_shift(kv->page_size);
-    // positions must fit max_len and the table row
-    const long long room = (long long)table_stride * kv->page_size;
+    // positions must fit max_len, the table row and 2^30 (sums of two of them fit an int)
+    const long long room = std::min((long long)table_stride * kv->page_size, 1LL << 30);
     a.max_pos = room < max_len ? (int)room : max_len;
     a.dtype = dtype;
     a.err = err_dev;

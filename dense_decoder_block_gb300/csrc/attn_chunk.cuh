@@ -4,8 +4,8 @@
 // its work is the keys that its last token attends and a constant for starting and storing a tile.  Lengths
 // and counts are read on the device, so both ways of dealing tiles out hold for any mixture of sequences
 // under any bound:
-//   - many tiles: whole tiles in rounds, the longest of a sequence first and every other round
-//     from the other end.  CTAs then walk the keys of a head at about the same time, and find them in L2
+//   - many tiles: whole tiles in rounds, the longest of a sequence first (few rounds: of all sequences) and every other
+//     round from the other end.  CTAs then walk the keys of a head at about the same time, and find them in L2
 //     (stretches of a line as below: 8192 tokens of 32 / 8 heads 920 us, in rounds 755, one tile a CTA at a time);
 //   - few: all tiles -- sequences in order, their KV heads, their tiles -- lie one after another on a line of length
 //     W, and CTA i of n takes the stretch from i W / n on, cut at chunks of kAttnChunk keys (chunk_cut): a
@@ -51,7 +51,11 @@ constexpr int kNeverSplit = (2 * kMinPiece - 1) * kAttnChunk + 1;
 // Tiles per CTA from which on they are dealt out whole ...
 constexpr int kRounds = 4;
 // ... and fewer are too where the last round's idle CTAs cost less than join_keys per CTA (2048 tokens of 32 / 8 heads,
-// 256 tiles: split 65 us, whole 40).
+// 256 tiles: split 65 us, whole 40).  Those of several sequences go in the order of all tiles' lengths (8 sequences of
+// mixed starts and counts, 32 / 8 heads, some 300 tiles: sequence by sequence 79 us, so 63), where more tiles than CTAs make an
+// order matter.  A warp finds a tile by bisection over the lengths (32 sequences of 4 tokens, nothing to gain: 0.3 us in
+// 39); a lane holds kSortSeqs / 32 sequences.
+constexpr int kSortSeqs = 64;
 
 // The sequences of a launch (shared memory).
 struct ChunkSeqs {
@@ -131,12 +135,16 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
     return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
 }
 
-// A CTA's pieces in order.
+// A CTA's pieces in order.  The whole warp walks.
 struct ChunkWalk {
     const ChunkSeqs& s;
     int batch, n_kv, tq, cta, n_ctas;
-    bool rounds;
+    bool rounds, sorted;
     int j;                 // rounds: the next one
+    // sorted: the least and most keys of a tile, and the sequences of the lane
+    int shortest, longest;
+    unsigned tq_inverse;
+    int lane_start[kSortSeqs / 32], lane_count[kSortSeqs / 32], lane_tiles[kSortSeqs / 32];
     long long w, w0, w1;   // beginning of the tile at hand, the stretch
     int b, g, y, n_qt, start, count;
 
@@ -149,8 +157,30 @@ struct ChunkWalk {
         g = y = n_qt = start = count = 0;
         const long long tiles = (long long)s.tiles[batch] * n_kv;
         rounds = tiles >= (long long)kRounds * n_ctas;
-        if (!rounds && tiles > 0)
-            rounds = quotient(tiles + n_ctas - 1, n_ctas) * quotient(total, tiles) <= quotient(total, n_ctas) + a.join_keys;
+        sorted = false;
+        if (!rounds && tiles > 0 &&
+            quotient(tiles + n_ctas - 1, n_ctas) * quotient(total, tiles) <= quotient(total, n_ctas) + a.join_keys) {
+            rounds = true;
+            sorted = tiles > n_ctas && batch > 1 && batch <= kSortSeqs;
+        }
+        if (sorted) {
+            tq_inverse = 0x80000000u / (unsigned)tq + 1;
+            longest = 0;
+            shortest = 0x7fffffff;
+#pragma unroll
+            for (int i = 0; i < kSortSeqs / 32; ++i) {
+                const int x = 32 * i + (threadIdx.x & 31), n = x < batch ? s.count[x] : 0;
+                lane_count[i] = n > 0 ? n : -1;
+                lane_start[i] = n > 0 ? s.start[x] : 0x3fffffff;
+                lane_tiles[i] = n > 0 ? s.tiles[x + 1] - s.tiles[x] : 0;
+                if (n > 0) {
+                    longest = max(longest, lane_start[i] + n);
+                    shortest = min(shortest, lane_start[i] + min(tq, n));
+                }
+            }
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            shortest = __reduce_min_sync(0xffffffffu, shortest);
+        }
         if (rounds) return;
         const int n = (int)min((long long)n_ctas, max(tiles, quotient(total, a.min_stretch)));
         if (cta >= n || total == 0) return;
@@ -196,8 +226,59 @@ struct ChunkWalk {
         p.c0 = 0;
         p.c1 = p.n;
     }
+    // Tiles of one of the lane's sequences under one KV head with `keys` keys or more (a tile has
+    // start + min((y + 1) tq, count)).  A division by tq is a product: below 2^23 x / tq = x (2^31 / tq + 1) / 2^31, and
+    // the tiles of a sorted launch hold fewer tokens.
+    __device__ __forceinline__ int tiles_from(int i, int keys) const {
+        const int over = keys - lane_start[i];
+        if (over > lane_count[i]) return 0;
+        return over <= 0 ? lane_tiles[i] : lane_tiles[i] - (int)__umulhi(2u * (unsigned)(over - 1), tq_inverse);
+    }
+    __device__ __forceinline__ int all_from(int keys) const {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kSortSeqs / 32; ++i) n += tiles_from(i, keys);
+        return __reduce_add_sync(0xffffffffu, n) * n_kv;
+    }
+    // Tile number l of the tiles in order of decreasing keys (equal ones: by sequence, then KV head).
+    __device__ __forceinline__ void pick_sorted(int l) {
+        int lo = shortest, hi = longest, above = 0;   // the most keys that more than l tiles have; tiles of more
+        while (lo < hi) {
+            const int mid = lo + ((hi - lo + 1) >> 1), n = all_from(mid);
+            if (n > l) {
+                lo = mid;
+            } else {
+                hi = mid - 1;
+                above = n;
+            }
+        }
+        const int r = l - above;   // among the tiles of `lo` keys, one per sequence and head at most
+        g = r % n_kv;
+        int left = r / n_kv, to_end = 0;
+#pragma unroll
+        for (int i = 0; i < kSortSeqs / 32; ++i) {
+            const int n = tiles_from(i, lo);
+            const unsigned word = __ballot_sync(0xffffffffu, n > tiles_from(i, lo + 1));
+            if (left >= 0 && left < __popc(word)) {
+                const int of = __fns(word, 0, left + 1);
+                b = 32 * i + of;
+                to_end = __shfl_sync(0xffffffffu, n, of);
+            }
+            left = left < __popc(word) ? -1 : left - __popc(word);
+        }
+        load();
+        y = n_qt - to_end;
+    }
     // The next piece; false behind the last.
     __device__ __forceinline__ bool next(ChunkPiece& p) {
+        if (sorted) {
+            const long long l = (long long)j * n_ctas + (j & 1 ? n_ctas - 1 - cta : cta);
+            ++j;
+            if (l >= (long long)s.tiles[batch] * n_kv) return false;
+            pick_sorted((int)l);
+            tile(p);
+            return true;
+        }
         if (rounds) {
             const long long l = (long long)j * n_ctas + (j & 1 ? n_ctas - 1 - cta : cta);
             ++j;

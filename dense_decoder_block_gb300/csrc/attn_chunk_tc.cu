@@ -185,18 +185,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::setmaxnreg_dec<kRegsCtrl>();
         if (warp == 2) {
             // ------------------------------------------------------------------ the pieces
-            if (lane == 0) {
-                ChunkWalk walk(a, seqs, blockIdx.x, gridDim.x);
-                a.cuts[blockIdx.x] = walk.begin();
-                ChunkPiece p;
-                for (int j = 0;; ++j) {
-                    const bool more = walk.next(p);
-                    if (j >= kRing && !ptx::mbar_wait(&pc_free[j % kRing], ((j / kRing) & 1) ^ 1, err)) break;
-                    if (!more) p.c0 = p.c1 = 0;
+            ChunkWalk walk(a, seqs, blockIdx.x, gridDim.x);
+            if (lane == 0) a.cuts[blockIdx.x] = walk.begin();
+            ChunkPiece p;
+            for (int j = 0;; ++j) {
+                const bool more = walk.next(p);
+                if (j >= kRing && !__all_sync(0xffffffffu, ptx::mbar_wait(&pc_free[j % kRing], ((j / kRing) & 1) ^ 1, err))) break;
+                if (!more) p.c0 = p.c1 = 0;
+                if (lane == 0) {
                     pieces[j % kRing] = p;
                     ptx::mbar_arrive(&pc_full[j % kRing]);
-                    if (!more) break;
                 }
+                if (!more) break;
             }
         } else if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer, the whole warp

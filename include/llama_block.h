@@ -455,14 +455,14 @@ int llama_block_decode_paged(llama_block blk, const void* x, int batch, const ll
  * positions 0 .. start[b] + t; heads and scale as in llama_paged_attention.  Rows of o at
  * t >= count[b] are left as they were, and those of q are not used.  max_len bounds
  * start + count.  A sequence with start < 0, a count outside 0 .. tokens, or more positions
- * than max_len or its table row holds is recorded (LLAMA_ERR_POS_RANGE) and its rows are left
+ * than max_len, its table row or 2^30 is recorded (LLAMA_ERR_POS_RANGE) and its rows are left
  * as they were; a page id outside [0, n_pages) among the pages that it attends is recorded
  * (LLAMA_ERR_INVALID_ARG) and leaves that sequence's rows undefined.  Cache rows and table
  * entries behind the last position are not used, and a token's row does not depend on the
  * keys and values behind its position, whatever they hold (infinities and NaN included).  A
  * row is NaN where no finite softmax exists.  bf16 (head_dim 128): products on the tensor
- * cores, weights rounded to bf16 before their product with V and their sum (both held in
- * fp32); fp32 (head_dim 32, 64, 128): fp32 throughout.  At most 64 query heads per KV
+ * cores, weights rounded to bf16 before their product with V (held in fp32, as is the sum of
+ * the weights before they are rounded); fp32 (head_dim 32, 64, 128): fp32 throughout.  At most 64 query heads per KV
  * head, batch * tokens < 2^31, batch <= 65535.  Where there are fewer query rows than the
  * device has room for, the positions of a row are split and joined: the split follows from
  * the call's sizes, starts and counts, so equal calls give equal bits, and a row's last bit

@@ -36,7 +36,7 @@ def chunk_tol(o, mass, reach, dtype, D, L):
     that relative amount, as do the weight's own exponential (2^-22) and the sums: at most 128 keys of a chunk, the 8
     partial sums of its threads, three roundings for each chunk of 64 keys or more that is folded, and three for each of
     at most 304 joined pieces (no more than there are chunks).  bf16 kernels round the weights to bf16 (2^-8 at most)
-    before both the products and their normaliser.  Weights and normaliser move the quotient by at most twice that of sum
+    before the products.  Weights and normaliser move the quotient by at most twice that of sum
     p |v|.  The output is rounded once."""
     chunks = ceil_div(L, 64)
     w = (D + 2) * U * reach + 2.0 ** -22 + (128 + 8 + 3 * chunks + 3 * min(304, chunks) + 4) * U
