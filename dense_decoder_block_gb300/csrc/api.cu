@@ -147,7 +147,7 @@ Ws layout(const llama_block_s* b, int B, int T, uint8_t* base, bool decode, bool
     if (chunk) {   // k and v before they go to their pages, and the attention's partials
         w.k_raw = take(M * kvd * es);
         w.v_raw = take(M * kvd * es);
-        w.chunk = take(attn_chunk_workspace_bytes(d.head_dim));
+        w.chunk = take(attn_chunk_workspace_bytes(d.head_dim, INT32_MAX));
     }
     w.total = off;
     return w;

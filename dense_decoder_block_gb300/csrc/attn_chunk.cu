@@ -17,12 +17,16 @@ bool heads_ok(int n_heads, int n_kv_heads, int head_dim) {
            n_heads / n_kv_heads <= 64 && (head_dim == 32 || head_dim == 64 || head_dim == 128);
 }
 
-size_t partial_bytes(int head_dim) { return (size_t)kChunkMaxCtas * 512 * (head_dim + 2) * sizeof(float); }
+// two partials (m, l, o) of up to 256 rows for each CTA where tiles may be split
+size_t partial_rows(int max_pos) { return max_pos < kNeverSplit ? 0 : (size_t)kChunkMaxCtas * 512; }
+size_t partial_bytes(int head_dim, int max_pos) { return partial_rows(max_pos) * (head_dim + 2) * sizeof(float); }
 
 }  // namespace
 
-// two partials (m, l, o) of up to 256 rows for each CTA, and where the CTAs begin
-size_t attn_chunk_workspace_bytes(int head_dim) { return partial_bytes(head_dim) + kChunkMaxCtas * sizeof(int4); }
+// the partials, and where the CTAs begin
+size_t attn_chunk_workspace_bytes(int head_dim, int max_pos) {
+    return partial_bytes(head_dim, max_pos) + kChunkMaxCtas * (sizeof(int4) + sizeof(int));
+}
 
 int attn_chunk_launches(const AttnArgs& a) {
     return (a.batch + kChunkSeqs - 1) / kChunkSeqs * (device_sm_count() == 1 || a.max_pos < kNeverSplit ? 1 : 2);
@@ -44,8 +48,9 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, const int* start, const in
     k.pages = a.pages;
     k.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
     k.partial = (float*)ws;
-    k.part_ml = (float2*)(k.partial + (size_t)kChunkMaxCtas * 512 * a.head_dim);
-    k.cuts = (int4*)((uint8_t*)ws + partial_bytes(a.head_dim));
+    k.part_ml = (float2*)(k.partial + partial_rows(a.max_pos) * a.head_dim);
+    k.cuts = (int4*)((uint8_t*)ws + partial_bytes(a.head_dim, a.max_pos));
+    k.cut_tokens = (int*)(k.cuts + kChunkMaxCtas);
     k.err = a.err;
     return a.dtype == LLAMA_BF16 ? launch_chunk_tc(k, a.head_dim, s) : launch_chunk_f32(k, a.head_dim, s);
 }
@@ -57,7 +62,7 @@ using namespace llama;
 extern "C" size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads,
                                                               int head_dim, int max_len) {
     if (batch <= 0 || tokens <= 0 || max_len <= 0 || !heads_ok(n_heads, n_kv_heads, head_dim)) return 0;
-    return attn_chunk_workspace_bytes(head_dim);
+    return attn_chunk_workspace_bytes(head_dim, max_len);
 }
 
 extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_heads, int n_kv_heads,

@@ -36,7 +36,8 @@ struct ChunkArgs {
     int min_stretch;     // the least work of a CTA (keys) for which tiles are split
     float* partial;      // [2 CTAs][halves of a tile][head_dim / 4][rows of a half] float4
     float2* part_ml;     // [2 CTAs][halves][rows]
-    int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it
+    int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it ...
+    int* cut_tokens;     // ... and the tile's tokens
     int* err;
 };
 cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s);    // bf16
@@ -130,12 +131,22 @@ struct ChunkPiece {
     int c0, c1, n;    // of n chunks
 };
 
-// a / b of numbers that are not negative, in 32 bits where they fit (a 64-bit division takes a microsecond of one lane)
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-    return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+// The last x of 0 .. n - 1 for which pred holds; it holds for 0, and for none behind one that it does not hold for.
+// The whole warp, 32 probes at a time (a bisection takes the latency of each of its probes).
+template <class Pred>
+__device__ __forceinline__ int last_that(int n, Pred pred) {
+    int lo = 0;
+    while (n > 1) {
+        const int by = (n + 31) >> 5, x = (threadIdx.x & 31) * by;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, x < n && pred(lo + x)));
+        lo += k * by;
+        n = min(by, n - k * by);
+    }
+    return lo;
 }
 
-// A CTA's pieces in order.  The whole warp walks.
+// A CTA's pieces in order.  The whole warp walks: the CTA waits for the first piece, and one lane's 64-bit divisions
+// and bisections took 2.5 us of it.
 struct ChunkWalk {
     const ChunkSeqs& s;
     int batch, n_kv, tq, cta, n_ctas;
@@ -155,11 +166,13 @@ struct ChunkWalk {
         j = 0;
         w = w0 = w1 = 0;
         g = y = n_qt = start = count = 0;
-        const long long tiles = (long long)s.tiles[batch] * n_kv;
-        rounds = tiles >= (long long)kRounds * n_ctas;
+        const int tiles = s.tiles[batch] * n_kv;
+        // work of a CTA, if all have the same and if it takes the tiles of a CTA in rounds
+        const int n_rounds = 1 + (tiles > n_ctas) + (tiles > 2 * n_ctas) + (tiles > 3 * n_ctas);
+        const float each_f = __fdividef((float)total, (float)n_ctas);
         sorted = false;
-        if (!rounds && tiles > 0 &&
-            quotient(tiles + n_ctas - 1, n_ctas) * quotient(total, tiles) <= quotient(total, n_ctas) + a.join_keys) {
+        rounds = tiles >= kRounds * n_ctas;
+        if (!rounds && tiles > 0 && (float)n_rounds * (float)total <= (each_f + a.join_keys) * (float)tiles) {
             rounds = true;
             sorted = tiles > n_ctas && batch > 1 && batch <= kSortSeqs;
         }
@@ -182,37 +195,26 @@ struct ChunkWalk {
             shortest = __reduce_min_sync(0xffffffffu, shortest);
         }
         if (rounds) return;
-        const int n = (int)min((long long)n_ctas, max(tiles, quotient(total, a.min_stretch)));
+        const int n = min(n_ctas, max(tiles, (int)__fdividef((float)total, (float)a.min_stretch)));
         if (cta >= n || total == 0) return;
-        const long long each = quotient(total, n);
+        // every CTA has the same `each`, whatever its last bits
+        const long long each = (long long)__fdividef((float)total, (float)n);
         w0 = each * cta;
         w1 = cta == n - 1 ? total : w0 + each;
-        int lo = 0, hi = batch - 1;   // the last sequence that begins at or before w0: one with work
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s.pre[mid] * n_kv <= w0) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
+        // the last sequence that begins at or before w0: one with work
+        b = last_that(batch, [&](int x) { return s.pre[x] * n_kv <= w0; });
         load();
         const long long one = s.pre[b + 1] - s.pre[b];
         long long r = w0 - s.pre[b] * n_kv;
-        g = (int)quotient(r, one);
+        g = last_that(n_kv, [&](int x) { return one * x <= r; });
         r -= g * one;
-        lo = 0;
-        hi = n_qt - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (tiles_work(start, tq, mid) <= r) lo = mid;
-            else hi = mid - 1;
-        }
-        y = lo;
+        y = last_that(n_qt, [&](int x) { return tiles_work(start, tq, x) <= r; });
         w = w0 - r + tiles_work(start, tq, y);
     }
     __device__ __forceinline__ void load() {
         start = s.start[b];
         count = s.count[b];
-        n_qt = (count + tq - 1) / tq;
+        n_qt = s.tiles[b + 1] - s.tiles[b];
     }
     __device__ __forceinline__ void tile(ChunkPiece& p) const {
         p.b = b;
@@ -231,8 +233,8 @@ struct ChunkWalk {
     // the tiles of a sorted launch hold fewer tokens.
     __device__ __forceinline__ int tiles_from(int i, int keys) const {
         const int over = keys - lane_start[i];
-        if (over > lane_count[i]) return 0;
-        return over <= 0 ? lane_tiles[i] : lane_tiles[i] - (int)__umulhi(2u * (unsigned)(over - 1), tq_inverse);
+        const int n = lane_tiles[i] - (int)__umulhi(2u * (unsigned)max(over - 1, 0), tq_inverse);
+        return over > lane_count[i] ? 0 : n;
     }
     __device__ __forceinline__ int all_from(int keys) const {
         int n = 0;
@@ -272,26 +274,20 @@ struct ChunkWalk {
     // The next piece; false behind the last.
     __device__ __forceinline__ bool next(ChunkPiece& p) {
         if (sorted) {
-            const long long l = (long long)j * n_ctas + (j & 1 ? n_ctas - 1 - cta : cta);
+            const int l = j * n_ctas + (j & 1 ? n_ctas - 1 - cta : cta);
             ++j;
-            if (l >= (long long)s.tiles[batch] * n_kv) return false;
-            pick_sorted((int)l);
+            if (l >= s.tiles[batch] * n_kv) return false;
+            pick_sorted(l);
             tile(p);
             return true;
         }
         if (rounds) {
-            const long long l = (long long)j * n_ctas + (j & 1 ? n_ctas - 1 - cta : cta);
+            const int l = j * n_ctas + (j & 1 ? n_ctas - 1 - cta : cta);
             ++j;
-            if (l >= (long long)s.tiles[batch] * n_kv) return false;
-            int lo = 0, hi = batch - 1;
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if ((long long)s.tiles[mid] * n_kv <= l) lo = mid;
-                else hi = mid - 1;
-            }
-            b = lo;
+            if (l >= s.tiles[batch] * n_kv) return false;
+            b = last_that(batch, [&](int x) { return s.tiles[x] * n_kv <= l; });
             load();
-            const int r = (int)(l - (long long)s.tiles[b] * n_kv);
+            const int r = l - s.tiles[b] * n_kv;
             g = r % n_kv;
             y = n_qt - 1 - r / n_kv;
             tile(p);
@@ -316,21 +312,29 @@ struct ChunkWalk {
         }
         return false;
     }
-    // Where the stretch begins: {b, g, tile, chunk}; chunk 0 when it begins with a tile.  Before the first next().
-    __device__ __forceinline__ int4 begin() const {
-        if (b >= batch) return make_int4(0, 0, 0, 0);
-        const int kv_last = start + min((y + 1) * tq, count) - 1, n = kv_last / kAttnChunk + 1;
-        const int c = chunk_cut(w0 - w, n, (long long)kv_last + 1 + kTileKeys);
-        return make_int4(b, g, y, c < n ? c : 0);
+    // Where the stretch begins (chunk 0 when it begins with a tile).  Before the first next().
+    __device__ __forceinline__ void begin(const ChunkArgs& a) const {
+        int4 cut = make_int4(0, 0, 0, 0);
+        int tokens = 0;
+        if (b < batch) {
+            tokens = min(tq, count - y * tq);
+            const int kv_last = start + y * tq + tokens - 1, n = kv_last / kAttnChunk + 1;
+            const int c = chunk_cut(w0 - w, n, (long long)kv_last + 1 + kTileKeys);
+            cut = make_int4(b, g, y, c < n ? c : 0);
+        }
+        if (threadIdx.x % 32 == 0) {
+            a.cuts[cta] = cut;
+            a.cut_tokens[cta] = tokens;
+        }
     }
 };
 
 namespace {
 
 // Joins the pieces of the split tiles, in ascending order: o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p, M the
-// largest m_p.  Every CTA reads all cuts and lists the split tiles; an item is one half of a tile and kJoinCols columns,
-// thread = row
-// (rows of 64: two column groups).  The loads of several pieces go out together.
+// largest m_p.  Every CTA reads all cuts and counts the split tiles; an item is one half of a tile and kJoinCols columns,
+// thread = row (rows of 64: two column groups).  The loads of several pieces go out together.  Bound by the partials (100
+// tokens behind 8192, 32 / 8 heads: 20 MB, written and read within L2) and the latency of two loads before them.
 constexpr int kJoinCols = 8, kJoinBatch = 6;
 constexpr int kJoinThreads = 128;
 
@@ -353,45 +357,41 @@ __device__ __forceinline__ void store_joined(float* dst, const float (&o)[kJoinC
 template <typename T, int DH, int HALVES, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArgs a, int n_ctas) {
     __shared__ int4 s_cut[kChunkMaxCtas];
-    __shared__ int s_first[kChunkMaxCtas];
-    __shared__ unsigned s_word[8];   // bit i: a split tile's list begins with CTA i
+    __shared__ int s_tokens[kChunkMaxCtas];
+    __shared__ unsigned s_word[8];   // bit i: the first CTA that begins inside its tile is CTA i
     static_assert(kChunkMaxCtas <= 2 * kJoinThreads && kJoinThreads == 128, "two CTAs a thread, words of 32");
+    auto same_tile = [](const int4& c, const int4& d) { return c.x == d.x && c.y == d.y && c.z == d.z; };
     ptx::griddep_wait();
-    for (int i = threadIdx.x; i < n_ctas; i += kJoinThreads) s_cut[i] = __ldcg(a.cuts + i);
-    __syncthreads();
-    // CTA j begins inside the tile that CTA i begins inside of
-    auto same = [&](int i, int j) {
-        return s_cut[j].w > 0 && s_cut[j].x == s_cut[i].x && s_cut[j].y == s_cut[i].y && s_cut[j].z == s_cut[i].z;
-    };
-    bool first[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int i = x * kJoinThreads + threadIdx.x;
-        first[x] = i > 0 && i < n_ctas && s_cut[i].w > 0 && !same(i, i - 1);
-        const unsigned word = __ballot_sync(0xffffffffu, first[x]);
+        bool first = false;
+        if (i < n_ctas) {
+            const int4 cut = __ldcg(a.cuts + i), before = __ldcg(a.cuts + max(i - 1, 0));
+            s_cut[i] = cut;
+            s_tokens[i] = __ldcg(a.cut_tokens + i);
+            first = cut.w > 0 && !(before.w > 0 && same_tile(cut, before));   // CTA 0 begins with a tile
+        }
+        const unsigned word = __ballot_sync(0xffffffffu, first);
         if ((threadIdx.x & 31) == 0) s_word[i >> 5] = word;
     }
     __syncthreads();
     int n_split = 0;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int i = x * kJoinThreads + threadIdx.x;
-        int at = __popc(s_word[i >> 5] & ((1u << (i & 31)) - 1));
-        for (int w = 0; w < i >> 5; ++w) at += __popc(s_word[w]);
-        if (first[x]) s_first[at] = i;
-    }
-#pragma unroll
     for (int w = 0; w < 8; ++w) n_split += __popc(s_word[w]);
-    __syncthreads();
+    // CTA j begins inside the tile that CTA i begins inside of
+    auto same = [&](int i, int j) { return s_cut[j].w > 0 && same_tile(s_cut[i], s_cut[j]); };
     constexpr int kCols = DH / kJoinCols, kSets = kJoinThreads / ROWS;   // column groups; of an item
     const int n_rep = a.n_heads / a.n_kv_heads, tqh = a.tq / HALVES, row = threadIdx.x % ROWS, t_local = row / n_rep;
     const int items = n_split * HALVES * (kCols / kSets);
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
         const int cols = item % (kCols / kSets) * kSets + threadIdx.x / ROWS, x = item / (kCols / kSets), half = x % HALVES;
-        const int i = s_first[x / HALVES];
+        int i = x / HALVES, w = 0;   // the CTA of the i-th bit
+        for (; i >= __popc(s_word[w]); ++w) i -= __popc(s_word[w]);
+        i = w * 32 + __fns(s_word[w], 0, i + 1);
         const int4 cut = s_cut[i];
         const int t = cut.z * a.tq + half * tqh + t_local;
-        if (t_local >= tqh || t >= a.count[cut.x]) continue;
+        if (t_local >= tqh || half * tqh + t_local >= s_tokens[i]) continue;
         int end = i + 1;   // CTAs that begin in the tile: i .. end - 1
         while (end < n_ctas && same(i, end)) ++end;
         // piece k of end - i + 1: CTA i - 1's last, then the first ones of CTAs i, i + 1, ...; a piece is empty where the

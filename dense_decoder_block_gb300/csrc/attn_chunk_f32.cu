@@ -59,10 +59,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
     __syncthreads();
     const int n_rep = a.n_heads / a.n_kv_heads, shift = a.pages.shift;
     ChunkWalk walk(a, seqs, blockIdx.x, gridDim.x);
-    if (tid == 0) {
-        a.cuts[blockIdx.x] = walk.begin();
-        ptx::griddep_launch_dependents();
-    }
+    if (tid < 32) walk.begin(a);
+    if (tid == 0) ptx::griddep_launch_dependents();
     ChunkPiece p;
     while (walk.next(p)) {
         const int rows = (p.t1 - p.t0) * n_rep;

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == 2) {
             // ------------------------------------------------------------------ the pieces
             ChunkWalk walk(a, seqs, blockIdx.x, gridDim.x);
-            if (lane == 0) a.cuts[blockIdx.x] = walk.begin();
+            walk.begin(a);
             ChunkPiece p;
             for (int j = 0;; ++j) {
                 const bool more = walk.next(p);
@@ -233,6 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return max(id, 0);   // recorded; the rows are undefined, the copy stays inside the cache
                 };
                 int id = lookup(p.c0), before = 0;
+                // Q's place is free when the piece before has its last S, K's a chunk earlier; the first piece waits for
+                // its page ids
+                if (j > 0) copy(&mK, p.c0, id, OFF_K, k_full, k_empty, kc);
+                if (!ok) break;
                 int go = 1;
                 if (lane == 0 && j >= 1) go = ptx::mbar_wait(q_empty, (j - 1) & 1, err);
                 if (!__shfl_sync(0xffffffffu, go, 0)) break;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // K a chunk ahead of V: its stage is free earlier
                 for (int c = p.c0; ok && c <= p.c1; ++c) {
                     const int next = lookup(c + 1);
-                    if (c < p.c1) copy(&mK, c, id, OFF_K, k_full, k_empty, kc);
+                    if (c < p.c1 && (j == 0 || c > p.c0)) copy(&mK, c, id, OFF_K, k_full, k_empty, kc);
                     if (ok && c > p.c0) copy(&mV, c - 1, before, OFF_V, v_full, v_empty, vc);
                     before = id;
                     id = next;
@@ -515,8 +519,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ok) ok = ptx::mbar_wait(&pv_done[s], took >> s & 1, err);
                 }
                 ptx::tc_fence_after();
+                // O read: the next piece's first PV may overwrite it (half 0's while half 1 is stored)
+                auto free_o = [&] {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::mbar_arrive(&o_free[half]);
+                        if (!pair) ptx::mbar_arrive(&o_free[1]);
+                    }
+                };
                 const int tokens = min(p.t1 - p.t0 - half * tqh, tqh);
-                if (quarter * 32 >= tokens * n_rep) continue;
+                if (quarter * 32 >= tokens * n_rep) {
+                    free_o();
+                    continue;
+                }
                 const bool valid = t_local < tokens;
                 float2 x = ml[((took >> half & 1) * 2 + half) * 128];
                 float w0 = 1.f, w1 = 0.f;   // weights of the streams
@@ -572,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                free_o();
                 if (poisoned && valid && ok) {
                     // infinities and NaN that were taken out of V: onto the columns of the rows that see them
                     const int first = max(p.pos0 + 1, p.c0 * kAttnChunk);
@@ -590,13 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             took ^= steps > 1 ? 3 : 1;
-            ptx::tc_fence_before();   // O read: the next piece's first PV may overwrite it
             __syncwarp();
-            if (lane == 0) {
-                ptx::mbar_arrive(&o_free[0]);
-                ptx::mbar_arrive(&o_free[1]);
-                ptx::mbar_arrive(&pc_free[j % kRing]);
-            }
+            if (lane == 0) ptx::mbar_arrive(&pc_free[j % kRing]);
         }
     }
 
@@ -644,7 +656,7 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
         r = launch_pdl(k_attn_chunk, dim3(n_ctas), dim3(kThreads), SMEM_BYTES, s, mq, mk, mv, k);
         if (r != cudaSuccess) return r;
         if (n_ctas == 1 || a.max_pos < kNeverSplit) continue;
-        r = launch_pdl(k_attn_chunk_join<bf16, 128, 2, 128>, dim3(8 * n_ctas), dim3(kJoinThreads), 0, s, k, (int)n_ctas);
+        r = launch_pdl(k_attn_chunk_join<bf16, 128, 2, 128>, dim3(4 * n_ctas), dim3(kJoinThreads), 0, s, k, (int)n_ctas);
         if (r != cudaSuccess) return r;
     }
     return cudaSuccess;
