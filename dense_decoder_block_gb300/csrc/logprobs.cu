@@ -112,7 +112,7 @@ struct Shared {
     unsigned long long cand[kSeg];        // candidates
     int segs[kMaxTop];
     unsigned least;
-    unsigned seg_max[kMaxSegs];           // order_bits of the segments' maxima
+    alignas(16) unsigned seg_max[kMaxSegs + 3];   // order_bits of the segments' maxima, and zeros up to a multiple of 4
 };
 
 __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == kManyThreads ? 7 : 2) k_
     const float* row = a.logits + (size_t)r * V;
     const int head = (int)((uintptr_t)row >> 2 & 3);
     const int n_segs = (head + V + kSeg - 1) / kSeg;
+    if (rank == 0 && tid < 3) sh.seg_max[n_segs + tid] = 0;
     // ---------------------------------------------------------------- the pass: warp x of the row takes segments x, x + n, ...
     const int me = rank * kWarps + warp, all = ctas * kWarps;
     const unsigned none = order_bits(-INFINITY);
@@ -293,14 +294,27 @@ __global__ void __launch_bounds__(kThreads, kThreads == kManyThreads ? 7 : 2) k_
             }
         }
     } else {
-        // all threads: a segment's rank is the number of better ones
-        for (int g = tid; g < n_segs; g += kThreads) {
-            const unsigned b = sh.seg_max[g];
+        // all threads: a segment's rank is the number of better ones, those of the same best in front among them.  Four
+        // at a time: the loop takes the latency of its reads, and a third of a row's time one by one (15.1 us, here
+        // 9.9; 1 row, 20 alternatives).
+        const int n4 = (n_segs + 3) & ~3;
+        const uint4* seg4 = reinterpret_cast<const uint4*>(sh.seg_max);
+        for (int g0 = warp * 32; g0 < n_segs; g0 += kThreads) {
+            const int g = g0 + lane;
+            const unsigned b = g < n_segs ? sh.seg_max[g] : 0;
             int better = 0;
-            for (int x = 0; x < n_segs; ++x) {
-                const unsigned o = sh.seg_max[x];
-                better += o > b || (o == b && x < g);
+#pragma unroll 1
+            for (int after = 0; after < 2; ++after) {   // the segments in front of the warp's 32, and behind them
+                const unsigned least = b + after;
+#pragma unroll 4
+                for (int x = after ? g0 / 4 + 8 : 0; x < (after ? n4 : g0) / 4; ++x) {
+                    const uint4 o = seg4[x];
+                    better += (o.x >= least) + (o.y >= least) + (o.z >= least) + (o.w >= least);
+                }
             }
+#pragma unroll 8
+            for (int x = 0; x < 32; ++x) better += __shfl_sync(0xffffffffu, b, x) >= b + (x >= lane);
+            if (g >= n_segs) continue;
             if (better < want) sh.segs[better] = g;
             if (better == want - 1) sh.least = b;
         }
