@@ -421,7 +421,7 @@ extern "C" int llama_paged_free(const int32_t* list, const int32_t* lens, int n,
     if (n < 0 || n > kMaxRows || table_rows <= 0 || table_stride <= 0) return LLAMA_ERR_INVALID_ARG;
     const int rc = paged_geometry_check(page_size, n_pages);
     if (rc != LLAMA_OK) return rc;
-    if (table_rows > kMaxRows || (long long)n * table_stride > INT32_MAX) return LLAMA_ERR_UNSUPPORTED_DIMS;
+    if (table_rows > kMaxRows || (long long)n * table_stride > INT32_MAX - 1024) return LLAMA_ERR_UNSUPPORTED_DIMS;
     if (!paged_pools_ok(pool, pool_out)) return LLAMA_ERR_INVALID_ARG;
     if (n > 0 && (!list || !lens || !refs || !free_pages || !table)) return LLAMA_ERR_INVALID_ARG;
     if (n > 0 && (!ws || ws_bytes < llama_paged_free_workspace_bytes(n, n_pages))) return LLAMA_ERR_WORKSPACE;

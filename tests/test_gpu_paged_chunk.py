@@ -314,6 +314,29 @@ def test_graphs_and_streams():
     assert torch.equal(o, want[0])
 
 
+def test_two_calls_at_once():
+    """A call whose tiles are split and one of whole tiles, on two streams over the same cache, a workspace each."""
+    ddb = _ddb()
+    calls = []
+    rows, pk, pv, table = make([6000, 40], [90, 1500], 8, 128, 64, BF, 21)
+    kv = ddb.PagedCache(pk, pv)
+    for start, count, tokens in (([6000, 40], [90, 3], 90), ([0, 40], [0, 1500], 1500)):
+        q = queries(2, tokens, 32, 128, BF, tokens, count)
+        calls.append((q, _i32(start), _i32(count), attend(ddb, q, kv, table, start, count, 6090)))
+    streams = [torch.cuda.Stream() for _ in calls]
+    spaces = [torch.empty(ddb.llama_paged_chunk_attention_workspace_bytes(2, q.shape[1], 32, 8, 128, 6090), dtype=torch.uint8,
+                          device=DEV) for q, *_ in calls]
+    outs = [torch.full_like(q, 7.0) for q, *_ in calls]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for (q, st, ct, _), o, ws, stream in zip(calls, outs, spaces, streams):
+            with torch.cuda.stream(stream):
+                ddb.llama_paged_chunk_attention(q, kv, table, st, ct, 6090, o, ws)
+    torch.cuda.synchronize()
+    for (_, _, _, want), o in zip(calls, outs):
+        assert torch.equal(o, want)
+
+
 def test_pages_beyond_32_bit_offsets():
     """A cache of 2.3e9 elements each for K and V: pages at its end give what a small cache gives."""
     ddb = _ddb()
