@@ -164,8 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
             const bool all = key0 + kKeys - 1 <= p.pos0 && rows == kRows;
             auto average = [&](auto masked) {
                 constexpr bool kMasked = decltype(masked)::value;
+                const int n_keys = kMasked ? min(kKeys, key_end - key0) : kKeys;   // 20 keys: the call 12.8 -> 11.4 us
 #pragma unroll 2
-                for (int k = 0; k < kKeys; k += 4) {
+                for (int k = 0; k < n_keys; k += 4) {
                     float4 w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sm + TL::OFF_P + (4 * y + i) * TL::LDP + k);
