@@ -134,11 +134,12 @@ __global__ void __launch_bounds__(kShareThreads) k_fork_jobs(const ForkArgs a) {
     }
 }
 
-// The copies of a fork -- K and V of every layer, heads, rows, vectors -- are one list, cut over gridDim.y - 1 CTAs; a
-// thread has kCopyVec loads under way.  (A CTA per layer and K or V read jobs and tables again and was mostly waiting:
-// 112 forks of 32 layers 37 us.)  The last CTA of a fork moves its table entries.
+// The copies of a fork -- the rows of one head, in K and V of every layer -- are one list, cut over the warps of
+// gridDim.y - 1 CTAs; a lane has kCopyVec loads under way.  (A CTA per layer and K or V read jobs and tables again and was
+// mostly waiting: 112 forks of 32 layers 37 us.  A list of single vectors took a division for each: 30 us, so 23.5, at 0.86
+// of the copy rate.)  The last CTA of a fork moves its table entries.
 constexpr int kCopyThreads = 256;
-constexpr int kCopyVec = 4;
+constexpr int kCopyVec = 8;
 constexpr int kCopyCtas = 16;   // per SM: from here on a CTA takes more
 
 __global__ void __launch_bounds__(kCopyThreads) k_fork_copy(const ForkArgs a, const __grid_constant__ ForkCaches c) {
@@ -164,25 +165,22 @@ __global__ void __launch_bounds__(kCopyThreads) k_fork_copy(const ForkArgs a, co
         return;
     }
     const size_t page = (size_t)a.n_kv_heads << (a.shift + a.log_vec);
-    const unsigned per_head = j.w << a.log_vec, per_buffer = a.n_kv_heads * per_head;   // vectors: below 2^31
-    const long long n = (long long)per_buffer * 2 * a.n_layers, step = (long long)parts * kCopyThreads;
-    for (long long x0 = (long long)blockIdx.y * kCopyThreads + threadIdx.x; x0 < n; x0 += step * kCopyVec) {
-        uint4 v[kCopyVec];
-        uint4* dst[kCopyVec];
+    const int run = j.w << a.log_vec, lane = threadIdx.x & 31;   // vectors of a head
+    const int heads = 2 * a.n_layers * a.n_kv_heads, step = parts * (kCopyThreads / 32);
+    for (int u = blockIdx.y * (kCopyThreads / 32) + (threadIdx.x >> 5); u < heads; u += step) {
+        const int b = u / a.n_kv_heads;
+        const size_t at = (size_t)(u - b * a.n_kv_heads) << (a.shift + a.log_vec);
+        const uint4* src = c.kv[b] + sp * page + at;
+        uint4* dst = c.kv[b] + dp * page + at;
+        for (int x0 = lane; x0 < run; x0 += 32 * kCopyVec) {
+            uint4 v[kCopyVec];
 #pragma unroll
-        for (int i = 0; i < kCopyVec; ++i) {
-            const long long x = x0 + i * step;
-            if (x < n) {
-                const unsigned b = n >> 31 ? (unsigned)(x / per_buffer) : (unsigned)x / per_buffer;
-                const unsigned r = (unsigned)(x - (long long)b * per_buffer), h = r / per_head;
-                const size_t at = ((size_t)h << (a.shift + a.log_vec)) + (r - h * per_head);
-                v[i] = __ldcg(c.kv[b] + sp * page + at);
-                dst[i] = c.kv[b] + dp * page + at;
-            }
+            for (int i = 0; i < kCopyVec; ++i)
+                if (x0 + 32 * i < run) v[i] = __ldcg(src + x0 + 32 * i);
+#pragma unroll
+            for (int i = 0; i < kCopyVec; ++i)
+                if (x0 + 32 * i < run) dst[x0 + 32 * i] = v[i];
         }
-#pragma unroll
-        for (int i = 0; i < kCopyVec; ++i)
-            if (x0 + i * step < n) *dst[i] = v[i];
     }
 }
 
@@ -403,8 +401,7 @@ extern "C" int llama_paged_fork(const int32_t* src, const int32_t* dst, const in
     cudaStream_t s = (cudaStream_t)stream;
     if (launch_pdl(k_fork_jobs, dim3(1), dim3(kShareThreads), 0, s, a) != cudaSuccess) return LLAMA_ERR_CUDA;
     if (n == 0) return LLAMA_OK;
-    const long long most = (((long long)n_kv_heads * (caches[0].page_size - 1)) << a.log_vec) * 2 * n_layers;   // vectors of a fork
-    const long long want = (most + kCopyThreads * kCopyVec - 1) / (kCopyThreads * kCopyVec);
+    const long long want = (2LL * n_layers * n_kv_heads + kCopyThreads / 32 - 1) / (kCopyThreads / 32);
     const long long room = std::max(1, kCopyCtas * device_sm_count() / n);
     const dim3 grid(n, (unsigned)std::min(want, room) + 1);
     return launch_pdl(k_fork_copy, grid, dim3(kCopyThreads), 0, s, a, c) == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA;
