@@ -20,6 +20,13 @@
 // Rows do not see what lies behind them: P is 0 there, and so that 0 times an infinity or a NaN does not reach
 // O, such values of a tile's newest positions are taken out of the chunk's V and added to the rows that do see
 // them at the end (an infinity or NaN in O either way).
+//
+// Bound, over long rows, by the tensor pipe and what of a stream's softmax the other stream's MMAs do not cover: a chunk's
+// four MMAs take 1.06 us, the step 1.45 (the pipe is 73 % active; the softmax issues in 41 % of the slots, at half the
+// rate of ex2).  A tile costs 4 us beside its steps: the first copies, the first softmax, the output; a call 5 before its
+// first MMA (lengths, the walk, the block table, Q and K: one load behind another).  Whole calls: 8192 tokens of 32 / 8
+// heads 355 us (1.55 PFLOP/s), 4096 of 64 / 8 behind 4096 515 (1.60), 2048 of 32 / 8 38, 32 x 4 behind 1000 35
+// (3.8 TB/s), 100 behind 8192 31, one token at 100 positions 7.
 #include <algorithm>
 
 #include "attn_chunk.cuh"

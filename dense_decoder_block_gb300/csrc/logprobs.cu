@@ -17,7 +17,8 @@
 // Few rows are split over a cluster of CTAs of 16 warps (their triples and segment maxima in distributed shared memory,
 // the first CTA finishes the row).  Many rows (kManyRows per SM or more) take a CTA of 4 warps each, 8 to an SM: one
 // finishes its row while the others read, and no round of large CTAs ends half empty (924 rows of 128256 logits: 137 us
-// with 16 warps a row).
+// with 16 warps a row, 75 so: 6.3 TB/s, 0.95 of the copy rate).  Few rows are bound by a chain of round trips: 1 row with
+// 20 alternatives 9.9 us, 32 rows with 5 11.5.
 #include <algorithm>
 #include <climits>
 #include <cmath>
