@@ -110,7 +110,8 @@ struct Shared {
     Sums part[kMaxCluster * kFewThreads / 32];
     Sums total;                           // m, log(1 + d), -
     int n_cand;
-    unsigned long long cand[kSeg];        // candidates
+    unsigned long long cand[kMaxTop * 32];   // candidates; the lanes' best of the segments
+    int tally[2][kFewThreads / 32];
     int segs[kMaxTop];
     unsigned least;
     alignas(16) unsigned seg_max[kMaxSegs + 3];   // order_bits of the segments' maxima, and zeros up to a multiple of 4
@@ -145,6 +146,51 @@ __device__ __forceinline__ void load_segment(const float* row, int head, int voc
             z[i] = v >= 0 && v < vocab ? __ldcg(row + v) : -INFINITY;
         }
     }
+}
+
+// The n-th largest of the lanes' bests, the best of each lane's 16 logits of the segments sh.segs[0 .. want - 1], found by
+// halving the keys' range.  A function of its own: seldom called, and within the kernel its instructions cost every row 0.6 us.
+template <int kThreads>
+__device__ __noinline__ unsigned long long nth_of_lanes(Shared& sh, const float* row, int head, int V, int want, int n) {
+    constexpr int kWarps = kThreads / 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int k = warp; k < want; k += kWarps) {
+        const int seg = sh.segs[k];
+        float c[4 * kVec];
+        load_segment(row, head, V, seg, c);
+        unsigned best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * kVec; ++i) {   // by increasing place
+            const int v = seg * kSeg - head + ((i >> 2) * 32 + lane) * 4 + (i & 3);
+            const unsigned bits = order_bits(c[i]);
+            if (v >= 0 && v < V && bits > best) {
+                best = bits;
+                at = v;
+            }
+        }
+        sh.cand[k * 32 + lane] = best ? order_key(best, at) : 0ull;
+    }
+    __syncthreads();
+    unsigned long long least = 0;
+    for (int bit = 63, turn = 0; bit >= 0; --bit, turn ^= 1) {
+        if (bit == 31) {   // the places: all below 2^20
+            bit = 19;
+            least |= 0xfff00000u;
+        }
+        const unsigned long long above = least | 1ull << bit;
+        int reach = 0;
+        for (int i = tid; i < want * 32; i += kThreads) reach += sh.cand[i] >= above;
+        reach = __reduce_add_sync(0xffffffffu, reach);
+        if (lane == 0) sh.tally[turn][warp] = reach;
+        __syncthreads();
+        reach = 0;
+        for (int w = 0; w < kWarps; ++w) reach += sh.tally[turn][w];
+        if (reach >= n) least = above;
+        if (reach == n) break;
+    }
+    __syncthreads();
+    return least;
 }
 
 template <int kThreads, bool CLUSTER>
@@ -321,58 +367,48 @@ __global__ void __launch_bounds__(kThreads, kThreads == kManyThreads ? 7 : 2) k_
         }
     }
     __syncthreads();
-    // their logits that may be among the n best: none below the least of the n segments' maxima (all, with fewer segments)
-    const unsigned least = want < n ? 0u : sh.least;
-    for (int k = warp; k < want; k += kWarps) {
-        const int seg = sh.segs[k];
-        float c[4 * kVec];
-        load_segment(row, head, V, seg, c);
+    // Their logits that may be among the n best are listed: none is below the least of the n segments' maxima (of fewer
+    // segments all may).  Where these are more than the list holds (rows of less than n segments, rows in order, rows of few
+    // values): the n-th largest of the lanes' bests bounds the n best logits, n lanes reach it, and so at most 16 n <= kSeg
+    // logits.  (One warp that sorted the segments in took 108 us for rows of 4584 logits, 20 alternatives; so 11.4.)
+    unsigned long long least = want < n ? 0ull : (unsigned long long)sh.least << 32;
+    bool narrow = want < n && V > kSeg;
+    while (true) {
+        if (narrow) least = nth_of_lanes<kThreads>(sh, row, head, V, want, n);
+        for (int k = warp; k < want; k += kWarps) {
+            const int seg = sh.segs[k];
+            float c[4 * kVec];
+            load_segment(row, head, V, seg, c);
 #pragma unroll
-        for (int i = 0; i < 4 * kVec; ++i) {
-            const int v = seg * kSeg - head + ((i >> 2) * 32 + lane) * 4 + (i & 3);
-            const unsigned bits = order_bits(c[i]);
-            if (v >= 0 && v < V && bits >= least) {
-                const int at = atomicAdd(&sh.n_cand, 1);
-                if (at < kSeg) sh.cand[at] = order_key(bits, v);
+            for (int i = 0; i < 4 * kVec; ++i) {
+                const int v = seg * kSeg - head + ((i >> 2) * 32 + lane) * 4 + (i & 3);
+                const unsigned bits = order_bits(c[i]);
+                if (v >= 0 && v < V && order_key(bits, v) >= least) {
+                    const int at = atomicAdd(&sh.n_cand, 1);
+                    if (at < kSeg) sh.cand[at] = order_key(bits, v);
+                }
             }
         }
+        __syncthreads();
+        if (sh.n_cand <= kSeg) break;   // always, once narrowed
+        narrow = true;
+        __syncthreads();
+        if (tid == 0) sh.n_cand = 0;
     }
-    __syncthreads();
+    // a candidate's place is the number of better ones
     const int found = sh.n_cand;
-    auto put = [&](int k, unsigned long long key) {
-        const float best = from_bits((unsigned)(key >> 32));
-        const float lse = sh.total.d;
-        a.top_ids[(size_t)r * n + k] = place_of(key);
-        a.top_logprobs[(size_t)r * n + k] =
-            sh.total.m == -INFINITY && lse == lse ? -INFINITY : (best - sh.total.m) - lse;
-    };
-    if (found <= kSeg) {
-        for (int i = tid; i < found; i += kThreads) {
-            const unsigned long long key = sh.cand[i];
-            int better = 0;
-            for (int x = 0; x < found; ++x) better += sh.cand[x] > key;
-            if (better < n) put(better, key);
+    const float lse = sh.total.d;
+    for (int i = tid; i < found; i += kThreads) {
+        const unsigned long long key = sh.cand[i];
+        int better = 0;
+        for (int x = 0; x < found; ++x) better += sh.cand[x] > key;
+        if (better < n) {
+            const float best = from_bits((unsigned)(key >> 32));
+            a.top_ids[(size_t)r * n + better] = place_of(key);
+            a.top_logprobs[(size_t)r * n + better] =
+                sh.total.m == -INFINITY && lse == lse ? -INFINITY : (best - sh.total.m) - lse;
         }
-        return;
     }
-    // More candidates than the list holds (rows in order, rows of few values): a segment at a time, the n best kept in order
-    // in the lanes of warp 0.
-    unsigned long long mine = 0;
-    for (int k = 0; k < want; ++k) {
-        __syncthreads();
-        for (int i = tid; i < kSeg; i += kThreads) {
-            const int v = sh.segs[k] * kSeg - head + i;
-            sh.cand[i] = v >= 0 && v < V ? order_key(order_bits(__ldcg(row + v)), v) : 0ull;
-        }
-        __syncthreads();
-        if (warp == 0)
-            for (int i = 0; i < kSeg; ++i) {   // insertion: later ones move a lane on
-                const unsigned long long key = sh.cand[i];
-                const unsigned long long up = __shfl_up_sync(0xffffffffu, mine, 1);
-                if (key > mine) mine = lane == 0 || up > key ? key : up;
-            }
-    }
-    if (warp == 0 && lane < n) put(lane, mine);
 }
 
 }  // namespace

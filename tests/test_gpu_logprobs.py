@@ -119,6 +119,28 @@ def test_masks_ties_and_wide_rows(vocab):
         check(z, tokens, run(ddb, z, tokens, n))
 
 
+@pytest.mark.parametrize("rows", [14, 1300])
+@pytest.mark.parametrize("vocab", [512, 513, 700, 1290, 4584, 16390])
+def test_rows_of_few_segments(rows, vocab):
+    """Vocabularies with fewer segments than alternatives, and rows in order or of few values, in both ways of sharing rows
+    out; equal logits everywhere, too."""
+    ddb = _ddb()
+    z = logits(rows, vocab, 8)
+    z[1] = torch.arange(vocab, device=DEV) * 1e-3
+    z[2] = -torch.arange(vocab, device=DEV) * 1e-3
+    z[3] = (z[3] * 2).round() / 2
+    z[4] = 0.25
+    z[5] = NEG
+    z[6, 3:] = NEG
+    z[7, : vocab // 2] = torch.finfo(torch.float32).min
+    z[8, vocab - 1] = 50.0
+    z[9, ::2] = 3.0
+    tokens = torch.randint(0, vocab, (rows,), device=DEV, generator=torch.Generator(device=DEV).manual_seed(3)).to(torch.int32)
+    for n in (1, 2, 7, 20, 32):
+        out = run(ddb, z, tokens, n)
+        check(z[:14], tokens[:14], [t[:14] for t in out])
+
+
 def test_peaked_rows_keep_small_probabilities():
     """A top logit far above the rest: its log probability and the entropy are small, and not rounded to zero."""
     ddb = _ddb()
