@@ -5,8 +5,8 @@
 // 4y + 3 and keys x, x + 16, x + 32, x + 48 of a block's scores, and columns of O: 8 scalar products' multiply-adds for
 // each 16-byte read of shared memory.  A row's maximum and sum run over its 16 threads by shuffles; O is scaled where the
 // maximum moves.  Bound by the multiply-adds and the reads that feed them; tiles are split over the CTAs and joined as
-// attn_chunk.cuh says, since a chunk of a tile takes microseconds.  2048 tokens of 8 / 2 heads of 128: 291 us (29.5 TFLOP/s);
-// 8 x 64 behind 2000, 8 / 2 heads of 64: 103; 2 x 16 behind 4: 11.4 in a graph, round trips.
+// attn_chunk.cuh says, since a chunk of a tile takes microseconds.  2048 tokens of 8 / 2 heads of 128: 276 us (31 TFLOP/s);
+// 8 x 64 behind 2000, 8 / 2 heads of 64: 100; 2 x 16 behind 4: 11 in a graph, round trips.
 #include <algorithm>
 
 #include "attn_chunk.cuh"
@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 64, kKeys = 64;
+constexpr int kGroupBlocks = 4;   // blocks of a piece from which on idle warps share its keys
 
 template <int DH>
 struct Tile {
@@ -25,7 +26,8 @@ struct Tile {
     static constexpr int OFF_K = kRows * LD;             // floats; [buffer]
     static constexpr int OFF_V = OFF_K + 2 * kKeys * LD;
     static constexpr int OFF_P = OFF_V + 2 * kKeys * DH;
-    static constexpr int OFF_SEQS = OFF_P + kRows * LDP;
+    static constexpr int OFF_IDS = OFF_P + kRows * LDP;  // [block % 4][4]: its pages, 16 rows each at least
+    static constexpr int OFF_SEQS = OFF_IDS + 16;
     static constexpr int BYTES = OFF_SEQS * 4 + (int)sizeof(ChunkSeqs);
     static constexpr int VPR = DH / 4;                   // vectors per row
     static constexpr int CPT = DH / 16;                  // columns of O per thread
@@ -54,7 +56,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
     constexpr int CPT = TL::CPT;
     extern __shared__ __align__(16) float sm[];
     ChunkSeqs& seqs = *reinterpret_cast<ChunkSeqs*>(sm + TL::OFF_SEQS);
-    const int tid = threadIdx.x, y = tid >> 4, x = tid & 15;
+    const int tid = threadIdx.x, x = tid & 15;
     ptx::griddep_wait();
     if (tid < 32) chunk_seqs(a, seqs, blockIdx.x == 0);
     __syncthreads();
@@ -66,8 +68,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
     while (walk.next(p)) {
         const int rows = (p.t1 - p.t0) * n_rep;
         const int key_end = min(p.c1 * kAttnChunk, p.kv_last + 1), blocks = (key_end - p.c0 * kAttnChunk + kKeys - 1) / kKeys;
+        // the pages of block i, looked up two blocks ahead of their copies (a look-up in front of each copy: the call
+        // 45 us, so 41.6; 1 token behind 4000, 8 heads of 128)
+        int* ids = reinterpret_cast<int*>(sm + TL::OFF_IDS);
+        auto look_up = [&](int i, int k) {
+            const int key = p.c0 * kAttnChunk + i * kKeys + (k << min(shift, 6));
+            if (k < max(kKeys >> shift, 1) && key < key_end) ids[(i & 3) * 4 + k] = max(page_of(a.pages, p.b, key >> shift, a.err), 0);
+        };
         // keys of block i into buffer i % 2; a thread's vectors: column tid % VPR of rows tid / VPR, ...
         auto copy = [&](int i) {
+            if (tid < 4) look_up(i + 2, tid);
             const int key0 = p.c0 * kAttnChunk + i * kKeys;
             float* ks = sm + TL::OFF_K + (i & 1) * kKeys * TL::LD;
             float* vs = sm + TL::OFF_V + (i & 1) * kKeys * DH;
@@ -76,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
                 const bool in = key < key_end;
                 size_t at = 0;
                 if (in) {
-                    const int id = max(page_of(a.pages, p.b, key >> shift, a.err), 0);
+                    const int id = ids[(i & 3) * 4 + (r >> shift)];   // blocks of 64 lie in one page of 64 or more
                     at = ((((size_t)id * a.n_kv_heads + p.g) << shift) + (key & ((1 << shift) - 1))) * DH + c;
                 }
                 cp_async16(ks + r * TL::LD + c, static_cast<const float*>(a.kc) + at, in);
@@ -85,6 +95,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         __syncthreads();   // the last piece's buffers are used up
+        if (tid < 8) look_up(tid >> 2, tid & 3);
+        __syncthreads();
         copy(0);
         for (int e = tid; e < kRows * TL::VPR; e += kThreads) {
             const int r = e / TL::VPR, c = e % TL::VPR * 4;
@@ -96,8 +108,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
             }
             *reinterpret_cast<float4*>(sm + r * TL::LD + c) = v;
         }
-        const bool live = 8 * (tid >> 5) < rows;
-        // this thread's rows: last key that each sees (-1: no row)
+        // 8 rows a warp; the warps that few rows leave over take a block's keys between them: group g of G the keys
+        // 64 g / G .. of every block, each group with a softmax of its own, joined at the end (1 token behind 4000, 8 heads of
+        // 128: 41.6 -> 32.4 us; joining costs 2 us, so not for few blocks)
+        const int groups = blocks < kGroupBlocks ? 1 : rows <= 16 ? 4 : rows <= 32 ? 2 : 1, warps = 8 / groups;
+        const int group = (tid >> 5) / warps, y = 2 * ((tid >> 5) % warps) + (tid >> 4 & 1);
+        const bool live = 8 * (y >> 1) < rows;
+        // this thread's rows 4y .. 4y + 3: last key that each sees (-1: no row)
         int last[4];
         float m[4], l[4], o[4][CPT];
 #pragma unroll
@@ -124,77 +141,121 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
                 __syncthreads();
                 continue;
             }
-            float s[4][4] = {};
+            auto block = [&](auto of) {   // JN times 16 keys
+                constexpr int JN = decltype(of)::value;
+                const int j0 = group * JN;
+                float s[4][JN] = {};
 #pragma unroll 4
-            for (int d = 0; d < DH; d += 4) {
-                float4 q[4], k[4];
+                for (int d = 0; d < DH; d += 4) {
+                    float4 q[4], k[JN];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sm + (4 * y + i) * TL::LD + d);
+                    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sm + (4 * y + i) * TL::LD + d);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(ks + (x + 16 * j) * TL::LD + d);
+                    for (int j = 0; j < JN; ++j) k[j] = *reinterpret_cast<const float4*>(ks + (x + 16 * (j0 + j)) * TL::LD + d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[i][j] = __fmaf_rn(q[i].w, k[j].w, __fmaf_rn(q[i].z, k[j].z, __fmaf_rn(q[i].y, k[j].y, __fmaf_rn(q[i].x, k[j].x, s[i][j]))));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    s[i][j] = key0 + x + 16 * j <= last[i] ? s[i][j] * a.scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, s[i][j]);
+                        for (int j = 0; j < JN; ++j)
+                            s[i][j] = __fmaf_rn(q[i].w, k[j].w, __fmaf_rn(q[i].z, k[j].z, __fmaf_rn(q[i].y, k[j].y, __fmaf_rn(q[i].x, k[j].x, s[i][j]))));
                 }
-                const float mn = fmaxf(m[i], row_max(mx)), ref = mn == -INFINITY ? 0.f : mn;
-                const float c = exp2f(m[i] - ref);   // m = -inf: 0
-                float sum = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float w = key0 + x + 16 * j <= last[i] ? exp2f(s[i][j] - ref) : 0.f;
-                    sm[TL::OFF_P + (4 * y + i) * TL::LDP + x + 16 * j] = w;
-                    sum += w;
+                for (int i = 0; i < 4; ++i) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < JN; ++j) {
+                        s[i][j] = key0 + x + 16 * (j0 + j) <= last[i] ? s[i][j] * a.scale_log2 : -INFINITY;
+                        mx = fmaxf(mx, s[i][j]);
+                    }
+                    const float mn = fmaxf(m[i], row_max(mx)), ref = mn == -INFINITY ? 0.f : mn;
+                    const float c = exp2f(m[i] - ref);   // m = -inf: 0
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < JN; ++j) {
+                        const float w = key0 + x + 16 * (j0 + j) <= last[i] ? exp2f(s[i][j] - ref) : 0.f;
+                        sm[TL::OFF_P + (4 * y + i) * TL::LDP + x + 16 * (j0 + j)] = w;
+                        sum += w;
+                    }
+                    l[i] = __fmaf_rn(l[i], c, row_sum(sum));
+                    m[i] = mn;
+#pragma unroll
+                    for (int e = 0; e < CPT; ++e) o[i][e] *= c;
                 }
-                l[i] = __fmaf_rn(l[i], c, row_sum(sum));
-                m[i] = mn;
-#pragma unroll
-                for (int e = 0; e < CPT; ++e) o[i][e] *= c;
-            }
-            __syncwarp();   // a warp's rows of P are its own
-            // a row does not see what lies behind it, infinities and NaN included: such products are left out
-            const bool all = key0 + kKeys - 1 <= p.pos0 && rows == kRows;
-            auto average = [&](auto masked) {
-                constexpr bool kMasked = decltype(masked)::value;
-                const int n_keys = kMasked ? min(kKeys, key_end - key0) : kKeys;   // 20 keys: the call 12.8 -> 11.4 us
+                __syncwarp();   // a warp's rows of P are its own
+                // a row does not see what lies behind it, infinities and NaN included: such products are left out
+                const bool all = key0 + kKeys - 1 <= p.pos0;
+                auto average = [&](auto masked) {
+                    constexpr bool kMasked = decltype(masked)::value;
+                    // (20 keys: the call 12.8 -> 11.4 us)
+                    const int k1 = kMasked ? min(16 * (j0 + JN), key_end - key0) : 16 * (j0 + JN);
 #pragma unroll 2
-                for (int k = 0; k < n_keys; k += 4) {
-                    float4 w[4];
+                    for (int k = 16 * j0; k < k1; k += 4) {
+                        float4 w[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sm + TL::OFF_P + (4 * y + i) * TL::LDP + k);
+                        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(sm + TL::OFF_P + (4 * y + i) * TL::LDP + k);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        float v[CPT];
-                        if constexpr (CPT >= 4) {
+                        for (int kk = 0; kk < 4; ++kk) {
+                            float v[CPT];
+                            if constexpr (CPT >= 4) {
 #pragma unroll
-                            for (int e = 0; e < CPT; e += 4)   // columns 4x .. 4x + 3 of each 64
-                                *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(vs + (k + kk) * DH + e * 16 + 4 * x);
-                        } else {
-                            *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(vs + (k + kk) * DH + 2 * x);
-                        }
+                                for (int e = 0; e < CPT; e += 4)   // columns 4x .. 4x + 3 of each 64
+                                    *reinterpret_cast<float4*>(v + e) = *reinterpret_cast<const float4*>(vs + (k + kk) * DH + e * 16 + 4 * x);
+                            } else {
+                                *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(vs + (k + kk) * DH + 2 * x);
+                            }
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float wi = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
-                            const bool sees = !kMasked || key0 + k + kk <= last[i];
+                            for (int i = 0; i < 4; ++i) {
+                                const float wi = kk == 0 ? w[i].x : kk == 1 ? w[i].y : kk == 2 ? w[i].z : w[i].w;
+                                const bool sees = !kMasked || key0 + k + kk <= last[i];
 #pragma unroll
-                            for (int e = 0; e < CPT; ++e)
-                                if (sees) o[i][e] = __fmaf_rn(wi, v[e], o[i][e]);
+                                for (int e = 0; e < CPT; ++e)
+                                    if (sees) o[i][e] = __fmaf_rn(wi, v[e], o[i][e]);
+                            }
                         }
                     }
-                }
+                };
+                if (all) average(std::false_type{});
+                else average(std::true_type{});
             };
-            if (all) average(std::false_type{});
-            else average(std::true_type{});
+            if (groups == 1) block(std::integral_constant<int, 4>{});
+            else if (groups == 2) block(std::integral_constant<int, 2>{});
+            else block(std::integral_constant<int, 1>{});
             __syncthreads();   // the buffer may be filled again
+        }
+        if (groups > 1) {
+            // [group][row] m, l and o, over K's buffers (as many values as one holds): group 0 joins
+            float* os = sm + TL::OFF_K;
+            float2* mls = reinterpret_cast<float2*>(sm + TL::OFF_P);
+            const int per = kRows / groups;
+            auto column = [&](int e) { return CPT >= 4 ? (e >> 2) * 64 + 4 * x + (e & 3) : 2 * x + e; };
+            if (live && group > 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (x == 0) mls[group * per + 4 * y + i] = make_float2(m[i], l[i]);
+#pragma unroll
+                    for (int e = 0; e < CPT; ++e) os[(group * per + 4 * y + i) * DH + column(e)] = o[i][e];
+                }
+            }
+            __syncthreads();
+            if (group > 0) continue;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (4 * y + i >= rows) break;
+                float M = m[i];
+                for (int g = 1; g < groups; ++g) M = fmaxf(M, mls[g * per + 4 * y + i].x);
+                // m = -inf: 0 (a NaN in l or o stays)
+                float c = m[i] == -INFINITY ? 0.f : exp2f(m[i] - M);
+                l[i] *= c;
+#pragma unroll
+                for (int e = 0; e < CPT; ++e) o[i][e] *= c;
+                for (int g = 1; g < groups; ++g) {
+                    const float2 ml = mls[g * per + 4 * y + i];
+                    c = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+                    l[i] = __fmaf_rn(ml.y, c, l[i]);
+#pragma unroll
+                    for (int e = 0; e < CPT; ++e) o[i][e] = __fmaf_rn(os[(g * per + 4 * y + i) * DH + column(e)], c, o[i][e]);
+                }
+                m[i] = M;
+            }
         }
         const bool split = p.c1 - p.c0 < p.n;
         const int slot = 2 * blockIdx.x + (p.c0 == 0);

@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (split) {
                     if (valid && ok) a.part_ml[(2 * slot + half) * 128 + row] = x;
                 } else {
-                    const float inv = 1.f / x.y;   // no key above -inf: 0 * infinity
+                    const float inv = __fdividef(1.f, x.y);   // no key above -inf: 0 * infinity
                     w0 *= inv;
                     w1 *= inv;
                 }
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else {
                         ptx::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= w0;
+                        for (int e = 0; e < 32; e += 2) unpack2(mul2(pack2(o[e], o[e + 1]), pack2(w0, w0)), o[e], o[e + 1]);
                     }
                     if (!valid || !ok) {
                     } else if (split) {
