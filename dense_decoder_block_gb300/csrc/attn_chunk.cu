@@ -18,7 +18,7 @@ bool heads_ok(int n_heads, int n_kv_heads, int head_dim) {
 }
 
 // two partials (m, l, o) of up to 256 rows for each CTA where tiles may be split
-size_t partial_rows(int max_pos) { return max_pos < kNeverSplit ? 0 : (size_t)kChunkMaxCtas * 512; }
+size_t partial_rows(int max_pos) { return max_pos < kNeverSplit ? 0 : kPartialRows; }
 size_t partial_bytes(int head_dim, int max_pos) { return partial_rows(max_pos) * (head_dim + 2) * sizeof(float); }
 
 }  // namespace
@@ -29,7 +29,7 @@ size_t attn_chunk_workspace_bytes(int head_dim, int max_pos) {
 }
 
 int attn_chunk_launches(const AttnArgs& a) {
-    return (a.batch + kChunkSeqs - 1) / kChunkSeqs * (device_sm_count() == 1 || a.max_pos < kNeverSplit ? 1 : 2);
+    return (a.batch + kTcSeqs - 1) / kTcSeqs * (device_sm_count() == 1 || a.max_pos < kNeverSplit ? 1 : 2);
 }
 
 cudaError_t launch_attention_chunk(const AttnArgs& a, const int* start, const int* count, void* ws, cudaStream_t s) {

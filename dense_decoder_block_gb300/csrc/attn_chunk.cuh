@@ -12,14 +12,18 @@
 //     tile that crosses the end of a stretch is shared by several CTAs, each of which leaves the softmax
 //     partial (m, l, o) of its chunks, and a second kernel joins them.
 #pragma once
+#include <algorithm>
+
 #include "common.cuh"
 #include "paged.cuh"
 #include "ptx.cuh"
 
 namespace llama {
 
-constexpr int kChunkSeqs = 1024;      // sequences of a launch
-constexpr int kChunkMaxCtas = 152;    // CTAs of a launch: two partials each (workspace)
+// Sequences and CTAs of a launch; each CTA leaves two partials at most (workspace), of 256 rows and of 64
+constexpr int kTcSeqs = 1024, kTcCtas = 152, kF32Seqs = 256, kF32Ctas = 304;
+constexpr int kChunkMaxCtas = std::max(kTcCtas, kF32Ctas);
+constexpr int kPartialRows = 2 * std::max(kTcCtas * 256, kF32Ctas * 64);
 
 struct ChunkArgs {
     const void* q;       // [batch, tokens, n_heads, head_dim]
@@ -34,6 +38,7 @@ struct ChunkArgs {
     int tq;              // tokens per tile
     int join_keys;       // work (keys) per CTA that the partials and their joining cost
     int min_stretch;     // the least work of a CTA (keys) for which tiles are split
+    float pieces;        // ... and the pieces of a tile of c chunks, at most: pieces * sqrt(c)
     float* partial;      // [2 CTAs][halves of a tile][head_dim / 4][rows of a half] float4
     float2* part_ml;     // [2 CTAs][halves][rows]
     int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it ...
@@ -58,11 +63,13 @@ constexpr int kRounds = 4;
 // 39); a lane holds kSortSeqs / 32 sequences.
 constexpr int kSortSeqs = 64;
 
-// The sequences of a launch (shared memory).
+// The sequences of a launch, N at most (shared memory).
+template <int N>
 struct ChunkSeqs {
-    long long pre[kChunkSeqs + 1];   // work of the sequences before, one KV head
-    int start[kChunkSeqs], count[kChunkSeqs];
-    int tiles[kChunkSeqs + 1];       // tiles of the sequences before, one KV head
+    static constexpr int kMost = N;
+    long long pre[N + 1];   // work of the sequences before, one KV head
+    int start[N], count[N];
+    int tiles[N + 1];       // tiles of the sequences before, one KV head
 };
 
 // Work of the first n tiles (all of tq tokens) of a sequence.
@@ -71,7 +78,8 @@ __device__ __forceinline__ long long tiles_work(int start, int tq, int n) {
 }
 
 // Fills s (one warp).  A sequence whose words are out of range has no tile; `record`: it is recorded.
-__device__ __forceinline__ void chunk_seqs(const ChunkArgs& a, ChunkSeqs& s, bool record) {
+template <class Seqs>
+__device__ __forceinline__ void chunk_seqs(const ChunkArgs& a, Seqs& s, bool record) {
     const int lane = threadIdx.x & 31;
     long long run = 0;
     int run_tiles = 0;
@@ -147,8 +155,9 @@ __device__ __forceinline__ int last_that(int n, Pred pred) {
 
 // A CTA's pieces in order.  The whole warp walks: the CTA waits for the first piece, and one lane's 64-bit divisions
 // and bisections took 2.5 us of it.
+template <class Seqs>
 struct ChunkWalk {
-    const ChunkSeqs& s;
+    const Seqs& s;
     int batch, n_kv, tq, cta, n_ctas;
     bool rounds, sorted;
     int j;                 // rounds: the next one
@@ -159,7 +168,7 @@ struct ChunkWalk {
     long long w, w0, w1;   // beginning of the tile at hand, the stretch
     int b, g, y, n_qt, start, count;
 
-    __device__ __forceinline__ ChunkWalk(const ChunkArgs& a, const ChunkSeqs& seqs, int cta_, int n_ctas_)
+    __device__ __forceinline__ ChunkWalk(const ChunkArgs& a, const Seqs& seqs, int cta_, int n_ctas_)
         : s(seqs), batch(a.batch), n_kv(a.n_kv_heads), tq(a.tq), cta(cta_), n_ctas(n_ctas_) {
         const long long total = s.pre[batch] * n_kv;
         b = batch;
@@ -195,7 +204,12 @@ struct ChunkWalk {
             shortest = __reduce_min_sync(0xffffffffu, shortest);
         }
         if (rounds) return;
-        const int n = min(n_ctas, max(tiles, (int)__fdividef((float)total, (float)a.min_stretch)));
+        // The join takes a tile's pieces a batch at a time, a round trip each: p pieces of c / p chunks and their joining take
+        // the least time at a p that grows with the root of c (4 tokens of one KV head behind 32768, bf16: split over all CTAs
+        // 31 us, so 25; behind 131072 58 and 43; fp32 58 and 50)
+        const float work = __fdividef((float)total, (float)a.min_stretch);
+        const float most = a.pieces * sqrtf((float)total * (float)max(tiles, 1) * (1.f / kAttnChunk));
+        const int n = min(n_ctas, max(tiles, (int)fminf(work, most)));
         if (cta >= n || total == 0) return;
         // every CTA has the same `each`, whatever its last bits
         const long long each = (long long)__fdividef((float)total, (float)n);
@@ -358,12 +372,12 @@ template <typename T, int DH, int HALVES, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArgs a, int n_ctas) {
     __shared__ int4 s_cut[kChunkMaxCtas];
     __shared__ int s_tokens[kChunkMaxCtas];
-    __shared__ unsigned s_word[8];   // bit i: the first CTA that begins inside its tile is CTA i
-    static_assert(kChunkMaxCtas <= 2 * kJoinThreads && kJoinThreads == 128, "two CTAs a thread, words of 32");
+    constexpr int kEach = (kChunkMaxCtas + kJoinThreads - 1) / kJoinThreads, kWords = kEach * (kJoinThreads / 32);
+    __shared__ unsigned s_word[kWords];   // bit i: the first CTA that begins inside its tile is CTA i
     auto same_tile = [](const int4& c, const int4& d) { return c.x == d.x && c.y == d.y && c.z == d.z; };
     ptx::griddep_wait();
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kEach; ++x) {
         const int i = x * kJoinThreads + threadIdx.x;
         bool first = false;
         if (i < n_ctas) {
@@ -378,7 +392,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArg
     __syncthreads();
     int n_split = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) n_split += __popc(s_word[w]);
+    for (int w = 0; w < kWords; ++w) n_split += __popc(s_word[w]);
     // CTA j begins inside the tile that CTA i begins inside of
     auto same = [&](int i, int j) { return s_cut[j].w > 0 && same_tile(s_cut[i], s_cut[j]); };
     constexpr int kCols = DH / kJoinCols, kSets = kJoinThreads / ROWS;   // column groups; of an item

@@ -28,9 +28,11 @@ struct Tile {
     static constexpr int OFF_P = OFF_V + 2 * kKeys * DH;
     static constexpr int OFF_IDS = OFF_P + kRows * LDP;  // [block % 4][4]: its pages, 16 rows each at least
     static constexpr int OFF_SEQS = OFF_IDS + 16;
-    static constexpr int BYTES = OFF_SEQS * 4 + (int)sizeof(ChunkSeqs);
+    static constexpr int BYTES = OFF_SEQS * 4 + (int)sizeof(ChunkSeqs<kF32Seqs>);
     static constexpr int VPR = DH / 4;                   // vectors per row
     static constexpr int CPT = DH / 16;                  // columns of O per thread
+    // per SM: two where shared memory has room for them (244 tokens behind 34056, 4 / 2 heads of 64: 318 us with one, 276)
+    static constexpr int CTAS = DH <= 64 ? 2 : 1;
 };
 
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem, bool valid) {
@@ -51,11 +53,12 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 template <int DH>
-__global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs a) {
+__global__ void __launch_bounds__(kThreads, Tile<DH>::CTAS) k_attn_chunk_f32(const ChunkArgs a) {
     using TL = Tile<DH>;
     constexpr int CPT = TL::CPT;
     extern __shared__ __align__(16) float sm[];
-    ChunkSeqs& seqs = *reinterpret_cast<ChunkSeqs*>(sm + TL::OFF_SEQS);
+    using Seqs = ChunkSeqs<kF32Seqs>;
+    Seqs& seqs = *reinterpret_cast<Seqs*>(sm + TL::OFF_SEQS);
     const int tid = threadIdx.x, x = tid & 15;
     ptx::griddep_wait();
     if (tid < 32) chunk_seqs(a, seqs, blockIdx.x == 0);
@@ -284,15 +287,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_chunk_f32(const ChunkArgs 
 
 template <int DH>
 cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
+    using TL = Tile<DH>;
     const auto kern = k_attn_chunk_f32<DH>;
     cudaError_t r = kernel_setup_once((const void*)kern, [](const void* k) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<DH>::BYTES);
     });
     if (r != cudaSuccess) return r;
-    for (int b0 = 0; b0 < a.batch; b0 += kChunkSeqs) {
+    for (int b0 = 0; b0 < a.batch; b0 += kF32Seqs) {
         ChunkArgs k = a;
         const size_t at = (size_t)b0 * a.tokens * a.n_heads * DH;
-        k.batch = std::min(a.batch - b0, kChunkSeqs);
+        k.batch = std::min(a.batch - b0, kF32Seqs);
         k.q = static_cast<const float*>(a.q) + at;
         k.o = static_cast<float*>(a.o) + at;
         k.start += b0;
@@ -301,7 +305,8 @@ cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
         k.tq = kRows / (a.n_heads / a.n_kv_heads);
         k.join_keys = 64;
         k.min_stretch = 256;
-        const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kChunkMaxCtas);
+        k.pieces = 4.f;
+        const unsigned n_ctas = (unsigned)std::min(device_sm_count() * TL::CTAS, kF32Ctas);
         r = launch_pdl(kern, dim3(n_ctas), dim3(kThreads), Tile<DH>::BYTES, s, k);
         if (r != cudaSuccess) return r;
         if (n_ctas == 1 || a.max_pos < kNeverSplit) continue;

@@ -48,7 +48,8 @@ constexpr int OFF_BAR = OFF_V + 4 * kSub;
 constexpr int OFF_PIECES = OFF_BAR + 512;     // the ring of pieces, and a word for each
 constexpr int OFF_ML = OFF_PIECES + 256;      // [parity][stream][128] (m, l): see ml_full
 constexpr int OFF_SEQS = OFF_ML + 4096;
-constexpr int SMEM_BYTES = OFF_SEQS + (int)sizeof(ChunkSeqs) + 1024;
+using Seqs = ChunkSeqs<kTcSeqs>;                 // of a launch
+constexpr int SMEM_BYTES = OFF_SEQS + (int)sizeof(Seqs) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
 constexpr int TM_S = 0, TM_O = 256;           // + 128 per stream
 
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_holder = (uint32_t*)(bars + 37);
     ChunkPiece* pieces = (ChunkPiece*)(sm + OFF_PIECES);
     int* poison = (int*)(sm + OFF_PIECES + kRing * sizeof(ChunkPiece));   // [4] j + 1: care was taken of piece j's V
-    ChunkSeqs& seqs = *reinterpret_cast<ChunkSeqs*>(sm + OFF_SEQS);
+    Seqs& seqs = *reinterpret_cast<Seqs*>(sm + OFF_SEQS);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform
     ptx::griddep_wait();   // lengths, tables, rows: whatever the stream holds in front
@@ -645,10 +646,10 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     });
     if (r != cudaSuccess) return r;
-    for (int b0 = 0; b0 < a.batch; b0 += kChunkSeqs) {
+    for (int b0 = 0; b0 < a.batch; b0 += kTcSeqs) {
         ChunkArgs k = a;
         const size_t at = (size_t)b0 * a.tokens * a.n_heads * 128;
-        k.batch = std::min(a.batch - b0, kChunkSeqs);
+        k.batch = std::min(a.batch - b0, kTcSeqs);
         k.q = static_cast<const bf16*>(a.q) + at;
         k.o = static_cast<bf16*>(a.o) + at;
         k.start += b0;
@@ -657,9 +658,10 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
         k.tq = 2 * (128 / n_rep);
         k.join_keys = 768;
         k.min_stretch = 512;
+        k.pieces = 2.f;
         if (!make_tmap_q3d(&mq, k.q, a.n_heads, k.batch * a.tokens, n_rep, k.tq / 2)) return cudaErrorInvalidValue;
         // persistent: one CTA per SM at most (work assigned on the device)
-        const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kChunkMaxCtas);
+        const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kTcCtas);
         r = launch_pdl(k_attn_chunk, dim3(n_ctas), dim3(kThreads), SMEM_BYTES, s, mq, mk, mv, k);
         if (r != cudaSuccess) return r;
         if (n_ctas == 1 || a.max_pos < kNeverSplit) continue;
