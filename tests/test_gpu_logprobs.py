@@ -120,7 +120,7 @@ def test_masks_ties_and_wide_rows(vocab):
 
 
 @pytest.mark.parametrize("rows", [14, 1300])
-@pytest.mark.parametrize("vocab", [512, 513, 700, 1290, 4584, 16390])
+@pytest.mark.parametrize("vocab", [161, 250, 257, 512, 513, 700, 1290, 4584, 16390])
 def test_rows_of_few_segments(rows, vocab):
     """Vocabularies with fewer segments than alternatives, and rows in order or of few values, in both ways of sharing rows
     out; equal logits everywhere, too."""
