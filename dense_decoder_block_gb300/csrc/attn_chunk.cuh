@@ -208,7 +208,9 @@ struct ChunkWalk {
         // the least time at a p that grows with the root of c (4 tokens of one KV head behind 32768, bf16: split over all CTAs
         // 31 us, so 25; behind 131072 58 and 43; fp32 58 and 50)
         const float work = __fdividef((float)total, (float)a.min_stretch);
-        const float most = a.pieces * sqrtf((float)total * (float)max(tiles, 1) * (1.f / kAttnChunk));
+        float most;   // (with sqrtf, whose code is longer, the bf16 kernel's 8192 tokens took 374 us, so 356)
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(most) : "f"((float)total * (float)tiles * (1.f / kAttnChunk)));
+        most *= a.pieces;
         const int n = min(n_ctas, max(tiles, (int)fminf(work, most)));
         if (cta >= n || total == 0) return;
         // every CTA has the same `each`, whatever its last bits
