@@ -407,8 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_wait_ld();
                     if (!__all_sync(0xffffffffu, last_key >= kAttnChunk - 1)) {
 #pragma unroll
-                        for (int e = 0; e < 128; ++e)
-                            if (e > last_key) v[e] = -INFINITY;
+                        for (int e0 = 0; e0 < 128; e0 += 32) {   // words of what is seen: bit e of the word is key e0 + e
+                            const int over = 31 - (last_key - e0);
+                            const uint32_t seen = over > 31 ? 0u : over <= 0 ? 0xffffffffu : 0xffffffffu >> over;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) v[e0 + e] = -INFINITY;
+                        }
                     }
                     float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
