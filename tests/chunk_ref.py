@@ -65,8 +65,11 @@ def token_logprobs(z, token, n_top):
 def logprob_tol(lp, z, V):
     """How far a log probability may be off: x = z - max is rounded once (2^-24 |x|, for the token and as an exponent);
     an exponential is off by 2^-22 relative at most beside that of its exponent, which is at most 2^-24 times 104 where
-    the exponential is not 0 in fp32; a thread's fp32 sum of n terms by n 2^-24 relative (n <= ceil(V / 256) + 32); the
-    rest is held in fp64 and rounded once."""
+    the exponential is not 0 in fp32.  The sums are held in fp32, all terms of one sign, and are off by 2^-24 relative for
+    each addition or product on the way of a term: a lane takes 16 logits of a segment of 512 in 5, and moves and adds
+    its sums in 4 a segment, of which it has ceil(V / 2048) + 1 at most (4 warps a row); 5 additions over a warp; 4 in
+    each of 9 joins at most, of which only those of two parts with terms round: 2, 5 and 9 up to 3, 18 and more segments.
+    That is at most 22 below 1024 logits, V / 512 + 38 below 9216 and V / 512 + 54 from there: below V / 256 + 36."""
     rel = (104 + 4 + ceil_div(V, 256) + 32) * U
     return rel + U * np.abs(z - np.max(z)) + U * np.abs(lp)
 
