@@ -3,7 +3,9 @@
 // A tile is 256 query rows of a KV group (two halves of tqh tokens x the group's heads, 128 rows each), its keys come
 // in chunks of 128:
 //   S = Q K^T     tcgen05.mma M = N = K = 128, operands in shared memory
-//   softmax       thread = row: a running reference m of the row (log2 domain), p = 2^(s c - m) rounded to bf16, l += p.
+//   softmax       thread = row: a running reference m of the row (log2 domain), p = 2^(s c - m) rounded to bf16, l += the
+//                 rounded p (in fp32), so that a weight's rounding goes to O and l alike: where one key outweighs the
+//                 others, or the heavy ones hold one value, the row is that value.
 //                 m follows the row's maximum only when that has grown by more than 2^kSlack, so O is
 //                 seldom scaled (p <= 2^kSlack; nothing is lost, bf16 and fp32 keep their relative precision)
 //   O += P V      tcgen05.mma, P from tensor memory, O accumulated in tensor memory
@@ -398,6 +400,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; left > 0; --left, ++step, last_key -= ahead) {
                 if (ok) ok = ptx::mbar_wait(&s_full[s], step & 1, err);
                 ptx::tc_fence_after();
+                uint32_t weights[8][8];   // two rounded weights each
+                float sc = 1.f;
                 if (live) {
                     float v[128];
                     ptx::tmem_ld<32>(s_taddr, v);
@@ -424,7 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], v[124 + x]);
                     const float mn = fmaxf(m, __fmul_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), c));
-                    float sc = 1.f;
                     if (mn != m && !(mn - m <= kSlack)) {
                         sc = ex2(m - mn);
                         m = mn;
@@ -443,10 +446,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
                     const uint64_t c2 = pack2(c, c), nm2 = pack2(-ref, -ref);
-                    uint64_t sum0 = pack2(0.f, 0.f), sum1 = sum0;
 #pragma unroll
                     for (int e0 = 0; e0 < 128; e0 += 16) {
-                        uint32_t packed[8];
+                        uint32_t (&packed)[8] = weights[e0 / 16];
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             float x0, x1, x2, x3;
@@ -456,8 +458,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             x1 = ex2(x1);
                             x2 = ex2(x2);
                             x3 = ex2(x3);
-                            sum0 = add2(sum0, pack2(x0, x1));
-                            sum1 = add2(sum1, pack2(x2, x3));
                             const __nv_bfloat162 p0 = __floats2bfloat162_rn(x0, x1), p1 = __floats2bfloat162_rn(x2, x3);
                             packed[e / 2] = *reinterpret_cast<const uint32_t*>(&p0);
                             packed[e / 2 + 1] = *reinterpret_cast<const uint32_t*>(&p1);
@@ -470,9 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (lane == 0) ptx::mbar_arrive(&p_half[s]);
                         }
                     }
-                    float a0, a1;
-                    unpack2(add2(sum0, sum1), a0, a1);
-                    l = __fmaf_rn(l, sc, a0 + a1);
                     ptx::tmem_wait_st();
                 } else if (lane == 0) {
                     ptx::mbar_arrive(&p_half[s]);
@@ -480,6 +477,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&p_full[s]);
+                // The rounded weights are summed while the MMAs have them (in front of the hand-over: 8192 tokens of 32 / 8
+                // heads, 16-row pages 433 us, so 382; 4096 of 64 behind 4096 580 and 514).
+                if (live) {
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) {
+                        const uint32_t w0 = weights[e / 8][e % 8], w1 = weights[e / 8][e % 8 + 1];
+                        sum[0] = add_bf16_lo(w0, sum[0]);
+                        sum[1] = add_bf16_hi(w0, sum[1]);
+                        sum[2] = add_bf16_lo(w1, sum[2]);
+                        sum[3] = add_bf16_hi(w1, sum[3]);
+                    }
+                    l = __fmaf_rn(l, sc, (sum[0] + sum[2]) + (sum[1] + sum[3]));
+                }
             }
             if (steps > 0) {
                 reinterpret_cast<float2*>(sm + OFF_ML)[(took * 2 + s) * 128 + row] = make_float2(m, l);
