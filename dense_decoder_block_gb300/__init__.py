@@ -403,7 +403,8 @@ def llama_paged_plan(start, count, page_size: int, n_pages: int, free_pages, poo
 
 def llama_paged_release(start, count, page_size: int, n_pages: int, free_pages, pool, table, pool_out=None,
                         err_dev=None, stream=None) -> None:
-    """The pages that a plan with the same start and count took go back on the stack."""
+    """The pages that a plan with the same start and count took go back on the stack (pages that llama_paged_fork shared
+    are given up with llama_paged_free instead)."""
     dev = torch.cuda.current_device()
     batch = start.numel()
     if count.numel() != batch:
@@ -490,7 +491,8 @@ def llama_paged_fork_workspace_bytes(n) -> int:
 def llama_paged_fork(src, dst, lens, refs, free_pages, pool, table, caches: PagedCacheList, ws, pool_out=None,
                      err_dev=None, stream=None) -> None:
     """Row dst[i] of table continues the first lens[i] positions of row src[i]: full pages are shared (refs [n_pages]
-    counts the further holders of each), the unfilled one is copied to a page from the stack, in every layer."""
+    counts the further holders of each), the unfilled one is copied to a page from the stack, in every layer.  Shared
+    pages are given up with llama_paged_free, not llama_paged_release, and not written or reordered."""
     f = caches.first
     dev = f.device
     n = src.numel()
@@ -557,7 +559,8 @@ def llama_beam_select(logits, scores, beams: int, n_out: int, parents, tokens, o
 
 
 def llama_beam_reorder(parents, beams: int, lens, table, caches: PagedCacheList, err_dev=None, stream=None) -> None:
-    """Rows of table, and the unfilled last pages of every layer's cache, follow parents [groups * beams] in place."""
+    """Rows of table, and the unfilled last pages of every layer's cache, follow parents [groups * beams] in place (not
+    for rows with pages that llama_paged_fork shared: no counts move)."""
     f = caches.first
     dev = f.device
     rows = parents.numel()

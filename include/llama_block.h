@@ -400,8 +400,11 @@ int llama_paged_plan(const int32_t* start, const int32_t* count, int batch, int 
  * has n_pages entries).  start = 0 and count = the length gives back all pages of
  * a request.  Nothing is given back when the stack has no room for all of them
  * (LLAMA_ERR_NO_PAGES); a request out of range is left out (LLAMA_ERR_POS_RANGE).
- * Every page is released once: pages that several rows share (beams) are released
- * through the row that planned them. */
+ * Every page is released once: pages that the beams of a llama_beam_reorder share are
+ * released through the row that planned them.  Pages that llama_paged_fork shared are
+ * not released here (no count is read: other rows may still hold them) but given up
+ * with llama_paged_free; the pages of such rows behind the shared ones may be released
+ * (drafts that were rejected). */
 int llama_paged_release(const int32_t* start, const int32_t* count, int batch, int page_size, int n_pages,
                         int32_t* free_pages, const int32_t* pool, int32_t* pool_out, const int32_t* table,
                         int table_stride, int32_t* err_dev, void* stream);
@@ -490,7 +493,15 @@ int llama_block_prefill_paged(llama_block blk, const void* x, int batch, int tok
                               void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Samples of one prompt share its pages.  refs [n_pages] counts, for each page, the rows
- * that hold it beside the first: all zeros at first, and of no concern to the calls above.
+ * that hold it beside the first: all zeros at first.  Only the two calls below read or
+ * write it.  From a fork on, therefore, the full pages of its first lens[i] positions are,
+ * in both of its rows,
+ *   - given up with llama_paged_free alone: llama_paged_release would hand a page out
+ *     again that other rows still read;
+ *   - not written (a plan of either row starts behind them);
+ *   - not in rows that go through llama_beam_reorder, which moves table entries and
+ *     counts nothing.
+ * No call can tell when this is broken.  All other pages of the rows are as before.
  *
  * Fork i (of n): row dst[i] of table [table_rows, table_stride] continues the first lens[i]
  * positions of row src[i], c = lens / page_size full pages and r = lens % page_size rows of
@@ -561,7 +572,8 @@ int llama_beam_select(const float* logits, int groups, int beams, int vocab, con
  * its parent (beams share full pages, which are not written again); if r > 0, rows
  * 0 .. r-1 of page table[i][c] become those of the parent's page, in the caches of
  * all n_layers (1 .. 128; distinct buffers of one n_pages and page_size).  Entries
- * from c on stay: they are the row's own pages.  A group whose parents lie outside
+ * from c on stay: they are the row's own pages.  No counts move: not for rows with pages
+ * that llama_paged_fork shared.  A group whose parents lie outside
  * it, whose lengths differ or exceed the table, or whose rows share the page to be
  * filled is left as it was (LLAMA_ERR_INVALID_ARG in err_dev).  beams <= 32. */
 int llama_beam_reorder(const int32_t* parents, int groups, int beams, const int32_t* lens, int32_t* table,
