@@ -413,10 +413,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArg
         // piece k of end - i + 1: CTA i - 1's last, then the first ones of CTAs i, i + 1, ...; a piece is empty where the
         // next begins at the same chunk
         auto slot_of = [&](int k) { return k == 0 ? 2 * (i - 1) + 1 : 2 * (i + k - 1); };
-        auto ml_of = [&](int k) {
+        auto is_empty = [&](int k) {
             const int j = i + k - 1;
-            if (k > 0 && j + 1 < end && s_cut[j + 1].w == s_cut[j].w) return make_float2(-INFINITY, 0.f);
-            return __ldcg(a.part_ml + (HALVES * slot_of(k) + half) * ROWS + row);
+            return k > 0 && j + 1 < end && s_cut[j + 1].w == s_cut[j].w;
         };
         const int n = end - i + 1;
         float M = -INFINITY, L = 0.f;
@@ -429,7 +428,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArg
 #pragma unroll
             for (int x = 0; x < kJoinBatch; ++x) {
                 if (k0 + x >= n) break;
-                ml[x] = ml_of(k0 + x);
+                ml[x] = __ldcg(a.part_ml + (HALVES * slot_of(k0 + x) + half) * ROWS + row);
                 const float4* part =
                     reinterpret_cast<const float4*>(a.partial + (size_t)(HALVES * slot_of(k0 + x) + half) * (ROWS * DH)) + row;
 #pragma unroll
@@ -438,9 +437,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_chunk_join(const ChunkArg
 #pragma unroll
             for (int x = 0; x < kJoinBatch; ++x) {
                 if (k0 + x >= n) break;
-                if (ml[x].x == -INFINITY && ml[x].y == 0.f) continue;   // nothing (or an empty piece: its part is not written)
+                if (is_empty(k0 + x)) continue;   // its part is not written
+                // a piece without a key above -inf has no weight; 0 times an infinity or a NaN among its values is NaN
                 const float Mn = fmaxf(M, ml[x].x);
-                const float c = M == -INFINITY ? 0.f : exp2f(M - Mn), w = exp2f(ml[x].x - Mn);
+                const float c = M == -INFINITY ? 0.f : exp2f(M - Mn), w = ml[x].x == -INFINITY ? 0.f : exp2f(ml[x].x - Mn);
                 M = Mn;
                 L = fmaf(L, c, ml[x].y * w);
 #pragma unroll
