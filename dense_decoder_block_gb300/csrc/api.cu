@@ -640,8 +640,15 @@ extern "C" int llama_block_decode_paged(llama_block b, const void* x, int batch,
     return run_block(b, x, batch, 1, &flat, 0, nullptr, y, ws, ws_bytes, stream, true, pos_seq, &pages);
 }
 
+namespace {
+// What llama_block_prefill_paged takes of them (0 of either: nothing to do).
+bool prefill_paged_rows_ok(int batch, int tokens) {
+    return batch >= 0 && batch <= 65535 && tokens >= 0 && (long long)batch * tokens <= INT32_MAX / 2;
+}
+}  // namespace
+
 extern "C" size_t llama_block_prefill_paged_workspace_bytes(llama_block b, int batch, int tokens) {
-    if (!b || batch <= 0 || tokens <= 0 || b->dims.dtype != LLAMA_BF16) return 0;
+    if (!b || batch <= 0 || tokens <= 0 || b->dims.dtype != LLAMA_BF16 || !prefill_paged_rows_ok(batch, tokens)) return 0;
     return layout(b, batch, tokens, nullptr, false, true).total;
 }
 
@@ -651,7 +658,7 @@ extern "C" int llama_block_prefill_paged(llama_block b, const void* x, int batch
     if (!b) return LLAMA_ERR_INVALID_ARG;
     if (batch < 0 || batch > 65535 || tokens < 0) return fail(b, LLAMA_ERR_INVALID_ARG, "batch or tokens out of range");
     const auto& d = b->dims;
-    if (d.dtype != LLAMA_BF16 || (long long)batch * tokens > INT32_MAX / 2)
+    if (d.dtype != LLAMA_BF16 || !prefill_paged_rows_ok(batch, tokens))
         return fail(b, LLAMA_ERR_UNSUPPORTED_DIMS, "paged prefill takes bf16 blocks and fewer than 2^30 rows");
     const int rc = paged_cache_check(kv, d.n_kv_heads, d.head_dim, d.dtype);
     if (rc != LLAMA_OK) return fail(b, rc, "paged cache: null, misaligned or of an unsupported geometry");

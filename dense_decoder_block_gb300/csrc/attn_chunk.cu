@@ -61,7 +61,9 @@ using namespace llama;
 
 extern "C" size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads,
                                                               int head_dim, int max_len) {
-    if (batch <= 0 || tokens <= 0 || max_len <= 0 || !heads_ok(n_heads, n_kv_heads, head_dim)) return 0;
+    if (batch <= 0 || batch > 65535 || tokens <= 0 || (long long)batch * tokens > INT32_MAX || max_len <= 0 ||
+        !heads_ok(n_heads, n_kv_heads, head_dim))
+        return 0;   // as the call refuses
     return attn_chunk_workspace_bytes(head_dim, max_len);
 }
 
