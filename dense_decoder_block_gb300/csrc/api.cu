@@ -147,7 +147,7 @@ Ws layout(const llama_block_s* b, int B, int T, uint8_t* base, bool decode, bool
     if (chunk) {   // k and v before they go to their pages, and the attention's partials
         w.k_raw = take(M * kvd * es);
         w.v_raw = take(M * kvd * es);
-        w.chunk = take(attn_chunk_workspace_bytes(d.head_dim, INT32_MAX));
+        w.chunk = take(attn_chunk_workspace_bytes(d.dtype, B, T, d.n_heads, d.n_kv_heads, d.head_dim, d.max_seq));
     }
     w.total = off;
     return w;

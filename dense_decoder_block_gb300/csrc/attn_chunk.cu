@@ -17,15 +17,29 @@ bool heads_ok(int n_heads, int n_kv_heads, int head_dim) {
            n_heads / n_kv_heads <= 64 && (head_dim == 32 || head_dim == 64 || head_dim == 128);
 }
 
-// two partials (m, l, o) of up to 256 rows for each CTA where tiles may be split
-size_t partial_rows(int max_pos) { return max_pos < kNeverSplit ? 0 : kPartialRows; }
-size_t partial_bytes(int head_dim, int max_pos) { return partial_rows(max_pos) * (head_dim + 2) * sizeof(float); }
+// CTAs among which tiles may be split: ChunkWalk's rule at the most tiles and work of a launch (its fp32 arithmetic is
+// within a thousandth).  All of them where no tile is ever cut: nothing is left in the workspace then.
+int split_ctas(const ChunkDeal& d, int batch, int tokens, int n_kv_heads, int max_pos) {
+    if (max_pos < kNeverSplit) return d.ctas;
+    const double tiles = (double)std::min(batch, d.seqs) * n_kv_heads * ((tokens - 1) / d.tq + 1);
+    const double work = tiles * ((double)max_pos + kTileKeys);
+    const double n = std::min(work / d.min_stretch, d.pieces * std::sqrt(work * tiles / kAttnChunk));
+    return (int)std::min((double)d.ctas, std::max(tiles, 1.001 * n + 1));
+}
+
+// rows of partials (m, l, o): two of a tile's rows for each of these CTAs
+size_t partial_rows(const ChunkDeal& d, int split, int max_pos) {
+    return max_pos < kNeverSplit ? 0 : (size_t)2 * split * d.rows;
+}
 
 }  // namespace
 
 // the partials, and where the CTAs begin
-size_t attn_chunk_workspace_bytes(int head_dim, int max_pos) {
-    return partial_bytes(head_dim, max_pos) + kChunkMaxCtas * (sizeof(int4) + sizeof(int));
+size_t attn_chunk_workspace_bytes(int dtype, int batch, int tokens, int n_heads, int n_kv_heads, int head_dim, int max_pos) {
+    const int n_rep = n_heads / n_kv_heads;
+    const ChunkDeal d = dtype == LLAMA_BF16 ? chunk_deal_tc(n_rep) : chunk_deal_f32(n_rep, head_dim);
+    const int split = split_ctas(d, batch, tokens, n_kv_heads, max_pos);
+    return partial_rows(d, split, max_pos) * (head_dim + 2) * sizeof(float) + kChunkMaxCtas * (sizeof(int4) + sizeof(int));
 }
 
 int attn_chunk_launches(const AttnArgs& a) {
@@ -47,9 +61,17 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, const int* start, const in
     k.count = count;
     k.pages = a.pages;
     k.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)a.head_dim));
+    const int n_rep = a.n_heads / a.n_kv_heads;
+    const ChunkDeal d = a.dtype == LLAMA_BF16 ? chunk_deal_tc(n_rep) : chunk_deal_f32(n_rep, a.head_dim);
+    k.tq = d.tq;
+    k.join_keys = d.join_keys;
+    k.min_stretch = d.min_stretch;
+    k.pieces = d.pieces;
+    k.split_ctas = split_ctas(d, a.batch, a.tokens, a.n_kv_heads, a.max_pos);
+    const size_t rows = partial_rows(d, k.split_ctas, a.max_pos);
     k.partial = (float*)ws;
-    k.part_ml = (float2*)(k.partial + partial_rows(a.max_pos) * a.head_dim);
-    k.cuts = (int4*)((uint8_t*)ws + partial_bytes(a.head_dim, a.max_pos));
+    k.part_ml = (float2*)(k.partial + rows * a.head_dim);
+    k.cuts = (int4*)(k.part_ml + rows);
     k.cut_tokens = (int*)(k.cuts + kChunkMaxCtas);
     k.err = a.err;
     return a.dtype == LLAMA_BF16 ? launch_chunk_tc(k, a.head_dim, s) : launch_chunk_f32(k, a.head_dim, s);
@@ -64,7 +86,10 @@ extern "C" size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tok
     if (batch <= 0 || batch > 65535 || tokens <= 0 || (long long)batch * tokens > INT32_MAX || max_len <= 0 ||
         !heads_ok(n_heads, n_kv_heads, head_dim))
         return 0;   // as the call refuses
-    return attn_chunk_workspace_bytes(head_dim, max_len);
+    // heads of 128 are of either type
+    const size_t f32 = attn_chunk_workspace_bytes(LLAMA_F32, batch, tokens, n_heads, n_kv_heads, head_dim, max_len);
+    if (head_dim != 128) return f32;
+    return std::max(f32, attn_chunk_workspace_bytes(LLAMA_BF16, batch, tokens, n_heads, n_kv_heads, head_dim, max_len));
 }
 
 extern "C" int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_heads, int n_kv_heads,

@@ -20,10 +20,25 @@
 
 namespace llama {
 
-// Sequences and CTAs of a launch; each CTA leaves two partials at most (workspace), of 256 rows and of 64
-constexpr int kTcSeqs = 1024, kTcCtas = 152, kF32Seqs = 256, kF32Ctas = 304;
+// Sequences and CTAs of a launch, and the query rows of a tile
+constexpr int kTcSeqs = 1024, kTcCtas = 152, kTcRows = 256;
+constexpr int kF32Seqs = 256, kF32Ctas = 304, kF32Rows = 64;
 constexpr int kChunkMaxCtas = std::max(kTcCtas, kF32Ctas);
-constexpr int kPartialRows = 2 * std::max(kTcCtas * 256, kF32Ctas * 64);
+
+// How a type's tiles are dealt out.
+struct ChunkDeal {
+    int seqs, ctas, rows;
+    int tq;              // tokens per tile
+    int join_keys;       // work (keys) per CTA that the partials and their joining cost
+    int min_stretch;     // the least work of a CTA (keys) for which tiles are split
+    float pieces;        // ... and the pieces of a tile of c chunks, at most: pieces * sqrt(c)
+};
+inline ChunkDeal chunk_deal_tc(int n_rep) { return {kTcSeqs, kTcCtas, kTcRows, 2 * (kTcRows / 2 / n_rep), 768, 512, 2.f}; }
+// two CTAs an SM where shared memory has room for them (244 tokens behind 34056, 4 / 2 heads of 64: 318 us with one, 276)
+constexpr int f32_ctas_per_sm(int head_dim) { return head_dim <= 64 ? 2 : 1; }
+inline ChunkDeal chunk_deal_f32(int n_rep, int head_dim) {
+    return {kF32Seqs, kF32Ctas / 2 * f32_ctas_per_sm(head_dim), kF32Rows, kF32Rows / n_rep, 64, 256, 4.f};
+}
 
 struct ChunkArgs {
     const void* q;       // [batch, tokens, n_heads, head_dim]
@@ -35,10 +50,9 @@ struct ChunkArgs {
     const int* count;
     PageTable pages;
     float scale_log2;
-    int tq;              // tokens per tile
-    int join_keys;       // work (keys) per CTA that the partials and their joining cost
-    int min_stretch;     // the least work of a CTA (keys) for which tiles are split
-    float pieces;        // ... and the pieces of a tile of c chunks, at most: pieces * sqrt(c)
+    int tq, join_keys, min_stretch;   // see ChunkDeal
+    float pieces;
+    int split_ctas;      // CTAs that stretches go to, at most: the workspace has partials of so many
     float* partial;      // [2 CTAs][halves of a tile][head_dim / 4][rows of a half] float4
     float2* part_ml;     // [2 CTAs][halves][rows]
     int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it ...
@@ -211,7 +225,7 @@ struct ChunkWalk {
         float most;   // (with sqrtf, whose code is longer, the bf16 kernel's 8192 tokens took 374 us, so 356)
         asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(most) : "f"((float)total * (float)tiles * (1.f / kAttnChunk)));
         most *= a.pieces;
-        const int n = min(n_ctas, max(tiles, (int)fminf(work, most)));
+        const int n = min(min(n_ctas, a.split_ctas), max(tiles, (int)fminf(work, most)));
         if (cta >= n || total == 0) return;
         // every CTA has the same `each`, whatever its last bits
         const long long each = (long long)__fdividef((float)total, (float)n);

@@ -16,7 +16,7 @@ namespace llama {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 64, kKeys = 64;
+constexpr int kRows = kF32Rows, kKeys = 64;
 constexpr int kGroupBlocks = 4;   // blocks of a piece from which on idle warps share its keys
 
 template <int DH>
@@ -31,8 +31,7 @@ struct Tile {
     static constexpr int BYTES = OFF_SEQS * 4 + (int)sizeof(ChunkSeqs<kF32Seqs>);
     static constexpr int VPR = DH / 4;                   // vectors per row
     static constexpr int CPT = DH / 16;                  // columns of O per thread
-    // per SM: two where shared memory has room for them (244 tokens behind 34056, 4 / 2 heads of 64: 318 us with one, 276)
-    static constexpr int CTAS = DH <= 64 ? 2 : 1;
+    static constexpr int CTAS = f32_ctas_per_sm(DH);     // per SM
 };
 
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem, bool valid) {
@@ -302,11 +301,7 @@ cudaError_t launch(const ChunkArgs& a, cudaStream_t s) {
         k.start += b0;
         k.count += b0;
         k.pages.table += (size_t)b0 * a.pages.stride;
-        k.tq = kRows / (a.n_heads / a.n_kv_heads);
-        k.join_keys = 64;
-        k.min_stretch = 256;
-        k.pieces = 4.f;
-        const unsigned n_ctas = (unsigned)std::min(device_sm_count() * TL::CTAS, kF32Ctas);
+        const unsigned n_ctas = (unsigned)std::min(device_sm_count() * TL::CTAS, kF32Ctas / 2 * TL::CTAS);
         r = launch_pdl(kern, dim3(n_ctas), dim3(kThreads), Tile<DH>::BYTES, s, k);
         if (r != cudaSuccess) return r;
         if (n_ctas == 1 || a.max_pos < kNeverSplit) continue;

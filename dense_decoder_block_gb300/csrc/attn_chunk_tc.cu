@@ -671,10 +671,6 @@ cudaError_t launch_chunk_tc(const ChunkArgs& a, int head_dim, cudaStream_t s) {
         k.start += b0;
         k.count += b0;
         k.pages.table += (size_t)b0 * a.pages.stride;
-        k.tq = 2 * (128 / n_rep);
-        k.join_keys = 768;
-        k.min_stretch = 512;
-        k.pieces = 2.f;
         if (!make_tmap_q3d(&mq, k.q, a.n_heads, k.batch * a.tokens, n_rep, k.tq / 2)) return cudaErrorInvalidValue;
         // persistent: one CTA per SM at most (work assigned on the device)
         const unsigned n_ctas = (unsigned)std::min(device_sm_count(), kTcCtas);

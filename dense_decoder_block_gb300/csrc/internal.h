@@ -150,7 +150,7 @@ cudaError_t launch_attention_tc_paged(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attention_paged_combine(const AttnArgs& a, cudaStream_t s);
 // Attention of chunks of new tokens over a paged cache (a.pages; a.tokens columns, sequence b's new tokens are
 // count[b] at positions start[b] on, below a.max_pos); ws: attn_chunk_workspace_bytes.
-size_t attn_chunk_workspace_bytes(int head_dim, int max_pos);
+size_t attn_chunk_workspace_bytes(int dtype, int batch, int tokens, int n_heads, int n_kv_heads, int head_dim, int max_pos);
 int attn_chunk_launches(const AttnArgs& a);   // kernels of a call
 cudaError_t launch_attention_chunk(const AttnArgs& a, const int* start, const int* count, void* ws, cudaStream_t s);
 // LLAMA_OK, or why the pages of kv cannot be used with these heads.

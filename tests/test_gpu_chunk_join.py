@@ -77,3 +77,29 @@ def test_values_of_keys_without_weight(shape, held, T):
     k[:, :, 0] = float("-inf")
     kv, table = pages(ddb)
     assert torch.isnan(attend(ddb, q, kv, table, [held], [T], held + T)).all()
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_writes_no_more_than_its_workspace(shape):
+    """Calls with exactly the workspace that they ask for: what lies behind it stays as it was, and so does the result beside a
+    larger one."""
+    ddb = _ddb()
+    dtype, Hq, Hkv, D = SHAPES[shape]
+    for T, held in ((1, 384), (1, 3000), (1, 60000), (5, 700), (40, 2000), (130, 9000), (600, 100)):
+        gen = torch.Generator(device=DEV).manual_seed(T + held)
+        k, v, pages = one_sequence(held + T, Hkv, D, 64, dtype, gen)
+        q = torch.randn(1, T, Hq, D, generator=gen, device=DEV).to(dtype)
+        kv, table = pages(ddb)
+        need = ddb.llama_paged_chunk_attention_workspace_bytes(1, T, Hq, Hkv, D, held + T)
+        room = torch.full((need + (1 << 20),), 0xa5, dtype=torch.uint8, device=DEV)
+        o, err = torch.zeros_like(q), _i32([0])
+        ddb.llama_paged_chunk_attention(q, kv, table, _i32([held]), _i32([T]), held + T, o, room[:need], err_dev=err)
+        assert int(err) == 0 and bool((room[need:] == 0xa5).all())
+        want, mass, reach = ref.chunk_attention(q[0].double(), k.double(), v.double(), held)
+        assert float(((o[0].double() - want).abs() - ref.chunk_tol(want, mass, reach, dtype, D, held + T)).max()) <= 0
+        wide = torch.full_like(q, 7.0)     # a bound far above the positions: more workspace, the same result up to rounding
+        if held > 400:
+            table = torch.cat([table, table.new_zeros(1, 5000)], 1).contiguous()
+            ws = torch.empty(ddb.llama_paged_chunk_attention_workspace_bytes(1, T, Hq, Hkv, D, 1 << 18), dtype=torch.uint8, device=DEV)
+            ddb.llama_paged_chunk_attention(q, kv, table, _i32([held]), _i32([T]), 1 << 18, wide, ws, err_dev=err)
+            assert int(err) == 0 and torch.equal(o, wide)
