@@ -103,3 +103,49 @@ def test_writes_no_more_than_its_workspace(shape):
             ws = torch.empty(ddb.llama_paged_chunk_attention_workspace_bytes(1, T, Hq, Hkv, D, 1 << 18), dtype=torch.uint8, device=DEV)
             ddb.llama_paged_chunk_attention(q, kv, table, _i32([held]), _i32([T]), 1 << 18, wide, ws, err_dev=err)
             assert int(err) == 0 and torch.equal(o, wide)
+
+
+@pytest.mark.parametrize("shape,seqs", [("bf16", 1100), ("bf16-8b", 2100), ("f32-64", 300), ("f32-128", 600)])
+def test_several_launches_that_split(shape, seqs):
+    """More sequences than a launch takes, most of them empty or short, with a long one under few tokens in the first launch and
+    in the last: each launch splits and joins, over the same partials.  Equal calls give equal bits."""
+    ddb = _ddb()
+    dtype, Hq, Hkv, D = SHAPES[shape]
+    T, ps = 6, 64
+    start, count = [0] * seqs, [0] * seqs
+    long = {3: (9000, 4), seqs - 2: (7000, 6)}
+    short = {0: (0, 1), 7: (30, 2), seqs // 2: (300, 6), seqs - 1: (64, 5)}
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    used = {**long, **short}
+    need = {b: ref.ceil_div(s + c, ps) for b, (s, c) in used.items()}
+    n_pages = sum(need.values())
+    perm = torch.randperm(n_pages, generator=gen, device=DEV)
+    pk, pv = (torch.full((n_pages, Hkv, ps, D), float("nan"), dtype=dtype, device=DEV) for _ in range(2))
+    table = torch.full((seqs, max(need.values())), -1, dtype=torch.int32, device=DEV)
+    rows, at = {}, 0
+    for b, (s, c) in used.items():
+        start[b], count[b] = s, c
+        ids = perm[at:at + need[b]]
+        at += need[b]
+        table[b, :need[b]] = ids.to(torch.int32)
+        rows[b] = [torch.randn(Hkv, s + c, D, generator=gen, device=DEV).to(dtype) for _ in range(2)]
+        for p, x in zip((pk, pv), rows[b]):
+            whole = torch.full((Hkv, need[b] * ps, D), float("nan"), dtype=dtype, device=DEV)
+            whole[:, :s + c] = x
+            p[ids] = whole.view(Hkv, need[b], ps, D).transpose(0, 1)
+    q = torch.randn(seqs, T, Hq, D, generator=gen, device=DEV).to(dtype)
+    kv = ddb.PagedCache(pk, pv)
+    o = attend(ddb, q, kv, table, start, count, 9004)
+    for b in range(seqs):
+        if b not in used:
+            continue
+        s, c = used[b]
+        k, v = (x.double() for x in rows[b])
+        want, mass, reach = ref.chunk_attention(q[b, :c].double(), k, v, s)
+        assert float(((o[b, :c].double() - want).abs() - ref.chunk_tol(want, mass, reach, dtype, D, s + c)).max()) <= 0, b
+        assert torch.all(o[b, c:] == 7.0)
+    off = torch.ones(seqs, dtype=torch.bool, device=DEV)
+    off[list(used)] = False
+    assert torch.all(o[off] == 7.0)
+    for _ in range(3):
+        assert torch.equal(o, attend(ddb, q, kv, table, start, count, 9004))
