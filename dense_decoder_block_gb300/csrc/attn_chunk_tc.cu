@@ -60,6 +60,40 @@ constexpr int TM_S = 0, TM_O = 256;           // + 128 per stream
 constexpr int kRing = 4;
 static_assert(sizeof(ChunkPiece) == 40, "ring entries");
 
+// MMAs issued by a whole converged warp, one elected lane executing them.  With values that are
+// uniform over the warp the compiler keeps descriptors in uniform registers, and an MMA costs the warp a few issue
+// slots; from a branch that one lane takes it costs dozens, and a busy scheduler then holds the tensor cores back (S and PV of
+// a 128-key chunk beside two warps of multiply-adds on the scheduler: 1025 cycles this way, 2080 the other).
+__device__ __forceinline__ void umma_ss_warp(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_ts_warp(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void umma_commit_warp(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(ptx::smem_u32(bar))
+        : "memory");
+}
+
+// A page's rows, from row group `group` on (see make_tmap_pages), through the default policy: several tiles read them.
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int group) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4}], [%2];" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(group)
+        : "memory");
+}
+
 // A barrier of n threads that tells whether `ok` holds for all of them.
 __device__ __forceinline__ bool named_bar_and(int id, int n, bool ok) {
     uint32_t r;

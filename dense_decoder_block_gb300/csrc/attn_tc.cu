@@ -55,6 +55,9 @@ struct TcArgs {
     int* err;
 };
 
+// Byte offset of the 16-byte chunk `c16` (0..7) of row `r` in a 128-byte-swizzled sub-tile.
+__device__ __forceinline__ uint32_t sw_off(int r, int c16) { return (uint32_t)(r * 128 + ((c16 ^ (r & 7)) << 4)); }
+
 // The softmax of one query row over one 128-key chunk.  Every kernel computes
 // exactly this (prefill with one thread per row, decode with four lanes per row):
 //   m   = c * max_{j <= jmax} S_j,  c = log2(e) / sqrt(d_h)   (keys 0..jmax visible;
@@ -101,6 +104,72 @@ __device__ __forceinline__ float quarter_max_raw(const float* sv, int j0, int jm
     return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
 }
 
+
+// Eight K = 16 steps of one accumulator chain from a single asm block.  Step ks's
+// descriptors are step 0's plus the step's byte offset / 16 in the start-address
+// field (shared-memory addresses stay below 256 KB, so the 14-bit field never
+// carries: the same descriptors the per-step helpers build), the accumulate
+// predicate off for step 0 and on after.  The issuing thread shares its scheduler
+// with softmax and fold warps; this keeps its instructions per MMA few.
+//
+// Both operands from shared memory.  A is K-major in two 64-column sub-tiles
+// A_SUB16 x 16 bytes apart (step ks at (ks / 4) sub-tiles + (ks % 4) * 32 bytes);
+// B likewise with B_SUB16, or MN-major (B_MN: step ks 16 rows on, B_SUB16 x 16 bytes).
+template <int A_SUB16, int B_SUB16, bool B_MN>
+__device__ __forceinline__ void umma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#define LLAMA_AOFF(ks) ((ks) / 4 * A_SUB16 + (ks) % 4 * 2)
+#define LLAMA_BOFF(ks) (B_MN ? (ks) * B_SUB16 : (ks) / 4 * B_SUB16 + (ks) % 4 * 2)
+    asm volatile(
+        "{\n\t.reg .pred pf, pt;\n\t.reg .b64 a<8>, b<8>;\n\t"
+        "setp.ne.b32 pf, %3, %3;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
+        "add.s64 a1, %1, %4;\n\tadd.s64 b1, %2, %11;\n\t"
+        "add.s64 a2, %1, %5;\n\tadd.s64 b2, %2, %12;\n\t"
+        "add.s64 a3, %1, %6;\n\tadd.s64 b3, %2, %13;\n\t"
+        "add.s64 a4, %1, %7;\n\tadd.s64 b4, %2, %14;\n\t"
+        "add.s64 a5, %1, %8;\n\tadd.s64 b5, %2, %15;\n\t"
+        "add.s64 a6, %1, %9;\n\tadd.s64 b6, %2, %16;\n\t"
+        "add.s64 a7, %1, %10;\n\tadd.s64 b7, %2, %17;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, pf;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, pt;\n\t"
+        "}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "n"(LLAMA_AOFF(1)), "n"(LLAMA_AOFF(2)), "n"(LLAMA_AOFF(3)), "n"(LLAMA_AOFF(4)), "n"(LLAMA_AOFF(5)),
+        "n"(LLAMA_AOFF(6)), "n"(LLAMA_AOFF(7)), "n"(LLAMA_BOFF(1)), "n"(LLAMA_BOFF(2)), "n"(LLAMA_BOFF(3)),
+        "n"(LLAMA_BOFF(4)), "n"(LLAMA_BOFF(5)), "n"(LLAMA_BOFF(6)), "n"(LLAMA_BOFF(7))
+        : "memory");
+#undef LLAMA_AOFF
+#undef LLAMA_BOFF
+}
+// A from tensor memory (step ks 8 columns on: 16 bf16 per row), B MN-major from
+// shared memory (step ks 16 rows = 2048 bytes on).
+__device__ __forceinline__ void umma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred pf, pt;\n\t.reg .b32 t<8>;\n\t.reg .b64 b<8>;\n\t"
+        "setp.ne.b32 pf, %3, %3;\n\tsetp.eq.b32 pt, %3, %3;\n\t"
+        "add.u32 t1, %1, 8;\n\tadd.s64 b1, %2, 128;\n\t"
+        "add.u32 t2, %1, 16;\n\tadd.s64 b2, %2, 256;\n\t"
+        "add.u32 t3, %1, 24;\n\tadd.s64 b3, %2, 384;\n\t"
+        "add.u32 t4, %1, 32;\n\tadd.s64 b4, %2, 512;\n\t"
+        "add.u32 t5, %1, 40;\n\tadd.s64 b5, %2, 640;\n\t"
+        "add.u32 t6, %1, 48;\n\tadd.s64 b6, %2, 768;\n\t"
+        "add.u32 t7, %1, 56;\n\tadd.s64 b7, %2, 896;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, pf;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t1], b1, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t2], b2, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t3], b3, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t4], b4, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t5], b5, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t6], b6, %3, pt;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [t7], b7, %3, pt;\n\t"
+        "}"
+        ::"r"(d), "r"(a_tmem), "l"(b), "r"(idesc)
+        : "memory");
+}
 
 // Thread-per-row form (prefill): this thread's S row is at s_taddr in TMEM.
 __device__ __forceinline__ void softmax_row(uint32_t s_taddr, int jmax, float scale_log2, uint8_t* p_base,
@@ -372,7 +441,92 @@ constexpr int PF_SMEM_BYTES = PF_OFF_XCH + 2048 + 1024;
 // of the next chunk has finished.
 constexpr int kPfSBufs = 3;
 constexpr int PF_TM_S = 0, PF_TM_OC = 384;
+// In S[parity], the softmax leaves P (bf16 pairs) in columns 0..63 and the row's
+// (m, l) in columns 64, 65.
+constexpr int PF_TM_ML = 64;
 static_assert(PF_SMEM_BYTES <= 232448, "shared memory per CTA");
+
+// Prefill softmax of one query row over one 128-key chunk, the keys split over
+// two threads (two warps of the same TMEM lane quarter): half h holds keys
+// 64h .. 64h+63 of the row's S in registers.  It computes exactly the canonical
+// softmax: the row max over the visible keys is the max of the two halves' maxima
+// (exchanged through shared memory; max is exact), p = bf16(2^(s c - m)) with
+// hidden keys at -inf, and l = ((L0 + L1) + L2) + L3 with each quarter sum in
+// ascending key order -- half 0 holds L0, L1, half 1 passes L2, L3 over.  Block c
+// (keys 16c .. 16c+15) of P, packed as bf16 pairs, goes to columns 8c .. 8c+7 of
+// the S row once both halves hold their scores in registers; half 0 writes the
+// row's (m, l) to the ML columns.  `xch` is 4 x 128 floats of shared memory; `bar`
+// the barrier id of this lane quarter.
+__device__ __forceinline__ void softmax_half_tmem(uint32_t s_taddr, int h, int row, int jmax, float scale_log2,
+                                                  float* xch, int bar, float& m_out) {
+    float v[64];
+    ptx::tmem_ld<32>(s_taddr + h * 64, v);
+    ptx::tmem_ld<32>(s_taddr + h * 64 + 32, v + 32);
+    ptx::tmem_wait_ld();
+    const int jl = jmax - h * 64;   // last visible key of this half, local index
+    const bool full = __all_sync(0xffffffffu, jl >= 63);
+    float mx;
+    if (full) {
+        float a0 = v[0], a1 = v[1];
+#pragma unroll
+        for (int j = 2; j < 64; j += 4) {
+            a0 = max3(a0, v[j], v[j + 1]);
+            a1 = max3(a1, v[j + 2], v[j + 3]);
+        }
+        mx = fmaxf(a0, a1);
+    } else {
+        float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            if (j <= jl) a[j & 3] = fmaxf(a[j & 3], v[j]);
+        mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+    }
+    xch[h * 128 + row] = mx;
+    ptx::named_bar_sync(bar, 64);   // both halves' maxima written, both S halves read
+    const float m = __fmul_rn(fmaxf(xch[row], xch[128 + row]), scale_log2);
+    const float m_use = (jmax >= 0) ? m : 0.f;   // a row with no visible key: every p is 0
+    if (!full) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            if (j > jl) v[j] = -INFINITY;
+    }
+    // The two quarter sums of this half (blocks 0, 1: quarter 2h; blocks 2, 3:
+    // quarter 2h + 1) advance side by side, each in ascending key order, each
+    // rounded p added straight from its bf16 half.
+    const uint64_t c2 = pack2(scale_log2, scale_log2), nm2 = pack2(-m_use, -m_use);
+    float lq[2] = {0.f, 0.f};
+#pragma unroll
+    for (int cp = 0; cp < 2; ++cp) {   // blocks cp (keys 64h + 16cp ..) and cp + 2
+        const float* va = v + cp * 16;
+        const float* vb = v + (cp + 2) * 16;
+        uint32_t pa[8], pb[8];
+#pragma unroll
+        for (int t = 0; t < 16; t += 2) {
+            float xa0, xa1, xb0, xb1;
+            unpack2(fma2(pack2(va[t], va[t + 1]), c2, nm2), xa0, xa1);
+            unpack2(fma2(pack2(vb[t], vb[t + 1]), c2, nm2), xb0, xb1);
+            const __nv_bfloat162 ba = __floats2bfloat162_rn(ex2(xa0), ex2(xa1));
+            const __nv_bfloat162 bb = __floats2bfloat162_rn(ex2(xb0), ex2(xb1));
+            pa[t >> 1] = *reinterpret_cast<const uint32_t*>(&ba);
+            pb[t >> 1] = *reinterpret_cast<const uint32_t*>(&bb);
+            lq[0] = add_bf16_hi(pa[t >> 1], add_bf16_lo(pa[t >> 1], lq[0]));
+            lq[1] = add_bf16_hi(pb[t >> 1], add_bf16_lo(pb[t >> 1], lq[1]));
+        }
+        tmem_st8(s_taddr + (h * 4 + cp) * 8, pa);
+        tmem_st8(s_taddr + (h * 4 + cp + 2) * 8, pb);
+    }
+    if (h == 1) {
+        xch[256 + row] = lq[0];
+        xch[384 + row] = lq[1];
+    }
+    ptx::named_bar_sync(bar, 64);   // L2, L3 written; the maxima read
+    if (h == 0) {
+        const float l = __fadd_rn(__fadd_rn(__fadd_rn(lq[0], lq[1]), xch[256 + row]), xch[384 + row]);
+        ptx::tmem_st2(s_taddr + PF_TM_ML, m, l);
+    }
+    ptx::tmem_wait_st();
+    m_out = m;
+}
 
 // The tiles of a launch: tile L is KV group bg = L % n_bg (sequence bg / n_kv_heads,
 // KV head bg % n_kv_heads) and query tile y = L / n_bg counted from the last, so
@@ -565,7 +719,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
                     ptx::tc_fence_after();
                     const uint32_t v_addr = ptx::smem_u32(sm + PF_OFF_V + k * 2 * kSub);
                     // P of keys 16ks.. in TMEM columns 8ks.., V rows 16ks..
-                    umma8_ts<128>(tmem + PF_TM_OC, tmem + PF_TM_S + sb * 128, ptx::sw128_mnmajor_desc(v_addr, kSub), IDESC_PV);
+                    umma8_ts(tmem + PF_TM_OC, tmem + PF_TM_S + sb * 128, ptx::sw128_mnmajor_desc(v_addr, kSub), IDESC_PV);
                     ptx::umma_commit(oc_full);
                     ptx::umma_commit(&v_empty[k]);
                     if (gi + kPfSBufs < n_total) ok = issue_s(gi + kPfSBufs);
@@ -735,6 +889,15 @@ __device__ __forceinline__ void tma_load_chunk(void* dst, const CUtensorMap* map
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
         " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(ptx::smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(row), "r"(0), "l"(policy)
+        : "memory");
+}
+
+// A page's rows, from row group `group` on (see make_tmap_pages).
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int group, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%3, %3, %3, %4}], [%2], %5;" ::"r"(ptx::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(ptx::smem_u32(bar)), "r"(0), "r"(group), "l"(policy)
         : "memory");
 }
 
