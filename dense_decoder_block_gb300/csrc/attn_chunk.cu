@@ -18,7 +18,8 @@ bool heads_ok(int n_heads, int n_kv_heads, int head_dim) {
 }
 
 // CTAs among which tiles may be split: ChunkWalk's rule at the most tiles and work of a launch (its fp32 arithmetic is
-// within a thousandth).  All of them where no tile is ever cut: nothing is left in the workspace then.
+// within a thousandth); whole tiles go to no more.  All of them where no tile is ever cut: nothing is left in the workspace
+// then.
 int split_ctas(const ChunkDeal& d, int batch, int tokens, int n_kv_heads, int max_pos) {
     if (max_pos < kNeverSplit) return d.ctas;
     const double tiles = (double)std::min(batch, d.seqs) * n_kv_heads * ((tokens - 1) / d.tq + 1);
@@ -31,15 +32,20 @@ int split_ctas(const ChunkDeal& d, int batch, int tokens, int n_kv_heads, int ma
 size_t partial_rows(const ChunkDeal& d, int split, int max_pos) {
     return max_pos < kNeverSplit ? 0 : (size_t)2 * split * d.rows;
 }
+// rows of O carried over: a tile's for each of them
+size_t carry_rows(const ChunkDeal& d, int split, int max_pos) {
+    return max_pos <= d.carry_keys ? 0 : (size_t)split * d.rows;
+}
 
 }  // namespace
 
-// the partials, and where the CTAs begin
+// the partials, what is carried over, and where the CTAs begin
 size_t attn_chunk_workspace_bytes(int dtype, int batch, int tokens, int n_heads, int n_kv_heads, int head_dim, int max_pos) {
     const int n_rep = n_heads / n_kv_heads;
     const ChunkDeal d = dtype == LLAMA_BF16 ? chunk_deal_tc(n_rep) : chunk_deal_f32(n_rep, head_dim);
     const int split = split_ctas(d, batch, tokens, n_kv_heads, max_pos);
-    return partial_rows(d, split, max_pos) * (head_dim + 2) * sizeof(float) + kChunkMaxCtas * (sizeof(int4) + sizeof(int));
+    return (partial_rows(d, split, max_pos) * (head_dim + 2) + carry_rows(d, split, max_pos) * head_dim) * sizeof(float) +
+           kChunkMaxCtas * (sizeof(int4) + sizeof(int));
 }
 
 int attn_chunk_launches(const AttnArgs& a) {
@@ -71,7 +77,8 @@ cudaError_t launch_attention_chunk(const AttnArgs& a, const int* start, const in
     const size_t rows = partial_rows(d, k.split_ctas, a.max_pos);
     k.partial = (float*)ws;
     k.part_ml = (float2*)(k.partial + rows * a.head_dim);
-    k.cuts = (int4*)(k.part_ml + rows);
+    k.carry = (float*)(k.part_ml + rows);
+    k.cuts = (int4*)(k.carry + carry_rows(d, k.split_ctas, a.max_pos) * a.head_dim);
     k.cut_tokens = (int*)(k.cuts + kChunkMaxCtas);
     k.err = a.err;
     return a.dtype == LLAMA_BF16 ? launch_chunk_tc(k, a.head_dim, s) : launch_chunk_f32(k, a.head_dim, s);

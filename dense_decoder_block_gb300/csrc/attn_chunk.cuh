@@ -22,22 +22,29 @@ namespace llama {
 
 // Sequences and CTAs of a launch, and the query rows of a tile
 constexpr int kTcSeqs = 1024, kTcCtas = 152, kTcRows = 256;
-constexpr int kF32Seqs = 256, kF32Ctas = 304, kF32Rows = 64;
+constexpr int kF32Seqs = 256, kF32Ctas = 304, kF32Rows = 64, kF32Keys = 64;
 constexpr int kChunkMaxCtas = std::max(kTcCtas, kF32Ctas);
+
+// A sum that goes on over millions of keys loses a little with each: O in tensor memory, whose additions are cut off, came out
+// 0.6 % small over 2^20 positions and 10 % over 2^24; products added up one by one in fp32 were off by up to 1 % over 2^20.
+// So a row's O and l are carried over to second sums, O in fp32 in the workspace, every kTcCarry chunks of a piece (2^-11 at
+// most lost in each) and every kF32Carry blocks of kF32Keys keys.
+constexpr int kTcCarry = 512, kF32Carry = 32;
 
 // How a type's tiles are dealt out.
 struct ChunkDeal {
     int seqs, ctas, rows;
+    int carry_keys;      // a row's sums over so many keys are carried over (see ChunkArgs::carry)
     int tq;              // tokens per tile
     int join_keys;       // work (keys) per CTA that the partials and their joining cost
     int min_stretch;     // the least work of a CTA (keys) for which tiles are split
     float pieces;        // ... and the pieces of a tile of c chunks, at most: pieces * sqrt(c)
 };
-inline ChunkDeal chunk_deal_tc(int n_rep) { return {kTcSeqs, kTcCtas, kTcRows, 2 * (kTcRows / 2 / n_rep), 768, 512, 2.f}; }
+inline ChunkDeal chunk_deal_tc(int n_rep) { return {kTcSeqs, kTcCtas, kTcRows, kTcCarry * kAttnChunk, 2 * (kTcRows / 2 / n_rep), 768, 512, 2.f}; }
 // two CTAs an SM where shared memory has room for them (244 tokens behind 34056, 4 / 2 heads of 64: 318 us with one, 276)
 constexpr int f32_ctas_per_sm(int head_dim) { return head_dim <= 64 ? 2 : 1; }
 inline ChunkDeal chunk_deal_f32(int n_rep, int head_dim) {
-    return {kF32Seqs, kF32Ctas / 2 * f32_ctas_per_sm(head_dim), kF32Rows, kF32Rows / n_rep, 64, 256, 4.f};
+    return {kF32Seqs, kF32Ctas / 2 * f32_ctas_per_sm(head_dim), kF32Rows, kF32Carry * kF32Keys, kF32Rows / n_rep, 64, 256, 4.f};
 }
 
 struct ChunkArgs {
@@ -55,6 +62,7 @@ struct ChunkArgs {
     int split_ctas;      // CTAs that stretches go to, at most: the workspace has partials of so many
     float* partial;      // [2 CTAs][halves of a tile][head_dim / 4][rows of a half] float4
     float2* part_ml;     // [2 CTAs][halves][rows]
+    float* carry;        // [CTAs][halves][head_dim / 4][rows of a half] float4: O as carried over
     int4* cuts;          // [CTAs]: the tile that a CTA's stretch begins in {b, g, tile} and its first chunk of it ...
     int* cut_tokens;     // ... and the tile's tokens
     int* err;
@@ -151,6 +159,7 @@ struct ChunkPiece {
     int pos0;         // position of t0
     int kv_last;      // position of t1 - 1
     int c0, c1, n;    // of n chunks
+    int from, to;     // the piece that they are a part of (k_attn_chunk)
 };
 
 // The last x of 0 .. n - 1 for which pred holds; it holds for 0, and for none behind one that it does not hold for.

@@ -4,8 +4,8 @@
 // (cp.async, 16 bytes a thread) under the arithmetic of this one.  256 threads: thread (y, x) of 16 x 16 holds rows 4y ..
 // 4y + 3 and keys x, x + 16, x + 32, x + 48 of a block's scores, and columns of O: 8 scalar products' multiply-adds for
 // each 16-byte read of shared memory.  A row's maximum and sum run over its 16 threads by shuffles; O is scaled where the
-// maximum moves.  Bound by the multiply-adds and the reads that feed them; tiles are split over the CTAs and joined as
-// attn_chunk.cuh says, since a chunk of a tile takes microseconds.  2048 tokens of 8 / 2 heads of 128: 276 us (31 TFLOP/s);
+// maximum moves, and every kF32Carry blocks O and l are added to second sums (attn_chunk.cuh).  Bound by the multiply-adds and the reads that feed them; tiles are split over the CTAs and joined as
+// attn_chunk.cuh says, since a chunk of a tile takes microseconds.  2048 tokens of 8 / 2 heads of 128: 278 us (31 TFLOP/s);
 // 8 x 64 behind 2000, 8 / 2 heads of 64: 100; 2 x 16 behind 4: 11 in a graph, round trips.
 #include <algorithm>
 
@@ -16,7 +16,7 @@ namespace llama {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = kF32Rows, kKeys = 64;
+constexpr int kRows = kF32Rows, kKeys = kF32Keys;
 constexpr int kGroupBlocks = 4;   // blocks of a piece from which on idle warps share its keys
 
 template <int DH>
@@ -27,7 +27,8 @@ struct Tile {
     static constexpr int OFF_V = OFF_K + 2 * kKeys * LD;
     static constexpr int OFF_P = OFF_V + 2 * kKeys * DH;
     static constexpr int OFF_IDS = OFF_P + kRows * LDP;  // [block % 4][4]: its pages, 16 rows each at least
-    static constexpr int OFF_SEQS = OFF_IDS + 16;
+    static constexpr int OFF_CARRY = OFF_IDS + 16;       // [row] (m, l) of what was carried over
+    static constexpr int OFF_SEQS = OFF_CARRY + 2 * kRows;
     static constexpr int BYTES = OFF_SEQS * 4 + (int)sizeof(ChunkSeqs<kF32Seqs>);
     static constexpr int VPR = DH / 4;                   // vectors per row
     static constexpr int CPT = DH / 16;                  // columns of O per thread
@@ -128,6 +129,34 @@ __global__ void __launch_bounds__(kThreads, Tile<DH>::CTAS) k_attn_chunk_f32(con
 #pragma unroll
             for (int e = 0; e < CPT; ++e) o[i][e] = 0.f;
         }
+        // O and l to the sums in the workspace and in shared memory (relative to each row's maximum then), the same threads'
+        // every time; they begin anew.  Rows of group g at kRows / groups * g.
+        const int carry_row = kRows / groups * group + 4 * y;
+        float* carry = a.carry + (size_t)blockIdx.x * (kRows * DH) + carry_row * DH + x * CPT;
+        float2* carried = reinterpret_cast<float2*>(sm + TL::OFF_CARRY) + carry_row;
+        auto carry_over = [&](bool first) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 before = carried[i];
+                const float w = before.x == -INFINITY ? 0.f : exp2f(before.x - m[i]);
+                if (!first) l[i] = __fmaf_rn(before.y, w, l[i]);
+#pragma unroll
+                for (int e = 0; e < CPT; e += 2) {
+                    float2* to = reinterpret_cast<float2*>(carry + i * DH + e);
+                    float2 sum = make_float2(o[i][e], o[i][e + 1]);
+                    if (!first) {
+                        const float2 z = __ldcg(to);
+                        sum = make_float2(__fmaf_rn(z.x, w, sum.x), __fmaf_rn(z.y, w, sum.y));
+                    }
+                    __stcg(to, sum);
+                    o[i][e] = o[i][e + 1] = 0.f;
+                }
+                __syncwarp();
+                if (x == 0) carried[i] = make_float2(m[i], l[i]);
+                l[i] = 0.f;
+            }
+            __syncwarp();
+        };
         for (int i0 = 0; i0 < blocks; ++i0) {
             if (i0 + 1 < blocks) {
                 copy(i0 + 1);
@@ -136,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, Tile<DH>::CTAS) k_attn_chunk_f32(con
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
             __syncthreads();
+            if (i0 > 0 && i0 % kF32Carry == 0 && live) carry_over(i0 == kF32Carry);
             const float* ks = sm + TL::OFF_K + (i0 & 1) * kKeys * TL::LD;
             const float* vs = sm + TL::OFF_V + (i0 & 1) * kKeys * DH;
             const int key0 = p.c0 * kAttnChunk + i0 * kKeys;
@@ -222,6 +252,16 @@ __global__ void __launch_bounds__(kThreads, Tile<DH>::CTAS) k_attn_chunk_f32(con
             else if (groups == 2) block(std::integral_constant<int, 2>{});
             else block(std::integral_constant<int, 1>{});
             __syncthreads();   // the buffer may be filled again
+        }
+        if (blocks > kF32Carry && live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 before = carried[i];
+                const float w = before.x == -INFINITY ? 0.f : exp2f(before.x - m[i]);
+                l[i] = __fmaf_rn(before.y, w, l[i]);
+#pragma unroll
+                for (int e = 0; e < CPT; ++e) o[i][e] = __fmaf_rn(__ldcg(carry + i * DH + e), w, o[i][e]);
+            }
         }
         if (groups > 1) {
             // [group][row] m, l and o, over K's buffers (as many values as one holds): group 0 joins

@@ -23,6 +23,10 @@
 // O, such values of a tile's newest positions are taken out of the chunk's V and added to the rows that do see
 // them at the end (an infinity or NaN in O either way).
 //
+// A piece of more than kTcCarry chunks goes through the pipeline in parts, each a softmax of its own: the output warps leave a
+// part's O in the workspace and its (m, l) in shared memory, and take them into O of the next (attn_chunk.cuh says why;
+// a carry within the softmax's loop cost every step 2 to 3 %; so: 9728 tokens of 4 / 1 heads behind 262144 3.00 -> 3.08 ms).
+//
 // Bound, over long rows, by the tensor pipe and what of a stream's softmax the other stream's MMAs do not cover: a chunk's
 // four MMAs take 1.06 us, the step 1.45 (the pipe is 73 % active; the softmax issues in 41 % of the slots, at half the
 // rate of ex2).  A tile costs 4 us beside its steps: the first copies, the first softmax, the output; a call 5 before its
@@ -49,7 +53,8 @@ constexpr int OFF_V = OFF_K + 4 * kSub;       // [stage] V
 constexpr int OFF_BAR = OFF_V + 4 * kSub;
 constexpr int OFF_PIECES = OFF_BAR + 512;     // the ring of pieces, and a word for each
 constexpr int OFF_ML = OFF_PIECES + 256;      // [parity][stream][128] (m, l): see ml_full
-constexpr int OFF_SEQS = OFF_ML + 4096;
+constexpr int OFF_CARRY = OFF_ML + 4096;      // [half][128] (m, l) of the parts before
+constexpr int OFF_SEQS = OFF_CARRY + 2048;
 using Seqs = ChunkSeqs<kTcSeqs>;                 // of a launch
 constexpr int SMEM_BYTES = OFF_SEQS + (int)sizeof(Seqs) + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
@@ -58,7 +63,7 @@ constexpr int TM_S = 0, TM_O = 256;           // + 128 per stream
 // A CTA's pieces as its roles read them: warp 2 walks the CTA's share a few pieces ahead and leaves them in a ring
 // (a walk in every role took registers that the softmax does not have).
 constexpr int kRing = 4;
-static_assert(sizeof(ChunkPiece) == 40, "ring entries");
+static_assert(kRing * (sizeof(ChunkPiece) + sizeof(int)) <= 256, "ring entries");
 
 // MMAs issued by a whole converged warp, one elected lane executing them.  With values that are
 // uniform over the warp the compiler keeps descriptors in uniform registers, and an MMA costs the warp a few issue
@@ -137,6 +142,26 @@ __device__ __forceinline__ int steps_of(const ChunkPiece& p, int tqh) { return (
 __device__ __forceinline__ int steps_of_stream(const ChunkPiece& p, int tqh, int s) {
     const int n = p.c1 - p.c0;
     return is_pair(p, tqh) ? n : (n + 1 - s) >> 1;
+}
+// O of a row (its 128 columns in tensor memory, (m, l) = x) takes in what the parts before left at `carry`, (m, l) = y;
+// returns (m, l) of both.  A side without a key above -inf has no weight, and 0 times its NaN is NaN.  The whole warp, two
+// columns at a time: rarely called, and longer code slows all other tiles (sixteen: 8192 tokens 359 us, so 369).
+__device__ __forceinline__ float2 take_in(uint32_t o_taddr, const float2& x, const float* carry, const float2& y) {
+    const float m = fmaxf(x.x, y.x);
+    const float wx = x.x == -INFINITY ? 0.f : ex2(x.x - m), wy = y.x == -INFINITY ? 0.f : ex2(y.x - m);
+    auto load = [&](int cb) { return __ldcg(reinterpret_cast<const float2*>(carry + (cb >> 2) * 512 + (cb & 2))); };
+    float2 next = load(0);
+#pragma unroll 1
+    for (int cb = 0; cb < 128; cb += 2) {
+        float o[2];
+        ptx::tmem_ld<2>(o_taddr + cb, o);
+        const float2 before = next;
+        next = load(min(cb + 2, 126));
+        ptx::tmem_wait_ld();
+        ptx::tmem_st2(o_taddr + cb, __fmaf_rn(before.x, wy, o[0] * wx), __fmaf_rn(before.y, wy, o[1] * wx));
+    }
+    ptx::tmem_wait_st();
+    return make_float2(m, __fmaf_rn(y.y, wy, x.y * wx));
 }
 // The first chunk with keys behind the tile's first position: from here on V wants care.
 __device__ __forceinline__ int care_from(const ChunkPiece& p) { return max(p.c0, (p.pos0 + 1) / kAttnChunk); }
@@ -232,10 +257,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             ChunkWalk walk(a, seqs, blockIdx.x, gridDim.x);
             walk.begin(a);
             ChunkPiece p;
+            p.c1 = p.to = 0;
             for (int j = 0;; ++j) {
-                const bool more = walk.next(p);
+                bool more = true;
+                if (p.c1 < p.to) {
+                    p.c0 = p.c1;   // the piece's next part
+                } else {
+                    more = walk.next(p);
+                    p.from = p.c0;
+                    p.to = p.c1;
+                }
+                p.c1 = min(p.to, p.c0 + kTcCarry);
                 if (j >= kRing && !__all_sync(0xffffffffu, ptx::mbar_wait(&pc_free[j % kRing], ((j / kRing) & 1) ^ 1, err))) break;
-                if (!more) p.c0 = p.c1 = 0;
+                if (!more) p.c0 = p.c1 = p.to = 0;
                 if (lane == 0) {
                     pieces[j % kRing] = p;
                     ptx::mbar_arrive(&pc_full[j % kRing]);
@@ -541,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t_local = row / n_rep, h_local = row - t_local * n_rep;
         const uint32_t o_taddr = tmem + ((uint32_t)(quarter * 32) << 16) + TM_O;
         const float2* ml = reinterpret_cast<const float2*>(sm + OFF_ML) + row;
+        float2* carried = reinterpret_cast<float2*>(sm + OFF_CARRY) + row;   // of this thread's rows
         bool ok = true;
         int c0 = 0;                        // chunks of the pieces before
         uint32_t took = 0, ml_phase = 0;   // parities of the streams' pieces, of ml_full
@@ -564,8 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // output: the halves one after another, or the two streams of one half joined
             named_bar_and(1, 128, true);   // poison is written
             const bool poisoned = poison[j % kRing] == j + 1;
-            const bool split = p.c1 - p.c0 < p.n;
-            const int slot = 2 * blockIdx.x + (p.c0 == 0);
+            const bool more = p.c1 < p.to;                       // parts behind this one
+            const bool split = more || p.to - p.from < p.n;      // O and (m, l) are left as they are
+            const int slot = 2 * blockIdx.x + (p.from == 0);
 #pragma unroll 1
             for (int half = 0; half < (pair ? 2 : 1); ++half) {
                 // this half's streams: `half`, or 0 and (with two chunks or more) 1
@@ -593,6 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const bool valid = t_local < tokens;
                 float2 x = ml[((took >> half & 1) * 2 + half) * 128];
+                float* carry = a.carry + (size_t)(2 * blockIdx.x + half) * (128 * 128) + row * 4;   // [column / 4][row][4]
+                if (p.c0 > p.from) x = take_in(o_taddr + half * 128, x, carry, carried[half * 128]);
                 float w0 = 1.f, w1 = 0.f;   // weights of the streams
                 if (both) {
                     const float2 y = ml[((took >> 1) * 2 + 1) * 128];
@@ -604,8 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 bf16* dst = static_cast<bf16*>(a.o) + ((size_t)p.b * a.tokens + p.t0 + half * tqh + t_local) * a.n_heads * 128 +
                             (size_t)(p.g * n_rep + h_local) * 128;
-                float* part = a.partial + (size_t)(2 * slot + half) * (128 * 128) + row * 4;   // [column / 4][row][4]
-                if (split) {
+                float* part = more ? carry : a.partial + (size_t)(2 * slot + half) * (128 * 128) + row * 4;
+                if (more) {
+                    carried[half * 128] = x;
+                } else if (split) {
                     if (valid && ok) a.part_ml[(2 * slot + half) * 128 + row] = x;
                 } else {
                     const float inv = __fdividef(1.f, x.y);   // no key above -inf: 0 * infinity

@@ -466,10 +466,12 @@ int llama_block_decode_paged(llama_block blk, const void* x, int batch, const ll
  * row is NaN where no finite softmax exists.  bf16 (head_dim 128): products on the tensor
  * cores, weights rounded to bf16 before their product with V (held in fp32) and summed as
  * rounded, in fp32, so that keys of like values give that value whatever their weights'
- * roundings; fp32 (head_dim 32, 64, 128): fp32 throughout.  At most 64 query heads per KV
- * head, batch * tokens < 2^31, batch <= 65535.  Where there are fewer query rows than the
- * device has room for, the positions of a row are split and joined: the split follows from
- * the call's sizes, starts and counts, so equal calls give equal bits, and a row's last bit
+ * roundings; fp32 (head_dim 32, 64, 128): fp32 throughout.  A row's sums are carried over to
+ * second ones, in fp32, every few thousand keys (bf16: 65536), so that their roundings do not
+ * grow with the cache.  At most 64 query heads per KV head, batch * tokens < 2^31, batch <=
+ * 65535.  Where there are fewer query rows than the device has room for, the positions of a
+ * row are split and joined: the split follows from the call's sizes, starts and counts, so
+ * equal calls give equal bits, and a row's last bit
  * may depend on the other sequences of the call.  workspace:
  * llama_paged_chunk_attention_workspace_bytes (0 for sizes that the call refuses). */
 size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads, int head_dim,

@@ -80,9 +80,12 @@ def test_grows_with_the_call(need):
     """Small calls ask for little, larger ones for no less, and none for more than all CTAs' partials."""
     assert need(1, 1, 1, 1, 128, 384) == 304 * 20
     assert need(1, 1, 1, 1, 128, 385) < 1 << 20 and need(1, 16, 4, 2, 64, 1000) < 1 << 20
-    whole = {128: 2 * 152 * 256 * 130 * 4 + 304 * 20, 64: 2 * 304 * 64 * 66 * 4 + 304 * 20, 32: 2 * 304 * 64 * 34 * 4 + 304 * 20}
-    for dim, top in whole.items():
-        assert need(8, 512, 32, 8, dim, 2560) == top and need(65535, 32768, 64, 8, dim, 2 ** 31 - 1) == top
+    # (CTAs, rows) of the type, and the keys from which on a row's O is carried over, in fp32 a row each
+    for dim, ctas, rows, keys in ((128, 152, 256, 65536), (64, 304, 64, 2048), (32, 304, 64, 2048)):
+        pieces, carried = 2 * ctas * rows * (dim + 2) * 4 + 304 * 20, ctas * rows * dim * 4
+        assert need(8, 512, 32, 8, dim, keys) == pieces and need(8, 512, 32, 8, dim, keys + 1) == pieces + carried
+        top = need(65535, 32768, 64, 8, dim, 2 ** 31 - 1)
+        assert top == pieces + carried
         for heads, kv in ((32, 8), (1, 1), (64, 1), (6, 2)):
             sizes = [need(*args) for args in ((1, 1, heads, kv, dim, 385), (1, 1, heads, kv, dim, 5000), (1, 20, heads, kv, dim, 5000),
                                               (3, 20, heads, kv, dim, 5000), (3, 20, heads, kv, dim, 10 ** 6))]
