@@ -28,11 +28,12 @@
 // a carry within the softmax's loop cost every step 2 to 3 %; so: 9728 tokens of 4 / 1 heads behind 262144 3.00 -> 3.08 ms).
 //
 // Bound, over long rows, by the tensor pipe and what of a stream's softmax the other stream's MMAs do not cover: a chunk's
-// four MMAs take 1.06 us, the step 1.45 (the pipe is 73 % active; the softmax issues in 41 % of the slots, at half the
+// four MMAs take 1.06 us, the step 1.45 (the pipe is 71 % active; the softmax issues in 50 % of the slots, at half the
 // rate of ex2).  A tile costs 4 us beside its steps: the first copies, the first softmax, the output; a call 5 before its
 // first MMA (lengths, the walk, the block table, Q and K: one load behind another).  Whole calls: 8192 tokens of 32 / 8
-// heads 355 us (1.55 PFLOP/s), 4096 of 64 / 8 behind 4096 515 (1.60), 2048 of 32 / 8 38, 32 x 4 behind 1000 35
-// (3.8 TB/s), 100 behind 8192 31, one token at 100 positions 7.
+// heads 354 us on pages of 128 rows (1.55 PFLOP/s), 362 of 64, 385 of 16 (a copy a page); 4096 of 64 / 8 behind 4096 513
+// (1.61) at 2070 MHz, 548 (1.51) once the power limit has taken the clock to 1920; 2048 of 32 / 8 42 to 46, 32 x 4 behind
+// 1000 37.5 (3.5 TB/s), 100 behind 8192 34 (with the join), one token at 100 positions 7.6.
 #include <algorithm>
 
 #include "attn_chunk.cuh"

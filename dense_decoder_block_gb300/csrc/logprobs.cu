@@ -15,10 +15,12 @@
 // it has.  So the alternatives come from n segments read a second time, from L2.
 //
 // Few rows are split over a cluster of CTAs of 16 warps (their triples and segment maxima in distributed shared memory,
-// the first CTA finishes the row).  Many rows (kManyRows per SM or more) take a CTA of 4 warps each, 8 to an SM: one
-// finishes its row while the others read, and no round of large CTAs ends half empty (924 rows of 128256 logits: 137 us
-// with 16 warps a row, 75 so: 6.3 TB/s, 0.95 of the copy rate).  Few rows are bound by a chain of round trips: 1 row with
-// 20 alternatives 9.9 us, 32 rows with 5 11.5.
+// the first CTA finishes the row).  Many rows (kManyRows per SM or more) take a CTA of 4 warps each, 7 to an SM (72
+// registers): one finishes its row while the others read, and no round of large CTAs ends half empty (924 rows of 128256
+// logits: 137 us with 16 warps a row, 75 so: 6.3 TB/s, 0.95 of the copy rate).  Few rows are bound by a chain of round
+// trips: 1 row with 20 alternatives 9.9 us, 32 rows with 5 11.7.  In between, with 5 alternatives: 64 rows 15 us, 128 21,
+// 152 22; from 153 on a row has one CTA of 16 warps, 27 (153) to 32 (304), and from 305 on a second round of them, 43 (305)
+// to 59 (607); 608 in small CTAs 57, 1024 83.  (305 rows are 156 MB, 23 us: the worst place of the rule.)
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -38,7 +40,8 @@ constexpr int kMaxSegs = (1 << 20) / kSeg + 1; // of a row (one more where it st
 constexpr int kMaxCluster = 8;
 // Logits of a short row that are all ranked, each by a look at all others (1024 rows of 500 logits all ranked 50 us, the
 // candidates narrowed 10.5; 1 row of 250: 7.2 and 8.8; 1024 rows of 170: 11.5 and 10.1).  At least 4 * 32 + 3: with more
-// logits no lane of a segment is without one.
+// logits every lane of the row's first segment has one, and 32 lanes with a logit bound 32 alternatives (of the last segment
+// most lanes may have none).
 constexpr int kListedFew = 256, kListedMany = 160;
 
 struct LogprobArgs {

@@ -223,8 +223,10 @@ __global__ void __launch_bounds__(256) k_rope_inplace(bf16* __restrict__ q, bf16
 }
 
 // RoPE of chunks of new tokens, their rows to pages (launch_rope_paged): as above, one thread per 8 elements of
-// kRopeRows rows of a token -- q rows in place, then k rows (rotated) and v rows (copied) into the pages.  Bound by the rows
-// (2048 tokens of 32 / 8 heads: 50 MB in 11.6 us with cold caches).
+// kRopeRows rows of a token -- q rows in place, then k rows (rotated) and v rows (copied) into the pages.  Bound by its chain of
+// loads (start and count, the page and the rotation, the rows) at four CTAs an SM (60 registers, 35 % of the warps
+// there): 2048 tokens of 32 / 8 heads (26 MB read, as much written) 13 us with cold caches, half the cycles waiting for
+// loads and DRAM a quarter busy.  In the block's call the rows come from L2.
 __global__ void __launch_bounds__(256) k_rope_paged(bf16* __restrict__ q, const bf16* __restrict__ k, const bf16* __restrict__ v,
                                                     int M, int T, int n_heads, int n_kv_heads, bf16* __restrict__ pk,
                                                     bf16* __restrict__ pv, const PageTable pages, const int* start,
