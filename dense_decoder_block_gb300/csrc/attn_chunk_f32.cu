@@ -4,9 +4,10 @@
 // (cp.async, 16 bytes a thread) under the arithmetic of this one.  256 threads: thread (y, x) of 16 x 16 holds rows 4y ..
 // 4y + 3 and keys x, x + 16, x + 32, x + 48 of a block's scores, and columns of O: 8 scalar products' multiply-adds for
 // each 16-byte read of shared memory.  A row's maximum and sum run over its 16 threads by shuffles; O is scaled where the
-// maximum moves, and every kF32Carry blocks O and l are added to second sums (attn_chunk.cuh).  Bound by the multiply-adds and the reads that feed them; tiles are split over the CTAs and joined as
-// attn_chunk.cuh says, since a chunk of a tile takes microseconds.  2048 tokens of 8 / 2 heads of 128: 278 us (31 TFLOP/s);
-// 8 x 64 behind 2000, 8 / 2 heads of 64: 100; 2 x 16 behind 4: 11 in a graph, round trips.
+// maximum moves, and every kF32Carry blocks O and l are added to second sums (attn_chunk.cuh).  Bound by the multiply-adds
+// and the reads that feed them; tiles are split over the CTAs and joined as attn_chunk.cuh says, since a chunk of a tile
+// takes microseconds.  2048 tokens of 8 / 2 heads of 128: 278 us (31 TFLOP/s); 8 x 64 behind 2000, 8 / 2 heads of 64: 100;
+// 2 x 16 behind 4: 10 in a graph, round trips.
 #include <algorithm>
 
 #include "attn_chunk.cuh"

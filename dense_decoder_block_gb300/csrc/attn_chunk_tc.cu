@@ -7,7 +7,8 @@
 //                 rounded p (in fp32), so that a weight's rounding goes to O and l alike: where one key outweighs the
 //                 others, or the heavy ones hold one value, the row is that value.
 //                 m follows the row's maximum only when that has grown by more than 2^kSlack, so O is
-//                 seldom scaled (p <= 2^kSlack; nothing is lost, bf16 and fp32 keep their relative precision)
+//                 seldom scaled (p <= 2^kSlack; nothing is lost, bf16 and fp32 keep their relative precision; a published
+//                 technique of attention kernels)
 //   O += P V      tcgen05.mma, P from tensor memory, O accumulated in tensor memory
 // Two streams run side by side so that one's MMAs cover the other's softmax: the halves of a tile, or, when a tile has
 // 128 rows at most (few new tokens), its even and its odd chunks, joined at the end.  A stream's S, P (over S) and O

@@ -471,9 +471,9 @@ int llama_block_decode_paged(llama_block blk, const void* x, int batch, const ll
  * grow with the cache.  At most 64 query heads per KV head, batch * tokens < 2^31, batch <=
  * 65535.  Where there are fewer query rows than the device has room for, the positions of a
  * row are split and joined: the split follows from the call's sizes, starts and counts, so
- * equal calls give equal bits, and a row's last bit
- * may depend on the other sequences of the call.  workspace:
- * llama_paged_chunk_attention_workspace_bytes (0 for sizes that the call refuses). */
+ * equal calls give equal bits, and a row's last bit may depend on the other sequences of the
+ * call.  workspace: llama_paged_chunk_attention_workspace_bytes (0 for sizes that the call
+ * refuses). */
 size_t llama_paged_chunk_attention_workspace_bytes(int batch, int tokens, int n_heads, int n_kv_heads, int head_dim,
                                                    int max_len);
 int llama_paged_chunk_attention(const void* q, int batch, int tokens, int n_heads, int n_kv_heads, int head_dim,

@@ -100,3 +100,34 @@ def test_random_values(dtype, T, Hq, Hkv, D, held):
         # (O, see above) + 3 * 46 + 3 * 304 in O and 600 + 3 * 46 + 3 * 304 in l, fp32 2048 + 3 * 49 + 3 * 304 in each
         tol = chunk_tol(want, mass, reach, dtype, D, 1 << 17 if dtype == BF else 1 << 16)
         assert float(((o[some, h] - want).abs() - tol).max()) <= 0, h
+
+
+def test_infinities_where_a_piece_is_parted():
+    """Whole tiles of 9728 tokens from position 60000 on: one of them ends its first 512 chunks among its own new positions.
+    Infinities and NaN among the values there reach the rows that see them, in their columns alone, and no row before."""
+    ddb = _ddb()
+    T, held, D = 9728, 60000, 128
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    q = torch.randn(1, T, 4, D, generator=gen, device=DEV).to(BF)
+    pk, pv = (torch.randn(3, 1, PS, D, generator=gen, device=DEV).to(BF) for _ in range(2))
+    table = torch.zeros(1, ceil_div(held + T, PS), dtype=torch.int32, device=DEV)
+    table[0, 63], table[0, 64] = 1, 2                    # positions 64512 .. 66559 have pages of their own
+    ws = torch.empty(ddb.llama_paged_chunk_attention_workspace_bytes(1, T, 4, 1, D, held + T), dtype=torch.uint8, device=DEV)
+    outs = []
+    for poison in (False, True):
+        v = pv.clone()
+        if poison:
+            for pos, col, value in ((65510, 5, "inf"), (65540, 17, "nan"), (65550, 5, "-inf"), (65559, 40, "inf")):
+                v[1 + (pos >= 65536), 0, pos % PS, col] = float(value)
+        o, err = torch.full_like(q, 7.0), _i32([0])
+        ddb.llama_paged_chunk_attention(q, ddb.PagedCache(pk, v), table, _i32([held]), _i32([T]), held + T, o, ws, err_dev=err)
+        assert int(err) == 0
+        outs.append(o[0])
+    want, o = outs
+    at = lambda pos: pos - held   # noqa: E731
+    clean = [c for c in range(D) if c not in (5, 17, 40)]
+    assert torch.equal(o[:, :, clean], want[:, :, clean]) and torch.isfinite(want.float()).all()
+    for col, first in ((5, 65510), (17, 65540), (40, 65559)):
+        assert torch.equal(o[:at(first), :, col], want[:at(first), :, col])
+    assert torch.all(o[at(65510):at(65550), :, 5] == float("inf")) and torch.isnan(o[at(65550):, :, 5]).all()
+    assert torch.isnan(o[at(65540):, :, 17]).all() and torch.all(o[at(65559):, :, 40] == float("inf"))
